@@ -187,12 +187,13 @@ def _mixed(h):
 
 
 def _random_bits(shape, seed, device):
-    """One 32-bit number for each value: of the seed, the matrix and the value's place in it."""
+    """16 random bits for each value: of the seed, the matrix and the value's place in it (two places share a 32-bit number)."""
     e, r, c = shape
     place = torch.arange(r * c, device=device, dtype=torch.int64)
     matrix = torch.arange(e, device=device, dtype=torch.int64)
     key = _mixed(_mixed(torch.full_like(matrix, seed & 0xFFFFFFFF)) ^ (matrix & 0xFFFFFFFF))
-    return _mixed((_mixed(place & 0xFFFFFFFF)[None] + key[:, None]) & 0xFFFFFFFF).view(e, r, c)
+    pair = _mixed(((place >> 1)[None] + key[:, None]) & 0xFFFFFFFF)
+    return ((pair >> (16 * (place & 1))) & 0xFFFF).view(e, r, c)
 
 
 def _blocks(x):
@@ -218,13 +219,13 @@ def _write(x, fmt, seed):
     y = torch.where(torch.isfinite(y), y, torch.zeros_like(y))
     u = None if seed is None else _random_bits((e, r, c), seed, x.device)
     if fmt == "int8":
-        q = torch.round(y) if u is None else torch.floor(y + (u >> 8).float() * 2.0 ** -24)
+        q = torch.round(y) if u is None else torch.floor(y + u.float() * 2.0 ** -16)
         return q.clamp(-127, 127).to(torch.int8), scale
     if u is not None:
         size = y.abs()
         bits = size.contiguous().view(torch.int32).to(torch.int64)
-        normal = ((bits + (u >> 12)) & ~0xFFFFF).to(torch.int32).view(torch.float32)
-        small = torch.floor(size * 512 + (u >> 8).float() * 2.0 ** -24) * 2.0 ** -9
+        normal = ((bits + (u << 4)) & ~0xFFFFF).to(torch.int32).view(torch.float32)
+        small = torch.floor(size * 512 + u.float() * 2.0 ** -16) * 2.0 ** -9
         size = torch.where(size >= 2.0 ** -6, normal, small).clamp(max=448.0)
         y = torch.copysign(size, y)
     return y.to(torch.float8_e4m3fn), scale
@@ -313,10 +314,9 @@ def _exact_rounded(x, fmt, bits):
         if u is None:
             q = torch.round(y / spacing) * spacing
         elif fmt == "int8":
-            q = torch.floor(y + (u >> 8).double() / 2 ** 24)
+            q = torch.floor(y + u.double() / 2 ** 16)
         else:
-            share = torch.where(y.abs() >= 2.0 ** -6, (u >> 12).double() / 2 ** 20, (u >> 8).double() / 2 ** 24)
-            q = torch.sign(y) * torch.floor(y.abs() / spacing + share) * spacing
+            q = torch.sign(y) * torch.floor(y.abs() / spacing + u.double() / 2 ** 16) * spacing
         values[:, :, at:at + BLOCK] = q.clamp(-TOP[fmt], TOP[fmt]) * torch.where(live, step, torch.zeros_like(step))
         scales.append(torch.where(live, step, torch.zeros_like(step)))
     return values, torch.cat(scales, 2)
