@@ -74,8 +74,9 @@ typedef enum {
   MUON_ERR_NO_DEVICE = 7       /* no sm_100 device current */
 } muon_status_t;
 
-/* Storage type of W, G, M (and of the X/O buffers of muon_orthogonalize). */
-typedef enum { MUON_BF16 = 0, MUON_FP32 = 1 } muon_dtype_t;
+/* Storage type of W, G, M (and of the X/O buffers of muon_orthogonalize).  MUON_FP16 is a type of
+ * views only (muon_view_t); a handle's own type is bf16 or fp32. */
+typedef enum { MUON_BF16 = 0, MUON_FP32 = 1, MUON_FP16 = 2 } muon_dtype_t;
 
 /* Arithmetic of the Newton-Schulz products.
  * FAST:     bf16 operands on the tcgen05 tensor cores, fp32 accumulation in
@@ -83,8 +84,18 @@ typedef enum { MUON_BF16 = 0, MUON_FP32 = 1 } muon_dtype_t;
  *           (X, A, and B' = a I + b A + c A A, every term of B' taken from the
  *           rounded A).
  * FP32_REF: fp32 operands and intermediates, products accumulated in fp64 on
- *           the CUDA cores (no TF32): a slow, accurate mode for checking. */
-typedef enum { MUON_MODE_FAST = 0, MUON_MODE_FP32_REF = 1 } muon_mode_t;
+ *           the CUDA cores (no TF32): a slow, accurate mode for checking.
+ * HALF:     the products of FAST with fp16 operands: three more significant bits at the
+ *           same tensor-core rate, an error about eight times smaller (2e-3 instead of 1-2e-2
+ *           after five quintic iterations).  X, A and B' are stored times powers of two
+ *           (2^12, 2^12, 2^8), so iterations whose singular values stay below 4 and whose
+ *           polynomials stay below 255 are in range (the usual ones stay below 1.3 and 10);
+ *           beyond that a matrix comes out not finite.  X is normalised before it
+ *           is rounded, so the inputs' size does not matter down to norms of about 1e-4 eps.
+ *           Matrices of at most 128 rows (or columns) and 4096 columns (rows) run every
+ *           iteration on chip.  Takes views, coefficients per iteration and 8-bit
+ *           momentum (below); iterations are launched as MUON_SCHEDULE_STAGED. */
+typedef enum { MUON_MODE_FAST = 0, MUON_MODE_FP32_REF = 1, MUON_MODE_HALF = 2 } muon_mode_t;
 
 typedef struct { int64_t rows, cols; } muon_shape_t;
 
@@ -149,6 +160,98 @@ MUON_API muon_status_t muon_step(muon_handle_t handle, void* const* W, const voi
  */
 MUON_API muon_status_t muon_orthogonalize(muon_handle_t handle, const void* const* X, void* const* O,
                                  const muon_hparams_t* hp, cudaStream_t stream);
+
+/*
+ * `count` equal matrices where and how the caller holds them: element (r, c) of matrix e is at
+ * data[e * batch_stride + r * row_stride + c * col_stride], strides in elements and not
+ * negative, one of row_stride and col_stride 1 (a matrix stored by rows or by columns; the
+ * stride of a dimension of size 1 does not matter).  Slices of fused weights, stacks of heads
+ * and transposed storage are views; so is a contiguous matrix.  Rows that start 16-byte
+ * aligned take vector accesses.
+ */
+typedef struct {
+  void* data;
+  int64_t count, batch_stride, row_stride, col_stride;
+  muon_dtype_t dtype;
+} muon_view_t;
+
+/*
+ * The orthogonaliser on views (MUON_MODE_HALF): O_i = NS_k(X_i) for the matrices of the handle, in
+ * order; view j covers its `count` next matrices, which must have one shape (X and O have n views of
+ * equal counts, adding up to the handle's matrices).  Each view has its own storage type: bf16,
+ * fp16 or fp32.  O may be X itself; otherwise an output overlaps no input and no other output.
+ * Only hp->eps, a, b, c and ns_steps are used; muon_set_coefficients overrides a, b, c.
+ * Returns MUON_ERR_UNSUPPORTED for a handle of another mode and for views that
+ * are stored neither by rows nor by columns.
+ */
+MUON_API muon_status_t muon_orthogonalize_views(muon_handle_t handle, const muon_view_t* X, const muon_view_t* O,
+                                                int n, const muon_hparams_t* hp, cudaStream_t stream);
+
+/*
+ * Coefficients of each Newton-Schulz iteration (MUON_MODE_HALF): abc is a host array of
+ * steps x 3 floats, iteration t (from 0) of later calls on the handle uses
+ * abc[3 t .. 3 t + 2] instead of the hyper-parameters' a, b, c.  A call with more iterations
+ * than that is refused with MUON_ERR_INVALID_ARG.  steps = 0 goes back to the hyper-parameters.
+ */
+MUON_API muon_status_t muon_set_coefficients(muon_handle_t handle, const float* abc, int steps);
+
+/*
+ * 8-bit optimizer state.  `count` matrices of rows x cols, back to back: codes holds one byte a value
+ * (row-major), scales one fp32 for each MUON_STATE_BLOCK columns of a row, [count][rows]
+ * [ceil(cols / MUON_STATE_BLOCK)].  With t the largest magnitude of a block:
+ *   INT8  code = x * (127 / t) rounded to an integer, scale = t / 127
+ *   E4M3  code = x * (448 / t) rounded to e4m3,       scale = t / 448
+ * and code * scale is the value.  E4M3 keeps small values beside large ones (relative steps of
+ * 1/16 to 1/8 over a range of 2^15); INT8 is finer (1/127 of t) where a block's values are
+ * alike.  A block with t < 2^-100 becomes zeros with scale 0; one that holds an infinity or
+ * a NaN gets the scale NaN, so that reading it shows it.  An all-zero state (zero bytes) is zero.
+ *
+ * Rounding is to nearest even where `seed` is NULL.  Otherwise it is stochastic: up with the
+ * probability of the remainder (to 16 bits), by a generator that depends on *seed (read
+ * before returning), the matrix's place in the call and the value's place in the matrix only.
+ * Give every step another seed.  A captured call repeats the seed it was captured with.
+ */
+#define MUON_STATE_BLOCK 128
+typedef enum { MUON_STATE_INT8 = 0, MUON_STATE_E4M3 = 1 } muon_state_format_t;
+typedef struct {
+  void* codes;
+  float* scales;
+  int64_t count, rows, cols;
+} muon_state_t;
+
+/*
+ * Write n states from views (quantise), and read them back into views (dequantise).  View j has the
+ * count and shape of state j and col_stride 1; all views of a call have one type.
+ * No handle and no workspace; enqueued on `stream`, with the tensors' device current.  n == 0 is a
+ * no-op.  Returns MUON_ERR_INVALID_ARG for null pointers, bad sizes, types or formats,
+ * mixed types and overlapping outputs, MUON_ERR_UNSUPPORTED for another col_stride or a matrix of 2^31
+ * blocks or more.
+ */
+MUON_API muon_status_t muon_state_quantize(const muon_view_t* X, const muon_state_t* S, int n,
+                                           muon_state_format_t format, const uint32_t* seed, cudaStream_t stream);
+MUON_API muon_status_t muon_state_dequantize(const muon_state_t* S, const muon_view_t* X, int n,
+                                             muon_state_format_t format, cudaStream_t stream);
+
+/*
+ * Momentum and Nesterov blend on 8-bit state, with the Frobenius norms: the first stage of a step,
+ * for the handle's matrices in order (any mode).  Per matrix, with m read from the state,
+ *   m1 = beta m + (1-beta) g;  u = (1-beta) g + beta m1 if nesterov, else m1
+ * in fp32; u is rounded once into U, m1 once into the state.  G and U are views of the handle's type
+ * with col_stride 1 (U may be G).  Only hp->beta and nesterov are used.  The norms
+ * of u are read with muon_get_norms.
+ */
+MUON_API muon_status_t muon_momentum_state(muon_handle_t handle, const muon_view_t* G, const muon_state_t* S,
+                                           const muon_view_t* U, int n, muon_state_format_t format,
+                                           const muon_hparams_t* hp, const uint32_t* seed, cudaStream_t stream);
+
+/*
+ * The Muon step on 8-bit momentum (MUON_MODE_HALF): muon_step with M held in S.  W and G are views of the
+ * handle's type (G with col_stride 1).  The direction is rounded to the
+ * handle's type once before it is orthogonalised.
+ */
+MUON_API muon_status_t muon_step_state(muon_handle_t handle, const muon_view_t* W, const muon_view_t* G,
+                                       const muon_state_t* S, int n, muon_state_format_t format,
+                                       const muon_hparams_t* hp, const uint32_t* seed, cudaStream_t stream);
 
 /*
  * AdamW for the parameters that are not matrices: the other half of the hybrid
@@ -230,7 +333,7 @@ MUON_API muon_status_t muon_get_plan(muon_handle_t handle, int ns_steps, int* n_
  *                         of STAGED with one launch per step instead of 3 k),
  *                         else STAGED.
  * The small-matrix kernel (MUON_KERNEL_NS_SMALL) keeps precedence when its
- * conditions hold; FP32_REF handles always run staged.  Returns
+ * conditions hold; FP32_REF and HALF handles always run staged.  Returns
  * MUON_ERR_UNSUPPORTED if FUSED is asked of a handle that cannot run it.
  * The setting applies to later calls; it must not change while a captured graph
  * of the handle is replayed.
@@ -288,7 +391,8 @@ MUON_API muon_status_t muon_momentum_norm_static(const void* G, void* M, void* U
  * muon_get_group_buffers gives a group's padded oriented shape (mp x np, both
  * multiples of 256), its matrix count and the device addresses of its buffers
  * inside the workspace: X0 and X1 ([count][mp][np]) and A and B
- * ([count][mp][mp]), elements bf16 in FAST mode and fp32 in FP32_REF mode.
+ * ([count][mp][mp]), elements bf16 in FAST mode, fp32 in FP32_REF mode and fp16 in HALF mode
+ * (there X0 is the normalised X times 2^12, and the addresses of a group that runs on chip are NULL).
  * After muon_orthogonalize/muon_step with k iterations, X0 holds U (oriented,
  * unnormalised), A and B hold the last iteration's Gram and polynomial
  * matrices, and X(k mod 2) the final iterate.  Any output pointer may be NULL.

@@ -12,8 +12,10 @@ import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmuon.so")
 
-MUON_BF16, MUON_FP32 = 0, 1
-MUON_MODE_FAST, MUON_MODE_FP32_REF = 0, 1
+MUON_BF16, MUON_FP32, MUON_FP16 = 0, 1, 2
+MUON_MODE_FAST, MUON_MODE_FP32_REF, MUON_MODE_HALF = 0, 1, 2
+MUON_STATE_INT8, MUON_STATE_E4M3 = 0, 1
+MUON_STATE_BLOCK = 128
 
 STATUS = {
     0: "MUON_OK",
@@ -54,6 +56,16 @@ class HParams(ctypes.Structure):
         ("nesterov", ctypes.c_int32),
         ("ns_steps", ctypes.c_int32),
     ]
+
+
+class View(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_int64), ("batch_stride", ctypes.c_int64),
+                ("row_stride", ctypes.c_int64), ("col_stride", ctypes.c_int64), ("dtype", ctypes.c_int)]
+
+
+class State(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("count", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
 _lib = None
@@ -103,6 +115,20 @@ def lib() -> ctypes.CDLL:
         L.muon_profile_end.restype = st
         L.muon_set_schedule.argtypes = [_VP, ctypes.c_int]
         L.muon_set_schedule.restype = st
+        views, states, hpp = ctypes.POINTER(View), ctypes.POINTER(State), ctypes.POINTER(HParams)
+        seed = ctypes.POINTER(ctypes.c_uint32)
+        L.muon_set_coefficients.argtypes = [_VP, ctypes.POINTER(ctypes.c_float), ctypes.c_int]
+        L.muon_set_coefficients.restype = st
+        L.muon_orthogonalize_views.argtypes = [_VP, views, views, ctypes.c_int, hpp, _VP]
+        L.muon_orthogonalize_views.restype = st
+        L.muon_state_quantize.argtypes = [views, states, ctypes.c_int, ctypes.c_int, seed, _VP]
+        L.muon_state_quantize.restype = st
+        L.muon_state_dequantize.argtypes = [states, views, ctypes.c_int, ctypes.c_int, _VP]
+        L.muon_state_dequantize.restype = st
+        L.muon_momentum_state.argtypes = [_VP, views, states, views, ctypes.c_int, ctypes.c_int, hpp, seed, _VP]
+        L.muon_momentum_state.restype = st
+        L.muon_step_state.argtypes = [_VP, views, views, states, ctypes.c_int, ctypes.c_int, hpp, seed, _VP]
+        L.muon_step_state.restype = st
         _lib = L
     return _lib
 
@@ -236,6 +262,50 @@ def muon_momentum_norm_static(G: int, M: int, U: int, rows: int, cols: int, dtyp
     f.restype = ctypes.c_int
     _check(f(ctypes.c_void_p(G), ctypes.c_void_p(M), ctypes.c_void_p(U), int(rows), int(cols), dtype, float(beta),
              1 if nesterov else 0, ctypes.c_void_p(norm), ctypes.c_void_p(stream)), "muon_momentum_norm_static")
+
+
+def _seed(seed):
+    return None if seed is None else ctypes.byref(ctypes.c_uint32(int(seed) & 0xFFFFFFFF))
+
+
+def views(items):
+    """Array of View from (data, count, batch_stride, row_stride, col_stride, dtype) tuples."""
+    return (View * max(len(items), 1))(*items)
+
+
+def states(items):
+    """Array of State from (codes, scales, count, rows, cols) tuples."""
+    return (State * max(len(items), 1))(*items)
+
+
+def muon_set_coefficients(handle: int, abc) -> None:
+    """abc: a sequence of (a, b, c), one per iteration; empty: back to the hyper-parameters."""
+    flat = [float(x) for t in abc for x in t]
+    arr = (ctypes.c_float * max(len(flat), 1))(*flat)
+    _check(lib().muon_set_coefficients(handle, arr, len(flat) // 3), "muon_set_coefficients")
+
+
+def muon_orthogonalize_views(handle: int, X, O, n: int, hp: HParams, stream: int) -> None:
+    _check(lib().muon_orthogonalize_views(handle, X, O, n, ctypes.byref(hp), ctypes.c_void_p(stream)),
+           "muon_orthogonalize_views")
+
+
+def muon_state_quantize(X, S, n: int, fmt: int, seed, stream: int) -> None:
+    _check(lib().muon_state_quantize(X, S, n, fmt, _seed(seed), ctypes.c_void_p(stream)), "muon_state_quantize")
+
+
+def muon_state_dequantize(S, X, n: int, fmt: int, stream: int) -> None:
+    _check(lib().muon_state_dequantize(S, X, n, fmt, ctypes.c_void_p(stream)), "muon_state_dequantize")
+
+
+def muon_momentum_state(handle: int, G, S, U, n: int, fmt: int, hp: HParams, seed, stream: int) -> None:
+    _check(lib().muon_momentum_state(handle, G, S, U, n, fmt, ctypes.byref(hp), _seed(seed), ctypes.c_void_p(stream)),
+           "muon_momentum_state")
+
+
+def muon_step_state(handle: int, W, G, S, n: int, fmt: int, hp: HParams, seed, stream: int) -> None:
+    _check(lib().muon_step_state(handle, W, G, S, n, fmt, ctypes.byref(hp), _seed(seed), ctypes.c_void_p(stream)),
+           "muon_step_state")
 
 
 class AdamWHParams(ctypes.Structure):

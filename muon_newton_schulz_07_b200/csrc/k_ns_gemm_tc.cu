@@ -148,24 +148,55 @@ __device__ __forceinline__ Tile decode_tile(const TcParams& p, int t) {
   return ti;
 }
 
+// The 16-bit operand type of an instantiation: bf16 (MUON_MODE_FAST) or fp16 (MUON_MODE_HALF, whose
+// X, A and B' carry the power-of-two factors of muon_internal.h).
+template <bool HALF>
+struct Operand;
+template <>
+struct Operand<false> {
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack2(uint32_t q) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q));
+  }
+  static __device__ __forceinline__ float widen(const uint8_t* p) {
+    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+  }
+  static __device__ __forceinline__ float round(float x) { return bf16_round(x); }
+};
+template <>
+struct Operand<true> {
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack2(uint32_t q) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&q));
+  }
+  static __device__ __forceinline__ float widen(const uint8_t* p) {
+    return __half2float(*reinterpret_cast<const __half*>(p));
+  }
+  static __device__ __forceinline__ float round(float x) { return __half2float(__float2half_rn(x)); }
+};
+template <bool HALF>
 __device__ __forceinline__ void unpack8(const uint4& q, float* v) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
+  const uint32_t* h = reinterpret_cast<const uint32_t*>(&q);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(h[i]);
+    const float2 f = Operand<HALF>::unpack2(h[i]);
     v[2 * i] = f.x;
     v[2 * i + 1] = f.y;
   }
 }
+template <bool HALF>
 __device__ __forceinline__ uint4 pack8(const float* v) {
-  uint4 q;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  return q;
+  return make_uint4(Operand<HALF>::pack2(v[0], v[1]), Operand<HALF>::pack2(v[2], v[3]),
+                    Operand<HALF>::pack2(v[4], v[5]), Operand<HALF>::pack2(v[6], v[7]));
 }
 
-template <int KIND, bool WIDE>
+template <int KIND, bool WIDE, bool HALF>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::THREADS, 1)
     ns_gemm_tc_kernel(const __grid_constant__ TcParams p) {
   // WIDE (Update only): the pair tile is 256 x 512, two N = 256 MMAs per k step into one
@@ -320,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
           const int kk = kb * BK / TILE;
           const bool mna = sym_a && kk < ia;                        // transposed block of A / B'
           const bool mnb = (KIND == kUpdate) || (sym_b && kk < jb);
-          const uint32_t idesc = idesc_bf16_f32(2 * BM, BN, mna ? 1 : 0, mnb ? 1 : 0);
+          const uint32_t idesc = idesc_f16_f32(HALF, 2 * BM, BN, mna ? 1 : 0, mnb ? 1 : 0);
           // K-major: 16 k per step = 32 bytes along the swizzled row; MN-major: 16 k rows
           // = 2 KB, with the two 64-wide M/N chunks 8 KB apart.  The start address sits
           // in the low bits of the descriptor (16-byte units), so a step is a plain add.
@@ -390,7 +421,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
         W = static_cast<__nv_bfloat16*>(p.wptr[slot]);
         cw = p.wcoef[slot];
         tr = p.wtrans[slot] != 0;
-        ldw = tr ? G.m_real : G.n_real;
+        ldw = p.wld[slot];
       }
       const bool wread = fw && p.w_decay != 0.0f && gr0 < G.m_real;
       // element (row rr, 8 columns from sub_c) of the chunk at column gc in W's own layout
@@ -460,8 +491,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
           tmem_ld_32cols(taddr + (ch0 + c) * 32, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(s * p.c_acc * v[2 * i], s * p.c_acc * v[2 * i + 1]);
-            pk[c][i] = *reinterpret_cast<const uint32_t*>(&h);
+            pk[c][i] = Operand<HALF>::pack2(s * p.c_acc * v[2 * i], s * p.c_acc * v[2 * i + 1]);
           }
         }
         tc_fence_before();
@@ -493,23 +523,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
                 const int rr = q * 8 + sub_r;
                 float x8[8], r8[8];
                 if (!tr) {
-                  unpack8(*reinterpret_cast<const uint4*>(stg + rr * PITCH + sub_c * 2), x8);
+                  unpack8<HALF>(*reinterpret_cast<const uint4*>(stg + rr * PITCH + sub_c * 2), x8);
                 } else {
                   // W row gc0 + rr, columns gr0 + sub_c .. +7: column rr of staged rows sub_c ..
 #pragma unroll
                   for (int j = 0; j < 8; ++j)
-                    x8[j] = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(stg + (sub_c + j) * PITCH + rr * 2));
+                    x8[j] = Operand<HALF>::widen(stg + (sub_c + j) * PITCH + rr * 2);
                 }
                 if (wread) {
                   float w8[8];
-                  unpack8(w4[q], w8);
+                  unpack8<false>(w4[q], w8);
 #pragma unroll
                   for (int i = 0; i < 8; ++i) r8[i] = fmaf(p.w_decay, w8[i], cw * x8[i]);
                 } else {
 #pragma unroll
                   for (int i = 0; i < 8; ++i) r8[i] = cw * x8[i];
                 }
-                __stcs(reinterpret_cast<uint4*>(W + woff(gc0, rr)), pack8(r8));
+                __stcs(reinterpret_cast<uint4*>(W + woff(gc0, rr)), pack8<false>(r8));
               }
             }
           }
@@ -551,17 +581,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
           // Last Update: write the parameters instead of X_k.  Chunks in the zero padding
           // of the workspace have no parameters (real dimensions are multiples of 32).
           if (gr0 < G.m_real && gc0 < G.n_real) {
-            // stage X_k = s * acc as its bf16 store would hold it (so the write is exactly
+            // stage X_k = s * c_acc * acc as its 16-bit store would hold it (so the write is exactly
             // param_write_kernel's on the stored X_k), row-major or transposed for tall parameters
             if (!tr) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4)
                 *reinterpret_cast<float4*>(st32 + lane * F32_PITCH + i) =
-                    make_float4(bf16_round(s * v[i]), bf16_round(s * v[i + 1]), bf16_round(s * v[i + 2]),
-                                bf16_round(s * v[i + 3]));
+                    make_float4(Operand<HALF>::round(s * p.c_acc * v[i]), Operand<HALF>::round(s * p.c_acc * v[i + 1]),
+                                Operand<HALF>::round(s * p.c_acc * v[i + 2]),
+                                Operand<HALF>::round(s * p.c_acc * v[i + 3]));
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) st32[i * F32_PITCH + lane] = bf16_round(s * v[i]);
+              for (int i = 0; i < 32; ++i) st32[i * F32_PITCH + lane] = Operand<HALF>::round(s * p.c_acc * v[i]);
             }
             __syncwarp();
 #pragma unroll
@@ -572,14 +603,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
               float r8[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
               if (wread) {
                 float w8[8];
-                unpack8(pf[q], w8);
+                unpack8<false>(pf[q], w8);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) r8[i] = fmaf(p.w_decay, w8[i], cw * r8[i]);
               } else {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) r8[i] = cw * r8[i];
               }
-              __stcs(reinterpret_cast<uint4*>(W + woff(gc0, rr)), pack8(r8));
+              __stcs(reinterpret_cast<uint4*>(W + woff(gc0, rr)), pack8<false>(r8));
             }
           }
 #pragma unroll
@@ -597,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float a8[8];
-            unpack8(*reinterpret_cast<const uint4*>(arow + ((q ^ swz) << 4)), a8);
+            unpack8<HALF>(*reinterpret_cast<const uint4*>(arow + ((q ^ swz) << 4)), a8);
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[8 * q + i] = s * fmaf(p.c_acc, v[8 * q + i], p.c_aux * a8[i]);
           }
@@ -618,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<uint4*>(otile + ob + lane * 64 + ((q ^ swz) << 4)) = pack8(v + 8 * q);
+          *reinterpret_cast<uint4*>(otile + ob + lane * 64 + ((q ^ swz) << 4)) = pack8<HALF>(v + 8 * q);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -660,7 +691,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
   }
 }
 
-template <int KIND, bool WIDE>
+template <int KIND, bool WIDE, bool HALF>
 cudaError_t launch_kind(const TcParams& p, int grid, cudaStream_t s) {
   // The shared-memory limit is a property of the function on each device: set it once per device.
   static std::atomic<unsigned long long> attr_set{0};
@@ -669,13 +700,21 @@ cudaError_t launch_kind(const TcParams& p, int grid, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if ((attr_set.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(ns_gemm_tc_kernel<KIND, WIDE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(ns_gemm_tc_kernel<KIND, WIDE, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(Layout<KIND, WIDE>::SMEM_BYTES));
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(bit);
   }
-  ns_gemm_tc_kernel<KIND, WIDE><<<grid, Layout<KIND, WIDE>::THREADS, Layout<KIND, WIDE>::SMEM_BYTES, s>>>(p);
+  ns_gemm_tc_kernel<KIND, WIDE, HALF><<<grid, Layout<KIND, WIDE>::THREADS, Layout<KIND, WIDE>::SMEM_BYTES, s>>>(p);
   return cudaGetLastError();
+}
+
+template <bool HALF>
+cudaError_t launch_stage(const TcParams& p, int grid, cudaStream_t s) {
+  if (p.kind == kGram) return launch_kind<kGram, false, HALF>(p, grid, s);
+  if (p.kind == kPoly) return launch_kind<kPoly, false, HALF>(p, grid, s);
+  if (p.wide) return launch_kind<kUpdate, true, HALF>(p, grid, s);
+  return launch_kind<kUpdate, false, HALF>(p, grid, s);
 }
 
 }  // namespace
@@ -687,10 +726,7 @@ cudaError_t launch_tc_gemm(const TcParams& p, int num_sms, cudaStream_t s) {
   if (p.wide && p.kind != kUpdate) return cudaErrorInvalidValue;  // 256-wide only
   // one CTA pair per TPC, at most one pair per tile
   const int grid = 2 * std::min(num_sms / 2, p.total_tiles);
-  if (p.kind == kGram) return launch_kind<kGram, false>(p, grid, s);
-  if (p.kind == kPoly) return launch_kind<kPoly, false>(p, grid, s);
-  if (p.wide) return launch_kind<kUpdate, true>(p, grid, s);
-  return launch_kind<kUpdate, false>(p, grid, s);
+  return p.half ? launch_stage<true>(p, grid, s) : launch_stage<false>(p, grid, s);
 }
 
 }  // namespace muon

@@ -27,43 +27,15 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "muon.h"
+#include "muon_ctx.h"
 #include "muon_internal.h"
 
 using namespace muon;
 
 namespace {
 
-constexpr unsigned long long kTimeoutNs = 4000000000ull;  // bounded waits give up after 4 s
-
-// An NVTX range around the host-side enqueue of a call or a stage: it names the stages on a
-// profiler's timeline and costs nothing when no profiler is attached.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
-
 size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 int round_up(long long x, int a) { return static_cast<int>((x + a - 1) / a * a); }
-
-struct GroupPlan {
-  int m, n, mp, np, cnt;
-  std::vector<int> mats;      // caller indices, in caller order
-  size_t off_x[2], off_a, off_b;
-  int scal_base;
-  CUtensorMap tm_x[2], tm_a, tm_b;   // row views (K-major operand tiles)
-  CUtensorMap tt_x[2], tt_a, tt_b;   // chunked views (MN-major operand tiles)
-  CUtensorMap ts_x[2], ts_a, ts_b;   // store views (32 x 32 epilogue tiles)
-};
-
-struct Plan {
-  std::vector<GroupPlan> groups;
-  std::vector<int> mat_group, mat_slot, scal_idx;
-  std::vector<int> ew_ntiles;
-  size_t off_status, off_deps, off_scal, off_norms, off_partials;
-  size_t total;
-};
 
 bool shapes_ok(const muon_shape_t* shapes, int n) {
   if (shapes == nullptr || n < 1 || n > MUON_MAX_MATRICES) return false;
@@ -74,8 +46,13 @@ bool shapes_ok(const muon_shape_t* shapes, int n) {
   return true;
 }
 
-void make_plan(const muon_shape_t* shapes, int n, muon_mode_t mode, Plan* P) {
-  const size_t elem = (mode == MUON_MODE_FAST) ? 2 : 4;
+bool type_ok(muon_dtype_t dtype, muon_mode_t mode) {
+  return (dtype == MUON_BF16 || dtype == MUON_FP32) &&
+         (mode == MUON_MODE_FAST || mode == MUON_MODE_FP32_REF || mode == MUON_MODE_HALF);
+}
+
+void make_plan(const muon_shape_t* shapes, int n, muon_dtype_t dtype, muon_mode_t mode, Plan* P) {
+  const size_t elem = (mode == MUON_MODE_FP32_REF) ? 4 : 2;
   std::map<std::pair<long long, long long>, int> key_to_group;
   P->groups.clear();
   P->mat_group.assign(n, 0);
@@ -95,6 +72,7 @@ void make_plan(const muon_shape_t* shapes, int n, muon_mode_t mode, Plan* P) {
       gp.mp = round_up(m, kPad);
       gp.np = round_up(nn, kPad);
       gp.cnt = 0;
+      gp.skinny = mode == MUON_MODE_HALF && m <= kSkinnyRows && nn <= kSkinnyCluster * kSkinnyColsPart;
       P->groups.push_back(gp);
     } else {
       g = it->second;
@@ -141,12 +119,27 @@ void make_plan(const muon_shape_t* shapes, int n, muon_mode_t mode, Plan* P) {
   P->off_partials = off;
   off = align_up(off + sizeof(float) * parts, 1024);
   for (GroupPlan& gp : P->groups) {
+    if (gp.skinny) continue;
     const size_t xb = static_cast<size_t>(gp.cnt) * gp.mp * gp.np * elem;
     const size_t ab = static_cast<size_t>(gp.cnt) * gp.mp * gp.mp * elem;
     gp.off_x[0] = off; off = align_up(off + xb, 1024);
     gp.off_x[1] = off; off = align_up(off + xb, 1024);
     gp.off_a = off;    off = align_up(off + ab, 1024);
     gp.off_b = off;    off = align_up(off + ab, 1024);
+  }
+  if (mode == MUON_MODE_HALF) {
+    // U of each matrix, rows x cols in the handle's type: in the second X buffer, which nothing
+    // uses before the first update, or in a place of its own where there is none or it is too short
+    P->off_u.assign(n, 0);
+    for (int i = 0; i < n; ++i) {
+      const GroupPlan& gp = P->groups[P->mat_group[i]];
+      if (dtype == MUON_BF16 && !gp.skinny) {
+        P->off_u[i] = gp.off_x[1] + static_cast<size_t>(P->mat_slot[i]) * gp.mp * gp.np * elem;
+      } else {
+        P->off_u[i] = off;
+        off = align_up(off + static_cast<size_t>(shapes[i].rows) * shapes[i].cols * (dtype == MUON_BF16 ? 2 : 4), 1024);
+      }
+    }
   }
   P->total = off;
 }
@@ -167,7 +160,7 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// Row view of a [cnt][rows][cols] bf16 buffer: one box is 64 columns x 128 rows of one
+// Row view of a [cnt][rows][cols] bf16 buffer (fp16 ones take the same maps: a copy does no arithmetic): one box is 64 columns x 128 rows of one
 // matrix (16 KB, 128-byte swizzle), the K-major operand tile of one CTA and k slice.
 bool encode_rows(CUtensorMap* map, void* base, int cols, int rows, int cnt) {
   EncodeTiledFn fn = encode_fn();
@@ -211,23 +204,9 @@ bool encode_chunks(CUtensorMap* map, void* base, int cols, int rows, int cnt) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-class DeviceGuard {
- public:
-  explicit DeviceGuard(int dev) {
-    if (cudaGetDevice(&prev_) == cudaSuccess && prev_ != dev) {
-      if (cudaSetDevice(dev) == cudaSuccess) switched_ = true;
-    }
-  }
-  ~DeviceGuard() {
-    if (switched_) cudaSetDevice(prev_);
-  }
+}  // namespace
 
- private:
-  int prev_ = -1;
-  bool switched_ = false;
-};
-
-bool hp_ok(const muon_hparams_t* hp, bool need_momentum) {
+bool muon::hp_ok(const muon_hparams_t* hp, bool need_momentum) {
   if (hp == nullptr) return false;
   if (hp->ns_steps < 0 || hp->ns_steps > 64) return false;
   if (!std::isfinite(hp->eps) || hp->eps < 0.0f) return false;
@@ -239,41 +218,8 @@ bool hp_ok(const muon_hparams_t* hp, bool need_momentum) {
   return true;
 }
 
-}  // namespace
-
-struct muon_ctx {
-  int device = 0;
-  int num_sms = 0;
-  muon_dtype_t dtype = MUON_BF16;
-  muon_mode_t mode = MUON_MODE_FAST;
-  int n = 0;
-  std::vector<muon_shape_t> shapes;
-  Plan plan;
-  char* ws = nullptr;
-  size_t ws_bytes = 0;
-  unsigned int* d_status = nullptr;
-  float* d_scal = nullptr;
-  float* d_partials = nullptr;
-  float* d_norms = nullptr;   // ||U_i||_F in caller order
-  bool fuse_shapes_ok = false;  // every group's real dimensions are multiples of 32, n <= kTcMaxFused
-  int schedule = MUON_SCHEDULE_AUTO;
-  // launch parameter blocks (tens of KB), reused by every call on this handle
-  EwParams ew;
-  WrParams wr;
-  TcParams tc;
-  SmallParams sm;
-  NsParams ns;
-  // tracing (muon_profile_begin / muon_profile_end)
-  int prof_steps_left = 0;
-  std::vector<std::pair<int, cudaEvent_t>> prof_events;  // kind (-1: start of a call), event
-};
-
-namespace {
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 // Record a tracing event after a launch of `kind` (or at the start of a call, kind -1).
-void trace(muon_ctx* h, int kind, cudaStream_t st) {
+void muon::trace(muon_ctx* h, int kind, cudaStream_t st) {
   if (h->prof_steps_left <= 0) return;
   cudaEvent_t ev;
   if (cudaEventCreate(&ev) != cudaSuccess) return;
@@ -284,9 +230,61 @@ void trace(muon_ctx* h, int kind, cudaStream_t st) {
   h->prof_events.emplace_back(kind, ev);
 }
 
-void trace_call_end(muon_ctx* h) {
+void muon::trace_call_end(muon_ctx* h) {
   if (h->prof_steps_left > 0) --h->prof_steps_left;
 }
+
+// One group's part of a staged launch.
+void muon::stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur, int nxt, int tw, TcGroup* G) {
+  G->cnt = gp.cnt;
+  G->mp = gp.mp;
+  G->np = gp.np;
+  G->scal_base = gp.scal_base;
+  const int T = gp.mp / 256;
+  if (kind == kGram) {
+    G->tm_a = gp.tm_x[cur];
+    G->tm_at = gp.tt_x[cur];
+    G->tm_b = gp.tm_x[cur];
+    G->tm_bt = gp.tt_x[cur];
+    G->tm_out = gp.ts_a;
+    G->out = h->ws + gp.off_a;
+    G->tiles_per_mat = T * (T + 1) / 2;  // 256 x 256 pair tiles on or above the diagonal
+    G->kblocks = gp.np / kTcBK;
+    G->tdim = T;
+    G->out_ld = gp.mp;
+    G->m_real = gp.m;
+  } else if (kind == kPoly) {
+    G->tm_a = gp.tm_a;
+    G->tm_at = gp.tt_a;
+    G->tm_b = gp.tm_a;
+    G->tm_bt = gp.tt_a;
+    G->tm_out = gp.ts_b;
+    G->out = h->ws + gp.off_b;
+    G->tm_aux = gp.ts_a;
+    G->tiles_per_mat = T * (T + 1) / 2;
+    G->m_real = gp.m;
+    G->kblocks = gp.mp / kTcBK;
+    G->tdim = T;
+    G->out_ld = gp.mp;
+  } else {
+    G->tm_a = gp.tm_b;
+    G->tm_at = gp.tt_b;
+    G->tm_b = gp.tm_x[cur];
+    G->tm_bt = gp.tt_x[cur];
+    G->tm_out = gp.ts_x[nxt];
+    G->out = h->ws + gp.off_x[nxt];
+    G->tiles_per_mat = (gp.mp / 256) * (gp.np / tw);  // 256 x tw pair tiles
+    G->kblocks = gp.mp / kTcBK;
+    G->tdim = gp.np / tw;
+    G->out_ld = gp.np;
+    G->m_real = gp.m;
+    G->n_real = gp.n;
+  }
+}
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool small_path(const muon_ctx* h, int k);
 
@@ -614,6 +612,7 @@ cudaError_t enqueue_ns(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st, i
                 const float r = static_cast<float>(h->shapes[i].rows), c = static_cast<float>(h->shapes[i].cols);
                 prm.wptr[slot] = dst[i];
                 prm.wcoef[slot] = store_only ? 1.0f : -hp->lr * std::sqrt(std::max(1.0f, r / c));
+                prm.wld[slot] = static_cast<int>(h->shapes[i].cols);
                 prm.wtrans[slot] = h->shapes[i].rows > h->shapes[i].cols ? 1 : 0;
               }
             }
@@ -622,51 +621,8 @@ cudaError_t enqueue_ns(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st, i
           for (int gi = 0; gi < ng; ++gi) {
             const GroupPlan& gp = P.groups[g0 + gi];
             TcGroup& G = prm.g[gi];
-            G.cnt = gp.cnt;
-            G.mp = gp.mp;
-            G.np = gp.np;
-            G.scal_base = gp.scal_base;
             G.tile_begin = tiles;
-            const int T = gp.mp / 256;
-            if (kind == kGram) {
-              G.tm_a = gp.tm_x[cur];
-              G.tm_at = gp.tt_x[cur];
-              G.tm_b = gp.tm_x[cur];
-              G.tm_bt = gp.tt_x[cur];
-              G.tm_out = gp.ts_a;
-              G.out = h->ws + gp.off_a;
-              G.tiles_per_mat = T * (T + 1) / 2;  // 256 x 256 pair tiles on or above the diagonal
-              G.kblocks = gp.np / kTcBK;
-              G.tdim = T;
-              G.out_ld = gp.mp;
-              G.m_real = gp.m;
-            } else if (kind == kPoly) {
-              G.tm_a = gp.tm_a;
-              G.tm_at = gp.tt_a;
-              G.tm_b = gp.tm_a;
-              G.tm_bt = gp.tt_a;
-              G.tm_out = gp.ts_b;
-              G.out = h->ws + gp.off_b;
-              G.tm_aux = gp.ts_a;
-              G.tiles_per_mat = T * (T + 1) / 2;
-              G.m_real = gp.m;
-              G.kblocks = gp.mp / kTcBK;
-              G.tdim = T;
-              G.out_ld = gp.mp;
-            } else {
-              G.tm_a = gp.tm_b;
-              G.tm_at = gp.tt_b;
-              G.tm_b = gp.tm_x[cur];
-              G.tm_bt = gp.tt_x[cur];
-              G.tm_out = gp.ts_x[nxt];
-              G.out = h->ws + gp.off_x[nxt];
-              G.tiles_per_mat = (gp.mp / 256) * (gp.np / tw);  // 256 x tw pair tiles
-              G.kblocks = gp.mp / kTcBK;
-              G.tdim = gp.np / tw;
-              G.out_ld = gp.np;
-              G.m_real = gp.m;
-              G.n_real = gp.n;
-            }
+            stage_group(h, gp, kind, cur, nxt, tw, &G);
             tiles += G.tiles_per_mat * gp.cnt;
           }
           prm.total_tiles = tiles;
@@ -772,6 +728,7 @@ cudaError_t enqueue_back(muon_ctx* h, void* const* dst, const muon_hparams_t* hp
 }
 
 int launches_for(const muon_ctx* h, int k) {
+  if (h->mode == MUON_MODE_HALF) return half_launches(h, k);
   const int chunks = (h->n + kEwMatsPerLaunch - 1) / kEwMatsPerLaunch;
   const int front = 2 * chunks;  // momentum/norm and the norms' finishing pass, per 192 matrices
   if (small_path(h, k)) return front + 1 + chunks;
@@ -804,10 +761,9 @@ const char* muon_status_string(muon_status_t s) {
 muon_status_t muon_workspace_size(const muon_shape_t* shapes, int n, muon_dtype_t dtype, muon_mode_t mode,
                                   size_t* bytes) {
   if (bytes == nullptr || !shapes_ok(shapes, n)) return MUON_ERR_INVALID_ARG;
-  if ((dtype != MUON_BF16 && dtype != MUON_FP32) || (mode != MUON_MODE_FAST && mode != MUON_MODE_FP32_REF))
-    return MUON_ERR_INVALID_ARG;
+  if (!type_ok(dtype, mode)) return MUON_ERR_INVALID_ARG;
   Plan P;
-  make_plan(shapes, n, mode, &P);
+  make_plan(shapes, n, dtype, mode, &P);
   *bytes = P.total;
   return MUON_OK;
 }
@@ -817,8 +773,7 @@ muon_status_t muon_create(muon_handle_t* handle, const muon_shape_t* shapes, int
   if (handle == nullptr) return MUON_ERR_INVALID_ARG;
   *handle = nullptr;
   if (!shapes_ok(shapes, n)) return MUON_ERR_INVALID_ARG;
-  if ((dtype != MUON_BF16 && dtype != MUON_FP32) || (mode != MUON_MODE_FAST && mode != MUON_MODE_FP32_REF))
-    return MUON_ERR_INVALID_ARG;
+  if (!type_ok(dtype, mode)) return MUON_ERR_INVALID_ARG;
   int dev = -1, ndev = 0;
   if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev < 1 || cudaGetDevice(&dev) != cudaSuccess) {
     cudaGetLastError();
@@ -836,7 +791,7 @@ muon_status_t muon_create(muon_handle_t* handle, const muon_shape_t* shapes, int
   h->mode = mode;
   h->n = n;
   h->shapes.assign(shapes, shapes + n);
-  make_plan(shapes, n, mode, &h->plan);
+  make_plan(shapes, n, dtype, mode, &h->plan);
   h->fuse_shapes_ok = n <= kTcMaxFused;
   for (const GroupPlan& gp : h->plan.groups)
     if (gp.m % 32 != 0 || gp.n % 32 != 0) h->fuse_shapes_ok = false;
@@ -855,8 +810,9 @@ muon_status_t muon_create(muon_handle_t* handle, const muon_shape_t* shapes, int
     delete h;
     return MUON_ERR_CUDA;
   }
-  if (mode == MUON_MODE_FAST) {
+  if (mode != MUON_MODE_FP32_REF) {
     for (GroupPlan& gp : h->plan.groups) {
+      if (gp.skinny) continue;
       bool ok = true;
       for (int b = 0; b < 2; ++b)
         ok = ok && encode_rows(&gp.tm_x[b], h->ws + gp.off_x[b], gp.np, gp.mp, gp.cnt) &&
@@ -889,6 +845,7 @@ muon_status_t muon_step(muon_handle_t h, void* const* W, const void* const* G, v
   if (h == nullptr || W == nullptr || G == nullptr || M == nullptr || !hp_ok(hp, true)) return MUON_ERR_INVALID_ARG;
   for (int i = 0; i < h->n; ++i)
     if (W[i] == nullptr || G[i] == nullptr || M[i] == nullptr) return MUON_ERR_INVALID_ARG;
+  if (h->mode == MUON_MODE_HALF) return half_step(h, W, G, M, hp, stream);
   DeviceGuard guard(h->device);
   NvtxRange range("muon_step");
   int launches = 0;
@@ -905,6 +862,7 @@ muon_status_t muon_orthogonalize(muon_handle_t h, const void* const* X, void* co
   if (h == nullptr || X == nullptr || O == nullptr || !hp_ok(hp, false)) return MUON_ERR_INVALID_ARG;
   for (int i = 0; i < h->n; ++i)
     if (X[i] == nullptr || O[i] == nullptr) return MUON_ERR_INVALID_ARG;
+  if (h->mode == MUON_MODE_HALF) return half_orthogonalize(h, X, O, hp, stream);
   DeviceGuard guard(h->device);
   NvtxRange range("muon_orthogonalize");
   muon_hparams_t q = *hp;
@@ -958,7 +916,7 @@ muon_status_t muon_check_plan(const muon_shape_t* shapes, int n, int ns_steps, i
       num_sms > 4096)
     return MUON_ERR_INVALID_ARG;
   Plan P;
-  make_plan(shapes, n, MUON_MODE_FAST, &P);
+  make_plan(shapes, n, MUON_BF16, MUON_MODE_FAST, &P);
   std::vector<muon_shape_t> sh(shapes, shapes + n);
   long long bad = 0;
   EwParams* ew = new (std::nothrow) EwParams;
@@ -1009,10 +967,10 @@ muon_status_t muon_get_group_buffers(muon_handle_t h, int group, int* mp, int* n
   if (mp) *mp = gp.mp;
   if (np) *np = gp.np;
   if (count) *count = gp.cnt;
-  if (x0) *x0 = h->ws + gp.off_x[0];
-  if (x1) *x1 = h->ws + gp.off_x[1];
-  if (a) *a = h->ws + gp.off_a;
-  if (b) *b = h->ws + gp.off_b;
+  if (x0) *x0 = gp.skinny ? nullptr : h->ws + gp.off_x[0];
+  if (x1) *x1 = gp.skinny ? nullptr : h->ws + gp.off_x[1];
+  if (a) *a = gp.skinny ? nullptr : h->ws + gp.off_a;
+  if (b) *b = gp.skinny ? nullptr : h->ws + gp.off_b;
   return MUON_OK;
 }
 

@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "muon_internal.h"
 
@@ -341,6 +342,12 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, int a_mn_maj
          | (static_cast<uint32_t>(b_mn_major) << 16) // B major
          | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
          | (static_cast<uint32_t>(M >> 4) << 24);    // M / 16
+}
+
+// The same with A and B both fp16 (format 0) when `half`, else both bf16 (format 1).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(bool half, int M, int N, int a_mn_major, int b_mn_major) {
+  return half ? idesc_bf16_f32(M, N, a_mn_major, b_mn_major) & ~((1u << 7) | (1u << 10))
+              : idesc_bf16_f32(M, N, a_mn_major, b_mn_major);
 }
 
 // ---------------------------------------------------------------- misc

@@ -123,6 +123,7 @@ struct TcParams {
   int total_tiles;
   int kind;
   int wide;              // Update with 256 x 512 pair tiles (every group's np a multiple of 512)
+  int half;              // operands are fp16 (MUON_MODE_HALF), not bf16
   int use_scal;          // first iteration: fold the normalisation in
   float c_acc, c_aux;    // out = s * (c_acc * acc + c_aux * aux) (+ c_diag on the real diagonal)
   float c_diag;
@@ -137,6 +138,7 @@ struct TcParams {
   float w_decay;
   void* wptr[kTcMaxFused];
   float wcoef[kTcMaxFused];
+  int wld[kTcMaxFused];  // elements between rows of the matrix as it is stored
   unsigned char wtrans[kTcMaxFused];
 };
 
@@ -231,6 +233,124 @@ struct SmallParams {
 
 size_t small_smem_bytes();
 cudaError_t launch_ns_small(const SmallParams& p, int num_sms, cudaStream_t s);
+
+// ------------------------------------------------------------------ fp16 operands (MUON_MODE_HALF)
+// The iteration's operands are stored in fp16 (11 significant bits, three more than bf16) times
+// powers of two, folded into the epilogues' coefficients, that keep what matters in fp16's normal
+// range: after Frobenius normalisation a typical entry of X is 1/sqrt(mn) and of A 1/(m sqrt(n)),
+// down to 2^-20, while no entry of X or A exceeds the largest singular value (squared) and none of
+// B' exceeds |a| + |b| s^2 + |c| s^4.  Singular values up to 4 and polynomials up to 255 fit.
+constexpr float kHalfX = 4096.0f;  // stored X  = 2^12 X
+constexpr float kHalfA = 4096.0f;  // stored A  = 2^12 A
+constexpr float kHalfB = 256.0f;   // stored B' = 2^8 B'
+
+// Storage types of a view (MUON_BF16, MUON_FP32, MUON_FP16).
+enum ViewType : int { kViewBF16 = 0, kViewF32 = 1, kViewF16 = 2 };
+
+// `count` equal matrices of a call: how their elements are stored on the source and destination
+// side, and their place in the launch's and the handle's tables.  A side is stored as rows of
+// contiguous elements, `ld` apart; `tr` says that those rows are the columns of the oriented X
+// (min x max), so that the tile is transposed on its way.  Matrix e starts at e * bs.
+struct ViewSeg {
+  const void* src;
+  void* dst;
+  long long src_ld, src_bs, dst_ld, dst_bs;
+  int src_type, dst_type;
+  int src_tr, dst_tr;
+  int src_vec, dst_vec;  // every stored row starts 16-byte aligned
+  void* x;               // workspace X of the first matrix, [count][mp][np] fp16
+  int m, n, mp, np;
+  int count;
+  int mat_begin;         // first matrix of the launch's numbering
+  int tile_begin;        // first tile (CTA) of the launch
+  int tiles_c, tiles;    // tiles along a row of X, tiles of one matrix
+  int part_begin;        // first partial sum; `parts` for each matrix
+  int parts;
+  int caller_idx;        // first matrix's place in the handle's list
+  float coef;            // the write: dst = decay * dst + coef * X (X as stored, 2^12 X)
+};
+
+constexpr int kViewSegs = 96;
+struct ViewParams {
+  ViewSeg seg[kViewSegs];
+  int nseg;
+  int total;             // CTAs
+  float eps;
+  float decay;           // 0: dst is not read
+  float* partials;
+  float* norms;
+};
+
+// Sums of squares of the sources, one partial per CTA (a 64 x 128 tile).
+cudaError_t launch_view_sumsq(const ViewParams& p, cudaStream_t s);
+// X0 = 2^12 src / (||src|| + eps), oriented and zero-padded; adds the partial sums itself.
+cudaError_t launch_view_orient(const ViewParams& p, cudaStream_t s);
+// dst = decay * dst + coef * X.
+cudaError_t launch_view_write(const ViewParams& p, cudaStream_t s);
+
+// Matrices of few rows: every iteration on chip, one cluster per 128-row tile (k_ns_skinny.cu).
+constexpr int kSkinnyRows = 128;       // most rows (of the oriented matrix)
+constexpr int kSkinnyColsOne = 768;    // most columns one CTA holds by itself
+constexpr int kSkinnyColsPart = 512;   // most columns of each CTA of a cluster
+constexpr int kSkinnyCluster = 8;      // most CTAs of a cluster
+constexpr int kSkinnySegs = 64;
+constexpr int kMaxSteps = 64;
+
+struct SkinnyParams {
+  ViewSeg seg[kSkinnySegs];  // mat_begin numbers the launch's matrices; the workspace is not used
+  int nseg;
+  int total;                 // matrices
+  int m, n;
+  int slot_rows;             // rows of the tile each matrix takes: a power of two >= m
+  int slots;                 // matrices in a tile
+  int cluster;               // CTAs of a tile
+  int width;                 // columns each CTA holds, a multiple of 64
+  int k;
+  float coef[kMaxSteps][3];  // (a, b, c) of each iteration
+  float eps;
+  float decay;
+  float* norms;
+  unsigned int* status;
+  unsigned long long timeout_ns;
+};
+cudaError_t launch_ns_skinny(const SkinnyParams& p, cudaStream_t s);
+
+// ------------------------------------------------------------------ 8-bit state
+constexpr int kStateBlock = 128;   // columns that share a scale
+constexpr int kStateUnits = 64;    // (row, block) units of one CTA
+enum StateFormat : int { kStateInt8 = 0, kStateE4M3 = 1, kStateDense = 2 };
+
+struct StateSeg {
+  const void* in;        // quantise: X; momentum: G
+  void* out;             // dequantise: X; momentum: U
+  void* codes;           // int8 / e4m3 codes, or the dense momentum
+  float* scales;
+  long long in_ld, in_bs, out_ld, out_bs;
+  int in_type, out_type;
+  int vec;               // every row of every side is aligned for vector accesses
+  int rows, cols, blocks;
+  int count;
+  int mat_begin;         // first matrix's number in the call (the random bits' key)
+  int unit_ctas;         // CTAs of one matrix
+  int cta_begin;
+  int caller_idx;        // momentum: first matrix's place in the handle's list
+};
+constexpr int kStateSegs = 128;
+struct StateParams {
+  StateSeg seg[kStateSegs];
+  int nseg;
+  int total;             // CTAs
+  int stochastic;
+  unsigned int seed;
+  float beta;
+  int nesterov;
+  float* partials;       // momentum: one sum of squares per CTA
+  float* norms;
+};
+cudaError_t launch_state_quantize(const StateParams& p, StateFormat f, cudaStream_t s);
+cudaError_t launch_state_dequantize(const StateParams& p, StateFormat f, cudaStream_t s);
+// G, U and a dense momentum have one type, bf16 or fp32.
+cudaError_t launch_state_momentum(const StateParams& p, StateFormat f, cudaStream_t s);
 
 // ------------------------------------------------------------------ fp32 reference GEMMs
 struct SgParams {

@@ -1,0 +1,94 @@
+// Device helpers for matrices that stay in the caller's layout: eight consecutive elements of a
+// stored row as fp32, whatever the storage type, and the power-of-two factors of the fp16 iterates.
+#pragma once
+
+#include "muon_device.cuh"
+
+namespace muon {
+
+__device__ __forceinline__ void widen8(const uint4& q, int type, float (&v)[8]) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = type == kViewBF16 ? __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]))
+                                       : __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ float load_one(const void* base, int type, long long at) {
+  if (type == kViewF32) return static_cast<const float*>(base)[at];
+  if (type == kViewBF16) return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[at]);
+  return __half2float(static_cast<const __half*>(base)[at]);
+}
+__device__ __forceinline__ void store_one(void* base, int type, long long at, float x) {
+  if (type == kViewF32)
+    static_cast<float*>(base)[at] = x;
+  else if (type == kViewBF16)
+    static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(x);
+  else
+    static_cast<__half*>(base)[at] = __float2half_rn(x);
+}
+
+// Elements at .. at + 7 of a stored row; the first `have` exist, the others come back as 0.
+// `vec`: the row starts 16-byte aligned and `at` is a multiple of 8 elements into it.
+__device__ __forceinline__ void load_eight(const void* base, int type, long long at, int have, bool vec,
+                                           float (&v)[8]) {
+  if (vec && have >= 8) {
+    if (type == kViewF32) {
+      const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
+      const float4 a = p[0], b = p[1];
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    } else {
+      widen8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at), type, v);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = i < have ? load_one(base, type, at + i) : 0.0f;
+}
+
+__device__ __forceinline__ void store_eight(void* base, int type, long long at, int have, bool vec,
+                                            const float (&v)[8]) {
+  if (vec && have >= 8) {
+    if (type == kViewF32) {
+      float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
+      p[0] = make_float4(v[0], v[1], v[2], v[3]);
+      p[1] = make_float4(v[4], v[5], v[6], v[7]);
+    } else {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (type == kViewBF16) {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (i < have) store_one(base, type, at + i, v[i]);
+}
+
+// x / (norm + eps) * 2^12 as one multiplication: x * pre * mul.  `pre` lifts x first when the
+// denominator is so small that its reciprocal would overflow.  A zero denominator gives 0.
+struct Normaliser {
+  float pre, mul;
+};
+__device__ __forceinline__ Normaliser normaliser(float norm, float eps) {
+  const float den = norm + eps;
+  Normaliser n;
+  n.pre = den < 1.0e-30f ? 1.8446744e19f : 1.0f;  // 2^64
+  n.mul = den > 0.0f ? kHalfX / (den * n.pre) : (den == 0.0f ? 0.0f : den);  // NaN stays NaN
+  return n;
+}
+
+}  // namespace muon

@@ -14,9 +14,116 @@ from . import binding as B
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
 
+_VIEW_TYPES = {torch.bfloat16: B.MUON_BF16, torch.float32: B.MUON_FP32, torch.float16: B.MUON_FP16}
+
+
+def _entries(shapes):
+    """(count, rows, cols, shape a tensor of the entry has) of (rows, cols) matrices and (count, rows, cols) stacks."""
+    out = []
+    for s in shapes:
+        s = tuple(int(x) for x in s)
+        if len(s) not in (2, 3):
+            raise ValueError(f"a shape is (rows, cols) or (count, rows, cols): got {s}")
+        out.append((s if len(s) == 3 else (1,) + s) + (s,))
+    return out
+
+
+def _view(t, count):
+    """The tuple of binding.views for a matrix or a stack of them."""
+    st = t.stride()
+    if len(st) == 2:
+        return (t.data_ptr(), 1, 0, st[0], st[1], _VIEW_TYPES[t.dtype])
+    return (t.data_ptr(), count, st[0], st[1], st[2], _VIEW_TYPES[t.dtype])
+
+
+def _views(tensors, entries, device, name, dtype=None, by_rows=False):
+    """Views of tensors that may be strided; dtype None: any of bf16, fp16 and fp32."""
+    if len(tensors) != len(entries):
+        raise ValueError(f"{name}: expected {len(entries)} tensors, got {len(tensors)}")
+    out = []
+    for t, (count, rows, cols, shape) in zip(tensors, entries):
+        if tuple(t.shape) != shape or t.device != device or (t.dtype != dtype if dtype else t.dtype not in _VIEW_TYPES):
+            raise ValueError(f"{name}: tensor {tuple(t.shape)} {t.dtype} {t.device} does not match {shape} "
+                             f"{dtype or 'bf16, fp16 or fp32'} {device}")
+        by_row = t.stride(-1) == 1 or cols == 1
+        if not by_row and (by_rows or not (t.stride(-2) == 1 or rows == 1)):
+            raise ValueError(f"{name}: a tensor of strides {t.stride()} is not stored by rows"
+                             + ("" if by_rows else " or by columns"))
+        out.append(_view(t, count))
+    return B.views(out)
+
+
+class QuantizedState:
+    """8-bit optimizer state: codes (int8 or e4m3), and one fp32 scale for each 128 columns of a row.
+
+        state = QuantizedState([(768, 768), (12, 64, 768)], fmt="int8")    # zero
+        state.write(tensors, seed=step)                                     # quantise
+        state.read(tensors)                                                 # read back
+        step(W, G, state, seed=t)                                           # a MuonStep's momentum (mode="half")
+
+    Shapes are (rows, cols) matrices or (count, rows, cols) stacks.  `codes` and `scales` are lists of tensors
+    of those shapes, to be saved, loaded and sharded by rows like any other.  Rounding is to nearest even, or, with
+    a seed, stochastic: unbiased, from a generator of the seed and the value's place; give every call another seed.
+    Int8 is finer where the values of a block are alike, e4m3 keeps small values beside large ones.
+    """
+
+    FORMATS = {"int8": (B.MUON_STATE_INT8, torch.int8), "e4m3": (B.MUON_STATE_E4M3, torch.float8_e4m3fn)}
+    BLOCK = B.MUON_STATE_BLOCK
+
+    def __init__(self, shapes, fmt: str = "int8", device=None):
+        if fmt not in self.FORMATS:
+            raise ValueError(f"fmt must be one of {sorted(self.FORMATS)}")
+        self.fmt = fmt
+        self._fmt, code = self.FORMATS[fmt]
+        self._entries = _entries(shapes)
+        self.shapes = [e[3] for e in self._entries]
+        dev = torch.device(device if device is not None else "cuda")
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        self.device = dev
+        self.codes = [torch.zeros(s, dtype=torch.uint8, device=dev).view(code) for s in self.shapes]
+        self.scales = [torch.zeros(s[:-1] + (-(-s[-1] // self.BLOCK),), dtype=torch.float32, device=dev)
+                       for s in self.shapes]
+
+    def _states(self):
+        code = self.FORMATS[self.fmt][1]
+        out = []
+        for q, s, (count, rows, cols, shape) in zip(self.codes, self.scales, self._entries):
+            blocks = shape[:-1] + (-(-cols // self.BLOCK),)
+            if tuple(q.shape) != shape or q.dtype != code or not q.is_contiguous() or q.device != self.device:
+                raise ValueError(f"codes: tensor {tuple(q.shape)} {q.dtype} {q.device} does not match {shape} {code} "
+                                 f"{self.device} (contiguous)")
+            if tuple(s.shape) != blocks or s.dtype != torch.float32 or not s.is_contiguous() or s.device != self.device:
+                raise ValueError(f"scales: tensor {tuple(s.shape)} {s.dtype} {s.device} does not match {blocks} "
+                                 f"torch.float32 {self.device} (contiguous)")
+            out.append((q.data_ptr(), s.data_ptr(), count, rows, cols))
+        return B.states(out)
+
+    def _side(self, tensors, name):
+        if tensors and any(t.dtype != tensors[0].dtype for t in tensors):
+            raise ValueError(f"{name}: tensors of one call have one dtype")
+        return _views(tensors, self._entries, self.device, name, by_rows=True)
+
+    def write(self, X, seed=None, stream=None) -> None:
+        """Quantise X (bf16, fp16 or fp32, stored by rows) into this state, on the current stream or `stream`."""
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        with torch.cuda.device(self.device):
+            B.muon_state_quantize(self._side(X, "X"), self._states(), len(self.shapes), self._fmt, seed, s.cuda_stream)
+
+    def read(self, out, stream=None) -> None:
+        """Read this state back into the tensors of `out` (bf16, fp16 or fp32, stored by rows)."""
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        with torch.cuda.device(self.device):
+            B.muon_state_dequantize(self._states(), self._side(out, "out"), len(self.shapes), self._fmt, s.cuda_stream)
+
 
 class MuonStep:
-    """A Muon step for one fixed list of matrix shapes, bound to one CUDA device."""
+    """A Muon step for one fixed list of matrix shapes, bound to one CUDA device.
+
+    A shape is (rows, cols), or (count, rows, cols) for a stack of equal matrices, each stepped by itself (experts,
+    attention heads).  mode: "fast" (bf16 operands), "half" (fp16 operands: an eighth of the rounding error at the
+    same rate; takes strided views, coefficients per iteration and 8-bit momentum) or "fp32_ref" (slow, exact).
+    """
 
     SCHEDULES = {"auto": B.MUON_SCHEDULE_AUTO, "staged": B.MUON_SCHEDULE_STAGED, "fused": B.MUON_SCHEDULE_FUSED,
                  "split": B.MUON_SCHEDULE_SPLIT}
@@ -24,20 +131,24 @@ class MuonStep:
     def __init__(self, shapes, dtype=torch.bfloat16, mode: str = "fast", device=None, schedule: str = "auto"):
         if dtype not in (torch.bfloat16, torch.float32):
             raise TypeError("dtype must be torch.bfloat16 or torch.float32")
-        if mode not in ("fast", "fp32_ref"):
-            raise ValueError("mode must be 'fast' or 'fp32_ref'")
-        self.shapes = [(int(r), int(c)) for r, c in shapes]
+        if mode not in ("fast", "half", "fp32_ref"):
+            raise ValueError("mode must be 'fast', 'half' or 'fp32_ref'")
+        self._entries = _entries(shapes)
+        self.shapes = [e[3] for e in self._entries]
+        matrices = [(rows, cols) for count, rows, cols, _ in self._entries for _ in range(count)]
+        self.mode = mode
         self.dtype = dtype
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         self._dt = B.MUON_BF16 if dtype == torch.bfloat16 else B.MUON_FP32
-        self._mode = B.MUON_MODE_FAST if mode == "fast" else B.MUON_MODE_FP32_REF
-        nbytes = B.muon_workspace_size(self.shapes, self._dt, self._mode)
+        self._mode = {"fast": B.MUON_MODE_FAST, "half": B.MUON_MODE_HALF, "fp32_ref": B.MUON_MODE_FP32_REF}[mode]
+        nbytes = B.muon_workspace_size(matrices, self._dt, self._mode)
+        self._n = len(matrices)
         self.workspace_bytes = nbytes
         with torch.cuda.device(self.device):
             self._ws = torch.empty(nbytes + 1024, dtype=torch.uint8, device=self.device)
             base = self._ws.data_ptr()
             self._ws_ptr = (base + 1023) // 1024 * 1024
-            self.handle = B.muon_create(self.shapes, self._dt, self._mode, self._ws_ptr, nbytes)
+            self.handle = B.muon_create(matrices, self._dt, self._mode, self._ws_ptr, nbytes)
         self.n_groups, _ = B.muon_get_plan(self.handle, 5)
         if schedule != "auto":
             self.set_schedule(schedule)
@@ -59,12 +170,52 @@ class MuonStep:
             if tuple(t.shape) != s or t.dtype != self.dtype or t.device != self.device or not t.is_contiguous():
                 raise ValueError(f"{name}: tensor {tuple(t.shape)} {t.dtype} {t.device} does not match {s} "
                                  f"{self.dtype} {self.device} (contiguous)")
-        return [t.data_ptr() for t in tensors]
+        # one pointer a matrix: a stack holds its matrices back to back
+        return [t.data_ptr() + e * rows * cols * t.element_size()
+                for t, (count, rows, cols, _) in zip(tensors, self._entries) for e in range(count)]
+
+    def _coefficients(self, abc, ns_steps):
+        """(abc for the hyper-parameters, iterations); a list of triples, one per iteration, goes to the handle."""
+        if len(abc) == 3 and not hasattr(abc[0], "__len__"):
+            if self.mode == "half":
+                B.muon_set_coefficients(self.handle, ())
+            return abc, 5 if ns_steps is None else ns_steps
+        if self.mode != "half":
+            raise ValueError("coefficients per iteration need mode='half'")
+        if any(len(t) != 3 for t in abc) or (ns_steps is not None and ns_steps != len(abc)):
+            raise ValueError("abc must be one (a, b, c), or one for each of the ns_steps iterations")
+        B.muon_set_coefficients(self.handle, abc)
+        return QUINTIC, len(abc)
+
+    def _momentum_state(self, state):
+        if state.shapes != self.shapes or state.device != self.device:
+            raise ValueError(f"state: shapes {state.shapes} on {state.device} do not match {self.shapes} on {self.device}")
+        return state._states()
 
     def __call__(self, W, G, M, lr=0.02, beta=0.95, weight_decay=0.0, eps=1e-7, abc=QUINTIC, nesterov=True,
-                 ns_steps=5, stream=None):
-        hp = B.make_hparams(lr, beta, weight_decay, eps, abc, nesterov, ns_steps)
+                 ns_steps=None, stream=None, seed=None):
+        """One step: W and M updated in place.
+
+        M is a list of tensors, or a QuantizedState (mode "half"; `seed` then makes its rounding stochastic, and
+        W and G may be strided: G stored by rows, W by rows or by columns).  abc is one coefficient triple for
+        ns_steps iterations (5 by default) or, in mode "half", a list with one for each iteration.
+        """
+        quantized = isinstance(M, QuantizedState)
+        if seed is not None and not quantized:
+            raise ValueError("seed is for a QuantizedState")
+        if quantized and self.mode != "half":
+            raise ValueError("a QuantizedState needs mode='half'")
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if quantized:
+            states = self._momentum_state(M)
+            w = _views(W, self._entries, self.device, "W", self.dtype)
+            g = _views(G, self._entries, self.device, "G", self.dtype, by_rows=True)
+            abc, ns_steps = self._coefficients(abc, ns_steps)
+            hp = B.make_hparams(lr, beta, weight_decay, eps, abc, nesterov, ns_steps)
+            B.muon_step_state(self.handle, w, g, states, len(self.shapes), M._fmt, hp, seed, s.cuda_stream)
+            return
+        abc, ns_steps = self._coefficients(abc, ns_steps)
+        hp = B.make_hparams(lr, beta, weight_decay, eps, abc, nesterov, ns_steps)
         B.muon_step(self.handle, self._check(W, "W"), self._check(G, "G"), self._check(M, "M"), hp, s.cuda_stream)
 
     def step_from_host(self, W, G_host, M, stream=None, **hp):
@@ -107,15 +258,43 @@ class MuonStep:
         """The side stream step_from_host copies on (created by its first call)."""
         return getattr(self, "_copy_stream", None)
 
-    def orthogonalize(self, X, O, eps=1e-7, abc=QUINTIC, ns_steps=5, stream=None):
-        hp = B.make_hparams(0.0, 0.0, 0.0, eps, abc, False, ns_steps)
+    def momentum(self, G, state, U, beta=0.95, nesterov=True, seed=None, norms=None, stream=None) -> torch.Tensor:
+        """The momentum of a step on a QuantizedState, by itself: the state updated in place, the blended direction
+        in U, its Frobenius norms (one a matrix, fp32) returned.  G and U: the handle's dtype, stored by rows; U may be G."""
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        hp = B.make_hparams(0.0, beta, 0.0, 0.0, QUINTIC, nesterov, 0)
+        g = _views(G, self._entries, self.device, "G", self.dtype, by_rows=True)
+        u = _views(U, self._entries, self.device, "U", self.dtype, by_rows=True)
+        B.muon_momentum_state(self.handle, g, self._momentum_state(state), u, len(self.shapes), state._fmt, hp, seed,
+                              s.cuda_stream)
+        return self.norms(norms, stream=s)
+
+    def orthogonalize(self, X, O, eps=1e-7, abc=QUINTIC, ns_steps=None, stream=None):
+        """O = the orthogonalised X, nothing else.
+
+        In mode "half" X and O may be views stored by rows or by columns (slices, stacks, transposed tensors) of
+        bf16, fp16 or fp32, O may be X itself, and abc may be a list with one coefficient triple per iteration.
+        """
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        if self.mode == "half":
+            x = _views(X, self._entries, self.device, "X")
+            o = _views(O, self._entries, self.device, "O")
+            abc, ns_steps = self._coefficients(abc, ns_steps)
+            hp = B.make_hparams(0.0, 0.0, 0.0, eps, abc, False, ns_steps)
+            B.muon_orthogonalize_views(self.handle, x, o, len(self.shapes), hp, s.cuda_stream)
+            return
+        abc, ns_steps = self._coefficients(abc, ns_steps)
+        hp = B.make_hparams(0.0, 0.0, 0.0, eps, abc, False, ns_steps)
         B.muon_orthogonalize(self.handle, self._check(X, "X"), self._check(O, "O"), hp, s.cuda_stream)
 
     def norms(self, out=None, stream=None) -> torch.Tensor:
         """||U_i||_F of the last step, fp32, enqueued as one copy into `out` (device or pinned host)."""
         if out is None:
-            out = torch.empty(len(self.shapes), dtype=torch.float32, device=self.device)
+            if stream is None:
+                out = torch.empty(self._n, dtype=torch.float32, device=self.device)
+            else:  # memory of the stream that writes it
+                with torch.cuda.stream(stream):
+                    out = torch.empty(self._n, dtype=torch.float32, device=self.device)
         s = stream if stream is not None else torch.cuda.current_stream(self.device)
         B.muon_get_norms(self.handle, out.data_ptr(), s.cuda_stream)
         return out
