@@ -87,9 +87,8 @@ typedef enum { MUON_BF16 = 0, MUON_FP32 = 1, MUON_FP16 = 2 } muon_dtype_t;
  *           the CUDA cores (no TF32): a slow, accurate mode for checking.
  * HALF:     the products of FAST with fp16 operands: three more significant bits at the
  *           same tensor-core rate, an error about eight times smaller (2e-3 instead of 1-2e-2
- *           after five quintic iterations).  X, A and B' are stored times powers of two
- *           (2^12, 2^12, 2^8), so iterations whose singular values stay below 4 and whose
- *           polynomials stay below 255 are in range (the usual ones stay below 1.3 and 10);
+ *           after five quintic iterations).  X and A are stored times 2^12, so iterations
+ *           whose singular values stay below 4 are in range (the usual ones stay below 1.3);
  *           beyond that a matrix comes out not finite.  X is normalised before it
  *           is rounded, so the inputs' size does not matter down to norms of about 1e-4 eps.
  *           Matrices of at most 128 rows (or columns) and 4096 columns (rows) run every

@@ -238,11 +238,11 @@ cudaError_t launch_ns_small(const SmallParams& p, int num_sms, cudaStream_t s);
 // The iteration's operands are stored in fp16 (11 significant bits, three more than bf16) times
 // powers of two, folded into the epilogues' coefficients, that keep what matters in fp16's normal
 // range: after Frobenius normalisation a typical entry of X is 1/sqrt(mn) and of A 1/(m sqrt(n)),
-// down to 2^-20, while no entry of X or A exceeds the largest singular value (squared) and none of
-// B' exceeds |a| + |b| s^2 + |c| s^4.  Singular values up to 4 and polynomials up to 255 fit.
+// down to 2^-20, while no entry of X or A exceeds the largest singular value (squared).  Singular
+// values up to 4 fit.
 constexpr float kHalfX = 4096.0f;  // stored X  = 2^12 X
 constexpr float kHalfA = 4096.0f;  // stored A  = 2^12 A
-constexpr float kHalfB = 256.0f;   // stored B' = 2^8 B'
+constexpr float kHalfB = 1.0f;     // B' as it is: its diagonal is of the order of a
 
 // Storage types of a view (MUON_BF16, MUON_FP32, MUON_FP16).
 enum ViewType : int { kViewBF16 = 0, kViewF32 = 1, kViewF16 = 2 };
@@ -290,8 +290,8 @@ cudaError_t launch_view_write(const ViewParams& p, cudaStream_t s);
 
 // Matrices of few rows: every iteration on chip, one cluster per 128-row tile (k_ns_skinny.cu).
 constexpr int kSkinnyRows = 128;       // most rows (of the oriented matrix)
-constexpr int kSkinnyColsOne = 768;    // most columns one CTA holds by itself
-constexpr int kSkinnyColsPart = 512;   // most columns of each CTA of a cluster
+constexpr int kSkinnyColsOne = 768;    // most columns of one CTA, or of each of two
+constexpr int kSkinnyColsPart = 512;   // most columns of each CTA of a larger cluster
 constexpr int kSkinnyCluster = 8;      // most CTAs of a cluster
 constexpr int kSkinnySegs = 64;
 constexpr int kMaxSteps = 64;
@@ -301,7 +301,7 @@ struct SkinnyParams {
   int nseg;
   int total;                 // matrices
   int m, n;
-  int slot_rows;             // rows of the tile each matrix takes: a power of two >= m
+  int slot_rows;             // rows of the tile each matrix takes: a power of two >= m, 8 at least
   int slots;                 // matrices in a tile
   int cluster;               // CTAs of a tile
   int width;                 // columns each CTA holds, a multiple of 64

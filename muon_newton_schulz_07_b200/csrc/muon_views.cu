@@ -278,12 +278,11 @@ cudaError_t enqueue_tiles(muon_ctx* h, const std::vector<Item>& items, const muo
 void skinny_layout(const GroupPlan& gp, int cnt, int num_sms, SkinnyParams* p) {
   p->m = gp.m;
   p->n = gp.n;
-  p->slot_rows = 1;
+  p->slot_rows = 8;
   while (p->slot_rows < gp.m) p->slot_rows *= 2;
   const int most = kSkinnyRows / p->slot_rows;
   p->cluster = 1;
-  if (gp.n > kSkinnyColsOne)
-    for (p->cluster = 2; gp.n > p->cluster * kSkinnyColsPart;) p->cluster *= 2;
+  while (gp.n > p->cluster * (p->cluster <= 2 ? kSkinnyColsOne : kSkinnyColsPart)) p->cluster *= 2;
   // one matrix a tile while there are SMs for it, then as many as fit
   const int room = std::max(1, num_sms / p->cluster);
   p->slots = std::min(most, (cnt + room - 1) / room);
