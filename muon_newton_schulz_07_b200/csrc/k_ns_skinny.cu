@@ -17,21 +17,24 @@
 //
 // Shared memory: X as w / 64 chunks of 128 rows x 64 columns (16 KB, 128-byte swizzle).  One layout
 // serves both products: read along k = n it is the K-major operand of the Gram product, read along
-// k = m the MN-major second operand of the update.  Then A, replaced by B' (32 KB, K-major).  The
-// fp32 shares of A that the CTAs of a cluster hold are added in a fixed order through
-// distributed shared memory: for C = 2 each CTA receives the other's share of its 64 rows in the
-// place of A (which nothing reads then), for C > 2 in 64 KB of its own.
-// TMEM (512 columns): A | A A | two 128-column buffers of the update.
+// k = m the MN-major second operand of the update.  Then A (32 KB, K-major).  The fp32 shares of A
+// that the CTAs of a cluster hold are added by rows: each CTA sends the owner of a row its share
+// (st.async, counted by a barrier of the owner), the owner adds the shares in a fixed order, rounds
+// once, and copies its rows of A to the others.  The shares arrive in 64 KB of their own or, for
+// C = 2, in the place of A, which nothing reads then: that leaves room for 768 columns a CTA.
+// TMEM (512 columns): A | two 128-column buffers of the update, the odd one also A A | B'.  B' and the
+// freshly updated blocks of X are first operands from TMEM: with both operands in shared memory, a
+// 128 x 128 MMA reads its full 128 bytes a cycle and leaves none to the epilogue.
 //
-// Warp 8 issues the MMAs, warps 0..7 do the rest.  The update runs in blocks of 128 columns, in
+// Warp 16 issues the MMAs, warps 0..15 do the rest.  The update runs in blocks of 128 columns, in
 // place (a block reads no other block's columns): while the warps turn block b into the new X, the tensor
 // core computes block b + 1, and block b enters the next iteration's Gram product as soon as it
 // is stored.  So an iteration costs its MMAs (2 x 128 x 128 x w) plus the A -> B' chain.
 //
 // Rounding: X, A and B' are fp16 (2^-11), products and sums fp32.  B' is dominated by its
-// diagonal, where one rounding shifts a whole row of the update the same way; that remainder is kept in fp32 and
-// added in the update's epilogue, which costs a read of the old X and an FMA a value and takes a
-// third off the error of the result (64 x 768, five quintic iterations: 1.9e-3 -> 1.2e-3).
+// diagonal, where one rounding scales a whole row of the update; the update's epilogue multiplies
+// the row by the exact diagonal entry over the rounded one, which takes a third off the error
+// of the result (64 x 768, five quintic iterations: 1.9e-3 -> 1.2e-3).
 //
 // All waits are bounded; a CTA whose wait runs out records the timeout, stops its work, and still
 // takes every barrier of the schedule.
@@ -43,7 +46,7 @@
 namespace muon {
 namespace {
 
-constexpr int EPI_WARPS = 8;                 // two per TMEM lane quadrant
+constexpr int EPI_WARPS = 16;                // four per TMEM lane quadrant
 constexpr int EPI = 32 * EPI_WARPS;
 constexpr int THREADS = EPI + 32;            // and the MMA issuer
 constexpr uint32_t CHUNK = 16384;            // 128 rows x 64 columns of fp16
@@ -52,7 +55,7 @@ constexpr uint32_t PART_BYTES = 128 * 128 * 4;
 constexpr uint32_t MISC_BYTES = 1024;
 constexpr size_t SMEM_LIMIT = 232448;
 constexpr size_t SMEM_ONE = 120 * 1024;      // at least this much, so that an SM holds one CTA
-constexpr uint32_t T_A = 0, T_AA = 128, T_UPD = 256;  // TMEM columns
+constexpr uint32_t T_A = 0, T_UPD = 128, T_AA = 256, T_B = 384;  // TMEM columns (A A: the odd update buffer)
 
 __host__ __device__ constexpr size_t smem_bytes(int width, int cluster) {
   const size_t need = 1024 + static_cast<size_t>(width / 64) * CHUNK + ABUF_BYTES +
@@ -75,16 +78,19 @@ __device__ __forceinline__ uint4 pack8h(const float* v) {
 __device__ __forceinline__ uint32_t group_at(int r, int u) {
   return static_cast<uint32_t>(u >> 3) * CHUNK + r * 128 + (((u & 7) ^ (r & 7)) << 4);
 }
-// Place of a 16-byte group (4 columns) of fp32 row r in a 128-column share of A.
-__device__ __forceinline__ uint32_t share_at(int r, int q) { return (r * 32 + (q ^ (r & 7))) * 16; }
 
-__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
+
+// 16 bytes into another CTA's shared memory, counted by a barrier of that CTA.
+__device__ __forceinline__ void st_async_v4(uint32_t addr, uint32_t bar, float a, float b, float c, float d) {
+  asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(addr),
+               "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
                : "memory");
-  return v;
+}
+// A piece of this CTA's shared memory into another CTA's, counted by a barrier of that CTA.
+__device__ __forceinline__ void copy_to_cta(uint32_t dst, uint32_t src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "r"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   float v;
@@ -123,10 +129,11 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   uint64_t* bars = reinterpret_cast<uint64_t*>(misc);
   const uint32_t bar0 = smem_u32(bars);
   const uint32_t a_full = bar0, a_ready = bar0 + 8, aa_full = bar0 + 16, b_ready = bar0 + 24, upd_full = bar0 + 32,
-                 upd_done = bar0 + 48;  // upd_full, upd_done: two each, for even and odd blocks
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 64);
+                 upd_done = bar0 + 48,  // upd_full, upd_done: two each, for even and odd blocks
+      share_full = bar0 + 64, rows_full = bar0 + 72, peer_free = bar0 + 80, peer_read = bar0 + 88, peer_got = bar0 + 96;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 112);
   volatile uint8_t* poison = misc + 128;                               // per matrix of the tile
-  volatile float* remainder = reinterpret_cast<float*>(misc + 256);    // of each row's diagonal entry of B'
+  volatile float* row_factor = reinterpret_cast<float*>(misc + 256);   // of each row of the update
   const uint32_t xaddr = smem_u32(xbuf), aaddr = smem_u32(abuf), saddr = smem_u32(share);
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -161,11 +168,16 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     mbar_init(upd_full + 8, 1);
     mbar_init(upd_done, EPI_WARPS);
     mbar_init(upd_done + 8, EPI_WARPS);
+    mbar_init(share_full, 1);
+    mbar_init(rows_full, 1);
+    mbar_init(peer_free, 1);
+    mbar_init(peer_read, 1);
+    mbar_init(peer_got, C > 1 ? C - 1 : 1);
     fence_barrier_init();
   }
   if (tid < 128) {
     poison[tid] = 0;
-    remainder[tid] = 0.0f;
+    row_factor[tid] = 1.0f;
   }
   if (warp == EPI_WARPS) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -187,11 +199,11 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     e = first_mat + slot_l - p.seg[seg].mat_begin;
   }
   const ViewSeg& sg = p.seg[seg];
-  const int u0 = ((tid >> 7) << 3) + (tid & 7);  // first group of this thread, then every 16th
+  const int u0 = ((tid >> 7) << 3) + (tid & 7);  // first group of this thread, then every 32nd
   const bool wide_src = sg.src_type == kViewF32;
-  float* part = reinterpret_cast<float*>(abuf);  // [2][16] sums of squares; A is not there yet
-  float* total = part + 32;                      // [16]
-  float2* factor = reinterpret_cast<float2*>(total + 16);  // [16] by slot
+  float* part = reinterpret_cast<float*>(abuf);  // [4][16] sums of squares; A is not there yet
+  float* total = part + 64;                      // [16]
+  float* factor = total + 16;                    // [16] by matrix of the tile
   // the storage rows of block (ig, u): address of the first, distance, how many, values in each
   struct Block { long long at; long long ld; int rows, have; };
   auto block_of = [&](int u, bool tr, long long ld, long long bs) {
@@ -204,23 +216,26 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     if (e < 0 || b.have <= 0) b.rows = 0;
     return b;
   };
-  auto load_f32 = [&](const Block& b, float (&v)[8][8]) {
+  auto load_f32 = [&](const Block& b, int k0, float (&v)[4][8]) {  // four storage rows
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      load_eight(sg.src, kViewF32, b.at + k * b.ld, k < b.rows ? b.have : 0, sg.src_vec != 0, v[k]);
+    for (int k = 0; k < 4; ++k)
+      load_eight(sg.src, kViewF32, b.at + (k0 + k) * b.ld, k0 + k < b.rows ? b.have : 0, sg.src_vec != 0, v[k]);
   };
   if (warp < EPI_WARPS) {
     float ss = 0.0f;
 #pragma unroll 1
-    for (int u = u0; u < groups; u += 16) {
+    for (int u = u0; u < groups; u += EPI / 16) {
       const Block b = block_of(u, sg.src_tr != 0, sg.src_ld, sg.src_bs);
       if (wide_src) {
-        float v[8][8];
-        load_f32(b, v);
+#pragma unroll 1
+        for (int k0 = 0; k0 < 8; k0 += 4) {
+          float v[4][8];
+          load_f32(b, k0, v);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < 4; ++k)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+            for (int i = 0; i < 8; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+        }
       } else {
         uint4 q[8];
         const uint16_t* src = static_cast<const uint16_t*>(sg.src) + b.at;
@@ -261,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   if (tid < 16) {
     float t = 0.0f;
     for (int c = 0; c < C; ++c)
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < EPI / 128; ++h)
         t += C > 1 ? ld_cluster_f32(map_to_rank(smem_u32(part + h * 16 + tid), c)) : part[h * 16 + tid];
     total[tid] = t;
   }
@@ -271,10 +286,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     float t = 0.0f;
     for (int i = 0; i * 8 < p.slot_rows; ++i) t += total[(tid >> 3) + i];
     const float norm = sqrtf(t);
-    const Normaliser nz = normaliser(norm, p.eps);
-    const bool fine = isfinite(norm);
-    if (!fine) poison[slot] = 1;
-    factor[slot] = make_float2(nz.pre, fine ? nz.mul : 0.0f);
+    if (!isfinite(norm)) poison[slot] = 1;
+    factor[slot] = normaliser(norm, p.eps);
     if (first_mat + slot < p.total && rank == 0) {
       int s = 0;
       while (s + 1 < p.nseg && p.seg[s + 1].mat_begin <= first_mat + slot) ++s;
@@ -284,18 +297,22 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   __syncthreads();
   if (warp < EPI_WARPS) {
     const bool out = slot_l >= p.slots || poison[slot_l] != 0;
-    const float2 f = out ? make_float2(0.0f, 0.0f) : factor[slot_l];
+    const float f = out ? 0.0f : factor[slot_l];
 #pragma unroll 1
-    for (int u = u0; u < groups; u += 16) {
+    for (int u = u0; u < groups; u += EPI / 16) {
       uint4 q[8];
       if (wide_src) {
-        float v[8][8];
-        load_f32(block_of(u, sg.src_tr != 0, sg.src_ld, sg.src_bs), v);
+        const Block b = block_of(u, sg.src_tr != 0, sg.src_ld, sg.src_bs);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k0 = 0; k0 < 8; k0 += 4) {
+          float v[4][8];
+          load_f32(b, k0, v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[k][i] = out ? 0.0f : v[k][i] * f.x * f.y;
-          q[k] = pack8h(v[k]);
+          for (int k = 0; k < 4; ++k) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[k][i] *= f;
+            q[k0 + k] = pack8h(v[k]);
+          }
         }
         if (sg.src_tr) transpose8(q);
       } else {
@@ -304,276 +321,281 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
           float v[8];
           widen8(*reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u)), sg.src_type, v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = out ? 0.0f : v[i] * f.x * f.y;
+          for (int i = 0; i < 8; ++i) v[i] *= f;
           q[k] = pack8h(v);
         }
+      }
+      if (out) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = make_uint4(0, 0, 0, 0);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = q[k];
     }
   }
-  sync_all();  // the sums and factors have been read, here and by the whole cluster
-  for (uint32_t i = tid * 16; i < ABUF_BYTES; i += THREADS * 16)
-    *reinterpret_cast<uint4*>(abuf + i) = make_uint4(0, 0, 0, 0);
   fence_async_smem();
-  sync_all();
+  sync_all();  // (and the sums and factors have been read, here and by the whole cluster)
 
   if (warp == EPI_WARPS) {
     // -------------------------------------------------------------- MMA issuer
-    const uint32_t idesc_sym = idesc_f16_f32(true, 128, used16, 0, 0);
-    const int ksteps = used16 / 16;
-    auto gram_block = [&](int b) {
-      for (int c = 2 * b; c < min(nch, 2 * b + 2); ++c) {
-        const uint64_t d = smem_desc_sw128(xaddr + c * CHUNK, 16, 1024);
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          tc_mma_bf16(tmem + T_A, d + ((32u * j) >> 4), d + ((32u * j) >> 4), idesc_sym, (c | j) != 0 ? 1u : 0u);
-      }
-    };
-    auto update_block = [&](int b) {
-      const uint32_t idesc = idesc_f16_f32(true, 128, min(128, p.width - b * 128), 0, 1);
-      const uint32_t d = tmem + T_UPD + (b & 1) * 128;
-      for (int j = 0; j < ksteps; ++j) {
-        const uint64_t ad = smem_desc_sw128(aaddr + (j >> 2) * CHUNK + (j & 3) * 32, 16, 1024);
-        const uint64_t bd = smem_desc_sw128(xaddr + b * 2 * CHUNK + j * 2048, CHUNK, 1024);
-        tc_mma_bf16(d, ad, bd, idesc, j != 0 ? 1u : 0u);
-      }
-      tc_commit(upd_full + 8 * (b & 1));
-    };
-    uint32_t done[2] = {0, 0};  // phases of upd_done
-    if (lane == 0 && p.k > 0) {
-      for (int b = 0; b < nblk; ++b) gram_block(b);
-      tc_commit(a_full);
-    }
+    if (lane == 0) {
+      const uint32_t idesc_sym = idesc_f16_f32(true, 128, used16, 0, 0);
+      const uint32_t idesc_128 = idesc_f16_f32(true, 128, 128, 0, 1), idesc_64 = idesc_f16_f32(true, 128, 64, 0, 1);
+      const uint64_t x_rows = smem_desc_sw128(xaddr, 16, 1024);     // X, K-major: 16 columns are 32 bytes
+      const uint64_t x_cols = smem_desc_sw128(xaddr, CHUNK, 1024);  // X, MN-major: 16 rows are 2 KB
+      const uint64_t a_rows = smem_desc_sw128(aaddr, 16, 1024);
+      constexpr uint64_t BLOCK = 2 * CHUNK >> 4;                    // 128 columns, in descriptor units
+      auto wait_one = [&](uint32_t bar, uint32_t par) {
+        if (ok) ok = mbar_wait_bounded(bar, par, tmo, nullptr, p.status);
+        tc_fence_after();
+      };
+      // MMAs go out four at a time (64 columns, or 64 rows of X), each descriptor the first one's plus a
+      // constant: what is computed between two MMAs adds to their time.  Rows beyond the tile's
+      // matrices are zero in X and B', so rounding their number up to 64 changes nothing.
+      // Block b's share of A: the first time from shared memory on both sides, later with the first
+      // operand where the update's epilogue left it in TMEM, 16 columns of X in 8 of 32 bits.
+      auto gram_first = [&](int b) {
 #pragma unroll 1
-    for (int it = 0; it < p.k; ++it) {
-      __syncwarp();
-      if (C > 1) {
-        for (int i = 0; i < (C == 2 ? 4 : 2); ++i) cluster_arrive_wait();
-      }
-      wait_on(a_ready, it & 1);
-      if (lane == 0 && ok) {
-        for (int j = 0; j < ksteps; ++j) {
-          const uint64_t d = smem_desc_sw128(aaddr + (j >> 2) * CHUNK + (j & 3) * 32, 16, 1024);
-          tc_mma_bf16(tmem + T_AA, d, d, idesc_sym, j != 0 ? 1u : 0u);
+        for (int c = 2 * b; c < min(nch, 2 * b + 2); ++c) {
+          const uint64_t d = x_rows + (CHUNK >> 4) * static_cast<uint64_t>(c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tc_mma_bf16(tmem + T_A, d + 2 * j, d + 2 * j, idesc_sym, (c | j) != 0 ? 1u : 0u);
         }
-        tc_commit(aa_full);
+      };
+      auto gram_next = [&](int b) {
+#pragma unroll 1
+        for (int c = 2 * b; c < min(nch, 2 * b + 2); ++c) {
+          const uint64_t d = x_rows + (CHUNK >> 4) * static_cast<uint64_t>(c);
+          const uint32_t t = tmem + T_UPD + (c & 3) * 64;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tc_mma_tmem_a(tmem + T_A, t + (j >> 1) * 32 + (j & 1) * 8, d + 2 * j, idesc_sym, (c | j) != 0 ? 1u : 0u);
+        }
+      };
+      auto update_block = [&](int b) {
+        const uint64_t d = x_cols + BLOCK * b;
+        const uint32_t t = tmem + T_UPD + (b & 1) * 128, idesc = 2 * b + 1 < nch ? idesc_128 : idesc_64;
+#pragma unroll 1
+        for (int g = 0; g < used; g += 64) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tc_mma_tmem_a(t, tmem + T_B + g / 2 + j * 8, d + 8 * g + j * 128, idesc, (g | j) != 0 ? 1u : 0u);
+        }
+        tc_commit(upd_full + 8 * (b & 1));
+      };
+      uint32_t done = 0;  // parities of upd_done, a bit each
+      if (p.k > 0) {
+#pragma unroll 1
+        for (int b = 0; b < nblk; ++b) gram_first(b);
+        tc_commit(a_full);
       }
-      __syncwarp();
-      wait_on(b_ready, it & 1);
-      if (lane == 0 && ok) {
-        update_block(0);
-        if (nblk > 1) update_block(1);
-      }
-      __syncwarp();
-      for (int b = 0; b < nblk; ++b) {
-        // block b is the new X and its TMEM columns are free.  (A barrier each for even and odd
-        // blocks: the warps may finish block b + 1 before this wait, but not b + 2.)
-        wait_on(upd_done + 8 * (b & 1), done[b & 1] & 1);
-        ++done[b & 1];
-        if (lane == 0 && ok) {
-          if (b + 2 < nblk) update_block(b + 2);
-          if (it + 1 < p.k) {
-            gram_block(b);
+#pragma unroll 1
+      for (int it = 0; it < p.k; ++it) {
+        wait_one(a_ready, it & 1);
+        if (ok) {
+#pragma unroll 1
+          for (int g = 0; g < used; g += 64) {
+            const uint64_t d = a_rows + (CHUNK >> 4) * static_cast<uint64_t>(g >> 6);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tc_mma_bf16(tmem + T_AA, d + 2 * j, d + 2 * j, idesc_sym, (g | j) != 0 ? 1u : 0u);
+          }
+          tc_commit(aa_full);
+        }
+        wait_one(b_ready, it & 1);
+        if (ok) {
+          update_block(0);
+          if (nblk > 1) update_block(1);
+        }
+#pragma unroll 1
+        for (int b = 0; b < nblk; ++b) {
+          // block b is the new X.  (A barrier each for even and odd blocks: the warps may finish
+          // block b + 1 before this wait, but not b + 2.)
+          wait_one(upd_done + 8 * (b & 1), (done >> (b & 1)) & 1);
+          done ^= 1u << (b & 1);
+          if (ok && it + 1 < p.k) {
+            gram_next(b);  // before the update that takes the same TMEM columns
             if (b + 1 == nblk) tc_commit(a_full);
           }
+          if (ok && b + 2 < nblk) update_block(b + 2);
         }
-        __syncwarp();
       }
     }
   } else {
     // -------------------------------------------------------------- the other warps
-    const int quad = warp & 3, half = warp >> 2;
+    const int quad = warp & 3, part4 = warp >> 2;
     const int r = quad * 32 + lane;                       // this thread's row of the tile
+    const int ca0 = part4 * 32;                           // its columns of A, and of a block of the update
     const bool active = quad * 32 < used;                 // rows that hold a matrix (warp-uniform)
     const int slot = r < used ? r >> lh : -1;             // -1: no matrix, the row stays 0
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    const int ca0 = half * 64;                            // this thread's columns of A
-    uint32_t uses[2] = {0, 0};                            // phases of upd_full
+    uint32_t uses = 0;                                    // parities of upd_full, a bit each
+    uint32_t own = 0;                                     // columns ca0 + i of the row's own matrix, a bit each
+    for (int i = 0; i < 32; ++i) own |= static_cast<uint32_t>(((ca0 + i) >> lh) == slot) << i;
     constexpr float kGram = kHalfA / (kHalfX * kHalfX);
-    // columns ca0 + c .. + 31 of this row's A: scaled, outside the row's own matrix 0, as fp16
-    auto pack_a = [&](int c, float (&v)[32], uint4 (&q)[4]) {
+    // keep the row's own matrix; of 32 rows and more, rows are all in or all out
+    auto masked = [&](float (&v)[32]) {
+      if (own == 0xffffffffu) return;
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = ((ca0 + c + i) >> lh) == slot ? v[i] * kGram : 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = pack8h(v + 8 * i);
+      for (int i = 0; i < 32; ++i) v[i] = (own >> i) & 1u ? v[i] : 0.0f;
+    };
+    const int rows_c = 128 / C;                           // rows of A that each CTA of the cluster adds up
+    const int owner = r / rows_c, in_slice = r & (rows_c - 1);
+    // the place of 16 bytes of a share of A in its owner's memory: neighbouring rows side by side
+    const uint32_t share_base = C == 2 ? aaddr : saddr;
+    auto share_at = [&](int from, int q) {
+      return static_cast<uint32_t>((C == 2 ? 0 : from * rows_c * 32) + q * rows_c + in_slice) * 16;
     };
 #pragma unroll 1
     for (int it = 0; it < p.k; ++it) {
+      const uint32_t par = it & 1;
       // ------------------------------------------------------------ A
-      wait_on(a_full, it & 1);
-      if (C == 1) {
-        if (ok && active) {
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            float v[32];
-            uint4 q[4];
-            tmem_ld_32cols(t_row + T_A + ca0 + c, v);
-            pack_a(c, v, q);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(abuf + group_at(r, ((ca0 + c) >> 3) + i)) = q[i];
+      wait_on(a_full, par);
+      uint4 h[4];
+      {
+        float v[32];
+        if (ok && (active || C > 1)) tmem_ld_32cols(t_row + T_A + ca0, v);
+        if (C > 1) {
+          // Each CTA sends every owner its share of the owner's rows; the owner adds its own and the
+          // others' in a fixed order, rounds once, and copies its rows of A to the others.
+          if (tid == 0 && ok) {
+            mbar_arrive_expect_tx(share_full, (C - 1) * rows_c * 512);
+            mbar_arrive_expect_tx(rows_full, (C - 1) * rows_c * 256);
           }
-        }
-        fence_async_smem();
-      } else if (C == 2) {
-        // rank 0 adds up rows 0..63, rank 1 rows 64..127
-        const bool mine = (quad >> 1) == rank;
-        const uint32_t peer = static_cast<uint32_t>(rank ^ 1);
-        uint4 q[8];
-        tc_fence_before();
-        cluster_arrive_wait();  // neither tensor core reads A any more
-        tc_fence_after();
-#pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float v[32];
-          if (!mine && ok) {
-            tmem_ld_32cols(t_row + T_A + ca0 + c, v);
+          __syncwarp();
+          if (C == 2 && it > 0) wait_on(peer_free, par ^ 1);
+          if (ok && owner != rank) {
+            const uint32_t bar = map_to_rank(share_full, owner);
+            const uint32_t to = map_to_rank(share_base + share_at(rank, ca0 >> 2), owner);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              st_cluster_v4(map_to_rank(aaddr + share_at(r & 63, ((ca0 + c) >> 2) + i), peer),
-                            make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                       __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+              st_async_v4(to + i * rows_c * 16, bar, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
           }
-        }
-        tc_fence_before();
-        cluster_arrive_wait();  // the shares have arrived
-        tc_fence_after();
-        if (mine && ok) {
+          __syncwarp();
+          wait_on(share_full, par);
+          if (ok && owner == rank) {
+            for (int c = 0; c < C; ++c) {
+              if (c == rank) continue;
+              const uint8_t* sh = (C == 2 ? abuf : share) + share_at(c, ca0 >> 2);
 #pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            float v[32];
-            uint4 h[4];
-            tmem_ld_32cols(t_row + T_A + ca0 + c, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float4 t = *reinterpret_cast<const float4*>(abuf + share_at(r & 63, ((ca0 + c) >> 2) + i));
-              v[4 * i] += t.x; v[4 * i + 1] += t.y; v[4 * i + 2] += t.z; v[4 * i + 3] += t.w;
-            }
-            pack_a(c, v, h);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) q[(c >> 3) + i] = h[i];
-          }
-        }
-        cluster_arrive_wait();  // and been read
-        if (mine && ok) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const uint32_t at = group_at(r, (ca0 >> 3) + i);
-            *reinterpret_cast<uint4*>(abuf + at) = q[i];
-            st_cluster_v4(map_to_rank(aaddr + at, peer), q[i]);
-          }
-        }
-        fence_async_all();
-        tc_fence_before();
-        cluster_arrive_wait();
-      } else {
-        if (ok) {
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            float v[32];
-            tmem_ld_32cols(t_row + T_A + ca0 + c, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              *reinterpret_cast<float4*>(share + share_at(r, ((ca0 + c) >> 2) + i)) =
-                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          }
-        }
-        tc_fence_before();
-        cluster_arrive_wait();
-        // rows 128 rank / C .. of A: the shares of every CTA, in order, then one rounding
-        const int rows = 128 / C;
-        for (int idx = tid; idx < rows * 16; idx += EPI) {
-          const int rr = rank * rows + (idx >> 4), u = idx & 15;
-          float s[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = 0.0f;
-          for (int c = 0; c < C; ++c) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float4 t = ld_cluster_v4(map_to_rank(saddr + share_at(rr, u * 2 + h), c));
-              s[4 * h] += t.x; s[4 * h + 1] += t.y; s[4 * h + 2] += t.z; s[4 * h + 3] += t.w;
+              for (int i = 0; i < 8; ++i) {
+                const float4 t = *reinterpret_cast<const float4*>(sh + i * rows_c * 16);
+                v[4 * i] += t.x; v[4 * i + 1] += t.y; v[4 * i + 2] += t.z; v[4 * i + 3] += t.w;
+              }
             }
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s[i] = ((u * 8 + i) >> lh) == (rr >> lh) ? s[i] * kGram : 0.0f;
-          const uint4 h = pack8h(s);
-          for (int c = 0; c < C; ++c) st_cluster_v4(map_to_rank(aaddr + group_at(rr, u), c), h);
+          if (C == 2) {
+            epi_sync();  // the share has been read: its place takes A
+            if (tid == 0 && ok) mbar_arrive_remote(map_to_rank(peer_read, rank ^ 1));
+          }
         }
-        fence_async_all();
-        tc_fence_before();
-        cluster_arrive_wait();
-        fence_async_smem();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= kGram;
+        masked(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = pack8h(v + 8 * i);
+      }
+      if (ok && (C == 1 ? active : owner == rank)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(abuf + group_at(r, (ca0 >> 3) + i)) = h[i];
+      }
+      fence_async_smem();
+      if (C > 1) {
+        epi_sync();
+        if (warp == 0) {
+          if (C == 2) wait_on(peer_read, par);
+          if (lane < C && lane != rank && ok) {
+            for (int c = 0; c < 2; ++c) {
+              const uint32_t at = aaddr + c * CHUNK + rank * rows_c * 128;
+              copy_to_cta(map_to_rank(at, lane), at, rows_c * 128, map_to_rank(rows_full, lane));
+            }
+          }
+          __syncwarp();
+        }
+        wait_on(rows_full, par);
+        if (tid < C && tid != rank && ok) mbar_arrive_remote(map_to_rank(peer_got, tid));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(a_ready);
-      epi_sync();
-      if (tid < 128) {  // a row of X that left fp16's range shows on the diagonal of A
-        const __half d = *reinterpret_cast<const __half*>(abuf + group_at(tid, tid >> 3) + (tid & 7) * 2);
-        if (tid < used && (__hisinf(d) || __hisnan(d))) poison[tid >> lh] = 1;
+      if (C > 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const uint4*>(abuf + group_at(r, (ca0 >> 3) + i));
+      }
+      if (part4 == quad && slot >= 0) {  // a row of X that left fp16's range shows on the diagonal of A
+        const unsigned short d =
+            *reinterpret_cast<const unsigned short*>(abuf + group_at(r, r >> 3) + (r & 7) * 2);
+        if ((d & 0x7C00) == 0x7C00) poison[slot] = 1;
       }
       // ------------------------------------------------------------ B' = a I + b A + c A A
-      wait_on(aa_full, it & 1);
+      const float ca = p.coef[it][0], cb = p.coef[it][1] * (1.0f / kHalfA),
+                  cc = p.coef[it][2] * (1.0f / (kHalfA * kHalfA));
+      wait_on(aa_full, par);
+      if (C > 1) wait_on(peer_got, par);  // the rows of A that this CTA copied have been read
       epi_sync();
+      if (C == 2 && tid == 0 && ok) mbar_arrive_remote(map_to_rank(peer_free, rank ^ 1));  // A has been read
       if (ok && active) {
-        const bool out = slot < 0 || poison[slot] != 0;
-        const float ca = p.coef[it][0], cb = p.coef[it][1] * (1.0f / kHalfA),
-                    cc = p.coef[it][2] * (1.0f / (kHalfA * kHalfA));
+        const bool out = slot >= 0 && poison[slot] != 0;
+        float v[32];
+        tmem_ld_32cols(t_row + T_AA + ca0, v);
 #pragma unroll
-        for (int c = 0; c < 64; c += 32) {
-          float v[32];
-          tmem_ld_32cols(t_row + T_AA + ca0 + c, v);
+        for (int q = 0; q < 4; ++q) {
+          float a8[8];
+          widen8(h[q], kViewF16, a8);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint8_t* at = abuf + group_at(r, ((ca0 + c) >> 3) + q);
-            float a8[8];
-            widen8(*reinterpret_cast<const uint4*>(at), kViewF16, a8);
+          for (int i = 0; i < 8; ++i) v[8 * q + i] = fmaf(cc, v[8 * q + i], cb * a8[i]);
+        }
+        masked(v);
+        if (part4 == quad) {  // the diagonal: entry `lane` of this thread
+          float d = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int col = ca0 + c + q * 8 + i;
-              const float diag = col == r ? ca : 0.0f;
-              float x = fmaf(cc, v[8 * q + i], fmaf(cb, a8[i], diag));
-              x = (col >> lh) == slot && !out ? x : 0.0f;
-              v[8 * q + i] = x;
-              if (col == r) remainder[r] = x - __half2float(__float2half_rn(x));
+          for (int i = 0; i < 32; ++i) {
+            if (i == lane) {
+              v[i] += ca;
+              d = v[i];
             }
-            *reinterpret_cast<uint4*>(at) = pack8h(v + 8 * q);
           }
+          const float rounded = __half2float(__float2half_rn(d));
+          row_factor[r] = fabsf(rounded) > 0x1p-10f ? d / rounded : 1.0f;
         }
-        if (out && slot >= 0) {  // nothing of this matrix may meet the others' rows
-          for (int u = half; u < groups; u += 2)
+        if (out) {  // nothing of this matrix may meet the others' rows
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          for (int u = part4; u < groups; u += 4)
             *reinterpret_cast<uint4*>(xbuf + group_at(r, u)) = make_uint4(0, 0, 0, 0);
+          fence_async_smem();
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = pack8h(v + 8 * q);
+        tmem_st_16cols(t_row + T_B + part4 * 16, h);
       }
-      fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(b_ready);
-      epi_sync();  // the remainders
-      const float rest = active ? remainder[r] : 0.0f;
+      epi_sync();  // the row factors
+      const float g = active ? row_factor[r] : 1.0f;
       // ------------------------------------------------------------ X <- B' X
 #pragma unroll 1
       for (int b = 0; b < nblk; ++b) {
-        wait_on(upd_full + 8 * (b & 1), uses[b & 1] & 1);
-        ++uses[b & 1];
-        const int chunks = min(128, p.width - b * 128) / 32;
-        if (ok && active) {
-#pragma unroll 1
-          for (int ch = half; ch < chunks; ch += 2) {
-            float v[32];
-            tmem_ld_32cols(t_row + T_UPD + (b & 1) * 128 + ch * 32, v);
+        wait_on(upd_full + 8 * (b & 1), (uses >> (b & 1)) & 1);
+        uses ^= 1u << (b & 1);
+        if (ok && active && ca0 < p.width - b * 128) {
+          const uint32_t t = t_row + T_UPD + (b & 1) * 128 + ca0;
+          float v[32];
+          tmem_ld_32cols(t, v);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              uint8_t* at = xbuf + group_at(r, b * 16 + ch * 4 + q);
-              float x[8];
-              widen8(*reinterpret_cast<const uint4*>(at), kViewF16, x);
+          for (int q = 0; q < 4; ++q) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[8 * q + i] = fmaf(rest, x[i], v[8 * q + i]);
-              *reinterpret_cast<uint4*>(at) = pack8h(v + 8 * q);
+            for (int i = 0; i < 8; i += 2) {
+              const float2 x = __fmul2_rn(make_float2(v[8 * q + i], v[8 * q + i + 1]), make_float2(g, g));
+              v[8 * q + i] = x.x;
+              v[8 * q + i + 1] = x.y;
             }
+            h[q] = pack8h(v + 8 * q);
+            *reinterpret_cast<uint4*>(xbuf + group_at(r, b * 16 + part4 * 4 + q)) = h[q];
           }
+          if (it + 1 < p.k) tmem_st_16cols(t, h);
+          fence_async_smem();
         }
-        fence_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(upd_done + 8 * (b & 1));
@@ -586,24 +608,27 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
       const bool nan = poison[slot_l] != 0;
       const float coef = nan ? __uint_as_float(0x7FC00000u) : sg.coef;
 #pragma unroll 1
-      for (int u = u0; u < groups; u += 16) {
+      for (int u = u0; u < groups; u += EPI / 16) {
         const Block b = block_of(u, sg.dst_tr != 0, sg.dst_ld, sg.dst_bs);
         uint4 q[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) q[k] = *reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u));
         if (sg.dst_tr) transpose8(q);
         if (p.decay != 0.0f) {
-          float w[8][8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            load_eight(sg.dst, sg.dst_type, b.at + k * b.ld, k < b.rows ? b.have : 0, sg.dst_vec != 0, w[k]);
+          for (int k0 = 0; k0 < 8; k0 += 4) {
+            float w[4][8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float v[8];
-            widen8(q[k], kViewF16, v);
+            for (int k = 0; k < 4; ++k)
+              load_eight(sg.dst, sg.dst_type, b.at + (k0 + k) * b.ld, k0 + k < b.rows ? b.have : 0, sg.dst_vec != 0, w[k]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = fmaf(p.decay, w[k][i], coef * v[i]);
-            store_eight(sg.dst, sg.dst_type, b.at + k * b.ld, k < b.rows ? b.have : 0, sg.dst_vec != 0, v);
+            for (int k = 0; k < 4; ++k) {
+              float v[8];
+              widen8(q[k0 + k], kViewF16, v);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = fmaf(p.decay, w[k][i], coef * v[i]);
+              store_eight(sg.dst, sg.dst_type, b.at + (k0 + k) * b.ld, k0 + k < b.rows ? b.have : 0, sg.dst_vec != 0, v);
+            }
           }
         } else {
 #pragma unroll
@@ -620,6 +645,11 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   }
 
   // ---------------------------------------------------------------- teardown
+  if (!ok && C > 1) {  // after a wait that ran out, let what is on its way between the CTAs arrive
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 1000000ull) __nanosleep(1000);
+  }
+  __syncwarp();
   sync_all();  // no CTA leaves while its shared memory may be read
   if (warp == EPI_WARPS) {
     __syncwarp();

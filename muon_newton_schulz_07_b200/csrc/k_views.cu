@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_co
   for (int i = threadIdx.x; i < s.parts; i += THREADS) ss += part[i];
   const float norm = sqrtf(block_sum(ss));
   if (w.tile == 0 && threadIdx.x == 0) p.norms[s.caller_idx + w.e] = norm;
-  const Normaliser nz = normaliser(norm, p.eps);
+  const float mul = normaliser(norm, p.eps);
   __half* x = static_cast<__half*>(s.x) + static_cast<size_t>(w.e) * s.mp * s.np;
   if (s.src_tr) {
 #pragma unroll
@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_co
       int r, c;
       place(true, q, r, c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) stage[c + i][r] = __float2half_rn(v[q][i] * nz.pre * nz.mul);
+      for (int i = 0; i < 8; ++i) stage[c + i][r] = __float2half_rn(v[q][i] * mul);
     }
     __syncthreads();
   }
@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_co
       if (s.src_tr)
         t = __halves2half2(stage[r][c + 2 * i], stage[r][c + 2 * i + 1]);
       else
-        t = __floats2half2_rn(v[q][2 * i] * nz.pre * nz.mul, v[q][2 * i + 1] * nz.pre * nz.mul);
+        t = __floats2half2_rn(v[q][2 * i] * mul, v[q][2 * i + 1] * mul);
       h[i] = *reinterpret_cast<const uint32_t*>(&t);
     }
     *reinterpret_cast<uint4*>(x + static_cast<size_t>(w.r0 + r) * s.np + w.c0 + c) = make_uint4(h[0], h[1], h[2], h[3]);

@@ -78,17 +78,11 @@ __device__ __forceinline__ void store_eight(void* base, int type, long long at, 
     if (i < have) store_one(base, type, at + i, v[i]);
 }
 
-// x / (norm + eps) * 2^12 as one multiplication: x * pre * mul.  `pre` lifts x first when the
-// denominator is so small that its reciprocal would overflow.  A zero denominator gives 0.
-struct Normaliser {
-  float pre, mul;
-};
-__device__ __forceinline__ Normaliser normaliser(float norm, float eps) {
+// The factor that makes x into the stored 2^12 x / (norm + eps).  The denominator counts as 2^-100 at
+// least, so that its reciprocal is finite; a NaN stays one.
+__device__ __forceinline__ float normaliser(float norm, float eps) {
   const float den = norm + eps;
-  Normaliser n;
-  n.pre = den < 1.0e-30f ? 1.8446744e19f : 1.0f;  // 2^64
-  n.mul = den > 0.0f ? kHalfX / (den * n.pre) : (den == 0.0f ? 0.0f : den);  // NaN stays NaN
-  return n;
+  return kHalfX / (den < 0x1p-100f ? 0x1p-100f : den);
 }
 
 }  // namespace muon
