@@ -117,11 +117,57 @@ __device__ __forceinline__ void transpose8(uint4 (&q)[8]) {
   for (int k = 0; k < 8; ++k) q[k] = make_uint4(out[k][0], out[k][1], out[k][2], out[k][3]);
 }
 
+template <int TYPE>
+__device__ __forceinline__ void squares8(const uint4& q, float2& ss) {
+  float v[8];
+  widen8(q, TYPE, v);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) ss = __ffma2_rn(make_float2(v[i], v[i + 1]), make_float2(v[i], v[i + 1]), ss);
+}
+
+// Eight 16-bit values times f, from one 16-bit type to another.
+template <int FROM, int TO>
+__device__ __forceinline__ uint4 rescale8(const uint4& q, float f) {
+  float v[8];
+  widen8(q, FROM, v);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 x = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(f, f));
+    if (TO == kViewBF16) {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      w[i] = pack2h(x.x, x.y);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight neighbouring values of the result (decay 0: without reading what was there).  Not inlined: it is
+// called from unrolled code that runs once.
+__device__ __noinline__ void write_eight(void* dst, int type, long long at, uint4 q, float coef, float decay) {
+  float v[8];
+  widen8(q, kViewF16, v);
+  if (decay != 0.0f) {
+    float w[8];
+    load_eight(dst, type, at, 8, true, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = fmaf(decay, w[i], coef * v[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= coef;
+  }
+  store_eight(dst, type, at, 8, true, v);
+}
+
+// CLUSTER: 1, 2, or 4 for any larger cluster.
+template <int CLUSTER>
 __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_constant__ SkinnyParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int nch = p.width / 64;
-  const int C = p.cluster;
+  const int C = CLUSTER <= 2 ? CLUSTER : p.cluster;
   uint8_t* xbuf = smem;
   uint8_t* abuf = smem + nch * CHUNK;
   uint8_t* share = abuf + ABUF_BYTES;  // C > 2 only
@@ -216,57 +262,63 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     if (e < 0 || b.have <= 0) b.rows = 0;
     return b;
   };
-  auto load_f32 = [&](const Block& b, int k0, float (&v)[4][8]) {  // four storage rows
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      load_eight(sg.src, kViewF32, b.at + (k0 + k) * b.ld, k0 + k < b.rows ? b.have : 0, sg.src_vec != 0, v[k]);
+  // Blocks that reach over the matrix's edge or whose rows are not aligned go value by value, in
+  // loops: this code runs once per tile, and what it costs is fetching its instructions.
+  auto whole = [&](const Block& b, bool vec) { return vec && b.rows >= 8 && b.have >= 8; };
+  auto x_value = [&](int u, bool tr, int k, int i) {  // value i of storage row k of block (ig, u), in X
+    const int row = ig * 8 + (tr ? i : k), at = tr ? k : i;
+    return reinterpret_cast<uint16_t*>(xbuf + group_at(row, u) + at * 2);
   };
+  const bool src_tr = sg.src_tr != 0, src_vec = sg.src_vec != 0;
   if (warp < EPI_WARPS) {
     float ss = 0.0f;
+    float2 ss2 = make_float2(0.0f, 0.0f);
 #pragma unroll 1
     for (int u = u0; u < groups; u += EPI / 16) {
-      const Block b = block_of(u, sg.src_tr != 0, sg.src_ld, sg.src_bs);
-      if (wide_src) {
+      const Block b = block_of(u, src_tr, sg.src_ld, sg.src_bs);
+      if (b.rows <= 0) {
+        if (!wide_src) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = make_uint4(0, 0, 0, 0);
+        }
+      } else if (!whole(b, src_vec)) {
 #pragma unroll 1
-        for (int k0 = 0; k0 < 8; k0 += 4) {
-          float v[4][8];
-          load_f32(b, k0, v);
+        for (int i = 0; i < 64; ++i) {
+          const int k = i >> 3, c = i & 7;
+          const bool there = k < b.rows && c < b.have;
+          const float v = there ? load_one(sg.src, sg.src_type, b.at + k * b.ld + c) : 0.0f;
+          ss = fmaf(v, v, ss);
+          if (!wide_src) *x_value(u, src_tr, k, c) = there ? static_cast<const uint16_t*>(sg.src)[b.at + k * b.ld + c] : 0;
+        }
+      } else if (wide_src) {
+        const float* src = static_cast<const float*>(sg.src) + b.at;
+        float4 q[8];
+#pragma unroll 1
+        for (int h = 0; h < 8; h += 4) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 8; ++k) q[k] = __ldg(reinterpret_cast<const float4*>(src + (k >> 1) * b.ld + (k & 1) * 4));
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(v[k][i], v[k][i], ss);
+          for (int k = 0; k < 8; ++k) ss = fmaf(q[k].x, q[k].x, fmaf(q[k].y, q[k].y, fmaf(q[k].z, q[k].z, fmaf(q[k].w, q[k].w, ss))));
+          src += 4 * b.ld;
         }
       } else {
         uint4 q[8];
         const uint16_t* src = static_cast<const uint16_t*>(sg.src) + b.at;
-        if (sg.src_vec && b.rows >= 8 && b.have >= 8) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) q[k] = __ldg(reinterpret_cast<const uint4*>(src + k * b.ld));
+        for (int k = 0; k < 8; ++k) q[k] = __ldg(reinterpret_cast<const uint4*>(src + k * b.ld));
+        if (sg.src_type == kViewBF16) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) squares8<kViewBF16>(q[k], ss2);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t lo = k < b.rows && 2 * i < b.have ? src[k * b.ld + 2 * i] : 0;
-              const uint32_t hi = k < b.rows && 2 * i + 1 < b.have ? src[k * b.ld + 2 * i + 1] : 0;
-              w[i] = lo | hi << 16;
-            }
-            q[k] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+          for (int k = 0; k < 8; ++k) squares8<kViewF16>(q[k], ss2);
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float v[8];
-          widen8(q[k], sg.src_type, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) ss = fmaf(v[i], v[i], ss);
-        }
-        if (sg.src_tr) transpose8(q);
+        if (src_tr) transpose8(q);
 #pragma unroll
         for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = q[k];
       }
     }
+    ss += ss2.x + ss2.y;
 #pragma unroll
     for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     if ((tid & 7) == 0) part[(tid >> 7) * 16 + ig] = ss;
@@ -300,37 +352,46 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     const float f = out ? 0.0f : factor[slot_l];
 #pragma unroll 1
     for (int u = u0; u < groups; u += EPI / 16) {
-      uint4 q[8];
       if (wide_src) {
-        const Block b = block_of(u, sg.src_tr != 0, sg.src_ld, sg.src_bs);
+        const Block b = block_of(u, src_tr, sg.src_ld, sg.src_bs);
+        const bool full = whole(b, src_vec);
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {  // (fp32: the second read, an L2 hit)
+          float v[8];
+          if (full) {
+            load_eight(sg.src, kViewF32, b.at + k * b.ld, 8, true, v);
+          } else {
 #pragma unroll
-        for (int k0 = 0; k0 < 8; k0 += 4) {
-          float v[4][8];
-          load_f32(b, k0, v);
+            for (int i = 0; i < 8; ++i)
+              v[i] = k < b.rows && i < b.have ? static_cast<const float*>(sg.src)[b.at + k * b.ld + i] : 0.0f;
+          }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int i = 0; i < 8; ++i) v[i] = out ? 0.0f : v[i] * f;
+          if (!src_tr) {
+            *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = pack8h(v);
+          } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[k][i] *= f;
-            q[k0 + k] = pack8h(v[k]);
+            for (int i = 0; i < 8; ++i) *x_value(u, true, k, i) = __half_as_ushort(__float2half_rn(v[i]));
           }
         }
-        if (sg.src_tr) transpose8(q);
+      } else if (out) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = make_uint4(0, 0, 0, 0);
       } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          float v[8];
-          widen8(*reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u)), sg.src_type, v);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= f;
-          q[k] = pack8h(v);
+        if (sg.src_type == kViewBF16) {
+#pragma unroll 4
+          for (int k = 0; k < 8; ++k) {
+            uint4* at = reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u));
+            *at = rescale8<kViewBF16, kViewF16>(*at, f);
+          }
+        } else {
+#pragma unroll 4
+          for (int k = 0; k < 8; ++k) {
+            uint4* at = reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u));
+            *at = rescale8<kViewF16, kViewF16>(*at, f);
+          }
         }
       }
-      if (out) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = make_uint4(0, 0, 0, 0);
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = q[k];
     }
   }
   fence_async_smem();
@@ -555,7 +616,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
             }
           }
           const float rounded = __half2float(__float2half_rn(d));
-          row_factor[r] = fabsf(rounded) > 0x1p-10f ? d / rounded : 1.0f;
+          row_factor[r] = fabsf(rounded) > 0x1p-10f ? __fdividef(d, rounded) : 1.0f;
         }
         if (out) {  // nothing of this matrix may meet the others' rows
 #pragma unroll
@@ -567,6 +628,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
 #pragma unroll
         for (int q = 0; q < 4; ++q) h[q] = pack8h(v + 8 * q);
         tmem_st_16cols(t_row + T_B + part4 * 16, h);
+        tmem_st_wait();
       }
       tc_fence_before();
       __syncwarp();
@@ -591,10 +653,13 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
               v[8 * q + i + 1] = x.y;
             }
             h[q] = pack8h(v + 8 * q);
-            *reinterpret_cast<uint4*>(xbuf + group_at(r, b * 16 + part4 * 4 + q)) = h[q];
           }
           if (it + 1 < p.k) tmem_st_16cols(t, h);
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *reinterpret_cast<uint4*>(xbuf + group_at(r, b * 16 + part4 * 4 + q)) = h[q];
           fence_async_smem();
+          if (it + 1 < p.k) tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
@@ -605,39 +670,35 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
 
     // -------------------------------------------------------------- X_k to its view
     if (e >= 0) {
-      const bool nan = poison[slot_l] != 0;
-      const float coef = nan ? __uint_as_float(0x7FC00000u) : sg.coef;
+      const float coef = poison[slot_l] != 0 ? __uint_as_float(0x7FC00000u) : sg.coef;
+      const bool dst_tr = sg.dst_tr != 0;
 #pragma unroll 1
       for (int u = u0; u < groups; u += EPI / 16) {
-        const Block b = block_of(u, sg.dst_tr != 0, sg.dst_ld, sg.dst_bs);
-        uint4 q[8];
+        const Block b = block_of(u, dst_tr, sg.dst_ld, sg.dst_bs);
+        if (whole(b, sg.dst_vec != 0)) {
+          uint4 q[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = *reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u));
-        if (sg.dst_tr) transpose8(q);
-        if (p.decay != 0.0f) {
+          for (int k = 0; k < 8; ++k) q[k] = *reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u));
+          if (dst_tr) transpose8(q);
+          if (p.decay == 0.0f && sg.dst_type == kViewBF16) {
+            uint16_t* dst = static_cast<uint16_t*>(sg.dst) + b.at;
 #pragma unroll
-          for (int k0 = 0; k0 < 8; k0 += 4) {
-            float w[4][8];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              load_eight(sg.dst, sg.dst_type, b.at + (k0 + k) * b.ld, k0 + k < b.rows ? b.have : 0, sg.dst_vec != 0, w[k]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float v[8];
-              widen8(q[k0 + k], kViewF16, v);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = fmaf(p.decay, w[k][i], coef * v[i]);
-              store_eight(sg.dst, sg.dst_type, b.at + (k0 + k) * b.ld, k0 + k < b.rows ? b.have : 0, sg.dst_vec != 0, v);
-            }
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(dst + k * b.ld) = rescale8<kViewF16, kViewBF16>(q[k], coef);
+            continue;
           }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) write_eight(sg.dst, sg.dst_type, b.at + k * b.ld, q[k], coef, p.decay);
         } else {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float v[8];
-            widen8(q[k], kViewF16, v);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= coef;
-            store_eight(sg.dst, sg.dst_type, b.at + k * b.ld, k < b.rows ? b.have : 0, sg.dst_vec != 0, v);
+#pragma unroll 1
+          for (int i = 0; i < 64; ++i) {
+            const int k = i >> 3, c = i & 7;
+            if (k < b.rows && c < b.have) {
+              const long long at = b.at + k * b.ld + c;
+              const float x = coef * __half2float(__ushort_as_half(*x_value(u, dst_tr, k, c)));
+              const float w = p.decay != 0.0f ? load_one(sg.dst, sg.dst_type, at) : 0.0f;
+              store_one(sg.dst, sg.dst_type, at, p.decay != 0.0f ? fmaf(p.decay, w, x) : x);
+            }
           }
         }
       }
@@ -659,8 +720,9 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
 
 }  // namespace
 
-cudaError_t launch_ns_skinny(const SkinnyParams& p, cudaStream_t s) {
-  if (p.total <= 0) return cudaSuccess;
+namespace {
+template <int CLUSTER>
+cudaError_t launch(const SkinnyParams& p, cudaStream_t s) {
   // The shared-memory limit is a property of the function on each device: set it once per device.
   static std::atomic<unsigned long long> attr_set{0};
   int dev = 0;
@@ -668,7 +730,7 @@ cudaError_t launch_ns_skinny(const SkinnyParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if ((attr_set.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(ns_skinny_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(ns_skinny_kernel<CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(SMEM_LIMIT));
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(bit);
@@ -686,7 +748,15 @@ cudaError_t launch_ns_skinny(const SkinnyParams& p, cudaStream_t s) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ns_skinny_kernel, p);
+  return cudaLaunchKernelEx(&cfg, ns_skinny_kernel<CLUSTER>, p);
+}
+}  // namespace
+
+cudaError_t launch_ns_skinny(const SkinnyParams& p, cudaStream_t s) {
+  if (p.total <= 0) return cudaSuccess;
+  if (p.cluster == 1) return launch<1>(p, s);
+  if (p.cluster == 2) return launch<2>(p, s);
+  return launch<4>(p, s);
 }
 
 }  // namespace muon
