@@ -399,17 +399,14 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
 
   if (warp == EPI_WARPS) {
     // -------------------------------------------------------------- MMA issuer
-    if (lane == 0) {
+    {
+      const uint32_t lead = elect_one();
       const uint32_t idesc_sym = idesc_f16_f32(true, 128, used16, 0, 0);
       const uint32_t idesc_128 = idesc_f16_f32(true, 128, 128, 0, 1), idesc_64 = idesc_f16_f32(true, 128, 64, 0, 1);
       const uint64_t x_rows = smem_desc_sw128(xaddr, 16, 1024);     // X, K-major: 16 columns are 32 bytes
       const uint64_t x_cols = smem_desc_sw128(xaddr, CHUNK, 1024);  // X, MN-major: 16 rows are 2 KB
       const uint64_t a_rows = smem_desc_sw128(aaddr, 16, 1024);
       constexpr uint64_t BLOCK = 2 * CHUNK >> 4;                    // 128 columns, in descriptor units
-      auto wait_one = [&](uint32_t bar, uint32_t par) {
-        if (ok) ok = mbar_wait_bounded(bar, par, tmo, nullptr, p.status);
-        tc_fence_after();
-      };
       // MMAs go out four at a time (64 columns, or 64 rows of X), each descriptor the first one's plus a
       // constant: what is computed between two MMAs adds to their time.  Rows beyond the tile's
       // matrices are zero in X and B', so rounding their number up to 64 changes nothing.
@@ -420,7 +417,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
         for (int c = 2 * b; c < min(nch, 2 * b + 2); ++c) {
           const uint64_t d = x_rows + (CHUNK >> 4) * static_cast<uint64_t>(c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) tc_mma_bf16(tmem + T_A, d + 2 * j, d + 2 * j, idesc_sym, (c | j) != 0 ? 1u : 0u);
+          for (int j = 0; j < 4; ++j) tc_mma_lead(lead, tmem + T_A, d + 2 * j, d + 2 * j, idesc_sym, (c | j) != 0 ? 1u : 0u);
         }
       };
       auto gram_next = [&](int b) {
@@ -430,7 +427,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
           const uint32_t t = tmem + T_UPD + (c & 3) * 64;
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc_mma_tmem_a(tmem + T_A, t + (j >> 1) * 32 + (j & 1) * 8, d + 2 * j, idesc_sym, (c | j) != 0 ? 1u : 0u);
+            tc_mma_tmem_a_lead(lead, tmem + T_A, t + (j >> 1) * 32 + (j & 1) * 8, d + 2 * j, idesc_sym, (c | j) != 0 ? 1u : 0u);
         }
       };
       auto update_block = [&](int b) {
@@ -440,29 +437,29 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
         for (int g = 0; g < used; g += 64) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc_mma_tmem_a(t, tmem + T_B + g / 2 + j * 8, d + 8 * g + j * 128, idesc, (g | j) != 0 ? 1u : 0u);
+            tc_mma_tmem_a_lead(lead, t, tmem + T_B + g / 2 + j * 8, d + 8 * g + j * 128, idesc, (g | j) != 0 ? 1u : 0u);
         }
-        tc_commit(upd_full + 8 * (b & 1));
+        tc_commit_lead(lead, upd_full + 8 * (b & 1));
       };
       uint32_t done = 0;  // parities of upd_done, a bit each
       if (p.k > 0) {
 #pragma unroll 1
         for (int b = 0; b < nblk; ++b) gram_first(b);
-        tc_commit(a_full);
+        tc_commit_lead(lead, a_full);
       }
 #pragma unroll 1
       for (int it = 0; it < p.k; ++it) {
-        wait_one(a_ready, it & 1);
+        wait_on(a_ready, it & 1);
         if (ok) {
 #pragma unroll 1
           for (int g = 0; g < used; g += 64) {
             const uint64_t d = a_rows + (CHUNK >> 4) * static_cast<uint64_t>(g >> 6);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) tc_mma_bf16(tmem + T_AA, d + 2 * j, d + 2 * j, idesc_sym, (g | j) != 0 ? 1u : 0u);
+            for (int j = 0; j < 4; ++j) tc_mma_lead(lead, tmem + T_AA, d + 2 * j, d + 2 * j, idesc_sym, (g | j) != 0 ? 1u : 0u);
           }
-          tc_commit(aa_full);
+          tc_commit_lead(lead, aa_full);
         }
-        wait_one(b_ready, it & 1);
+        wait_on(b_ready, it & 1);
         if (ok) {
           update_block(0);
           if (nblk > 1) update_block(1);
@@ -471,11 +468,11 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
         for (int b = 0; b < nblk; ++b) {
           // block b is the new X.  (A barrier each for even and odd blocks: the warps may finish
           // block b + 1 before this wait, but not b + 2.)
-          wait_one(upd_done + 8 * (b & 1), (done >> (b & 1)) & 1);
+          wait_on(upd_done + 8 * (b & 1), (done >> (b & 1)) & 1);
           done ^= 1u << (b & 1);
           if (ok && it + 1 < p.k) {
             gram_next(b);  // before the update that takes the same TMEM columns
-            if (b + 1 == nblk) tc_commit(a_full);
+            if (b + 1 == nblk) tc_commit_lead(lead, a_full);
           }
           if (ok && b + 2 < nblk) update_block(b + 2);
         }
