@@ -212,8 +212,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     mbar_init(b_ready, EPI_WARPS);
     mbar_init(upd_full, 1);
     mbar_init(upd_full + 8, 1);
-    mbar_init(upd_done, EPI_WARPS);
-    mbar_init(upd_done + 8, EPI_WARPS);
+    mbar_init(upd_done, EPI_WARPS / 2);
+    mbar_init(upd_done + 8, EPI_WARPS / 2);
     mbar_init(share_full, 1);
     mbar_init(rows_full, 1);
     mbar_init(peer_free, 1);
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     const bool active = quad * 32 < used;                 // rows that hold a matrix (warp-uniform)
     const int slot = r < used ? r >> lh : -1;             // -1: no matrix, the row stays 0
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-    uint32_t uses = 0;                                    // parities of upd_full, a bit each
+    uint32_t uses = 0;                                    // parity of upd_full
     uint32_t own = 0;                                     // columns ca0 + i of the row's own matrix, a bit each
     for (int i = 0; i < 32; ++i) own |= static_cast<uint32_t>(((ca0 + i) >> lh) == slot) << i;
     constexpr float kGram = kHalfA / (kHalfX * kHalfX);
@@ -500,6 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     const int owner = r / rows_c, in_slice = r & (rows_c - 1);
     // the place of 16 bytes of a share of A in its owner's memory: neighbouring rows side by side
     const uint32_t share_base = C == 2 ? aaddr : saddr;
+    const int helper = C == 2 ? 2 * (1 - rank) : 0;       // a warp that sends the signals: for C = 2 one without rows to add
     auto share_at = [&](int from, int q) {
       return static_cast<uint32_t>((C == 2 ? 0 : from * rows_c * 32) + q * rows_c + in_slice) * 16;
     };
@@ -543,7 +544,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
           }
           if (C == 2) {
             epi_sync();  // the share has been read: its place takes A
-            if (tid == 0 && ok) mbar_arrive_remote(map_to_rank(peer_read, rank ^ 1));
+            if (warp == helper && lane == 0 && ok) mbar_arrive_remote(map_to_rank(peer_read, rank ^ 1));
           }
         }
 #pragma unroll
@@ -559,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
       fence_async_smem();
       if (C > 1) {
         epi_sync();
-        if (warp == 0) {
+        if (warp == helper) {
           if (C == 2) wait_on(peer_read, par);
           if (lane < C && lane != rank && ok) {
             for (int c = 0; c < 2; ++c) {
@@ -570,11 +571,11 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
           __syncwarp();
         }
         wait_on(rows_full, par);
-        if (tid < C && tid != rank && ok) mbar_arrive_remote(map_to_rank(peer_got, tid));
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(a_ready);
+      if (C > 1 && tid < C && tid != rank && ok) mbar_arrive_remote(map_to_rank(peer_got, tid));
       if (C > 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[i] = *reinterpret_cast<const uint4*>(abuf + group_at(r, (ca0 >> 3) + i));
@@ -600,7 +601,12 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
           float a8[8];
           widen8(h[q], kViewF16, a8);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[8 * q + i] = fmaf(cc, v[8 * q + i], cb * a8[i]);
+          for (int i = 0; i < 8; i += 2) {
+            const float2 x = __ffma2_rn(make_float2(cc, cc), make_float2(v[8 * q + i], v[8 * q + i + 1]),
+                                        __fmul2_rn(make_float2(cb, cb), make_float2(a8[i], a8[i + 1])));
+            v[8 * q + i] = x.x;
+            v[8 * q + i + 1] = x.y;
+          }
         }
         masked(v);
         if (part4 == quad) {  // the diagonal: entry `lane` of this thread
@@ -615,15 +621,15 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
           const float rounded = __half2float(__float2half_rn(d));
           row_factor[r] = fabsf(rounded) > 0x1p-10f ? __fdividef(d, rounded) : 1.0f;
         }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = pack8h(v + 8 * q);
         if (out) {  // nothing of this matrix may meet the others' rows
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+          for (int q = 0; q < 4; ++q) h[q] = make_uint4(0, 0, 0, 0);
           for (int u = part4; u < groups; u += 4)
             *reinterpret_cast<uint4*>(xbuf + group_at(r, u)) = make_uint4(0, 0, 0, 0);
           fence_async_smem();
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = pack8h(v + 8 * q);
         tmem_st_16cols(t_row + T_B + part4 * 16, h);
         tmem_st_wait();
       }
@@ -633,34 +639,40 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
       epi_sync();  // the row factors
       const float g = active ? row_factor[r] : 1.0f;
       // ------------------------------------------------------------ X <- B' X
+      // Warps 0..7 take the even blocks, 8..15 the odd ones, 64 columns a warp: a block's chain of
+      // TMEM read, conversion, stores and fence is latency, which two blocks at a time hide.
+      const int grp = warp >> 3;
 #pragma unroll 1
-      for (int b = 0; b < nblk; ++b) {
-        wait_on(upd_full + 8 * (b & 1), (uses >> (b & 1)) & 1);
-        uses ^= 1u << (b & 1);
-        if (ok && active && ca0 < p.width - b * 128) {
-          const uint32_t t = t_row + T_UPD + (b & 1) * 128 + ca0;
-          float v[32];
-          tmem_ld_32cols(t, v);
+      for (int b = grp; b < nblk; b += 2) {
+        wait_on(upd_full + 8 * grp, uses);
+        uses ^= 1u;
+        if (ok && active) {
+#pragma unroll 1
+          for (int c = (part4 & 1) * 64; c < min((part4 & 1) * 64 + 64, p.width - b * 128); c += 32) {
+            const uint32_t t = t_row + T_UPD + grp * 128 + c;
+            float v[32];
+            tmem_ld_32cols(t, v);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 4; ++q) {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float2 x = __fmul2_rn(make_float2(v[8 * q + i], v[8 * q + i + 1]), make_float2(g, g));
-              v[8 * q + i] = x.x;
-              v[8 * q + i + 1] = x.y;
+              for (int i = 0; i < 8; i += 2) {
+                const float2 x = __fmul2_rn(make_float2(v[8 * q + i], v[8 * q + i + 1]), make_float2(g, g));
+                v[8 * q + i] = x.x;
+                v[8 * q + i + 1] = x.y;
+              }
+              h[q] = pack8h(v + 8 * q);
             }
-            h[q] = pack8h(v + 8 * q);
-          }
-          if (it + 1 < p.k) tmem_st_16cols(t, h);
+            if (it + 1 < p.k) tmem_st_16cols(t, h);
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(xbuf + group_at(r, b * 16 + part4 * 4 + q)) = h[q];
+            for (int q = 0; q < 4; ++q)
+              *reinterpret_cast<uint4*>(xbuf + group_at(r, b * 16 + (c >> 3) + q)) = h[q];
+          }
           fence_async_smem();
           if (it + 1 < p.k) tmem_st_wait();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(upd_done + 8 * (b & 1));
+        if (lane == 0) mbar_arrive(upd_done + 8 * grp);
       }
     }
     epi_sync();  // X_k is complete
