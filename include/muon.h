@@ -93,7 +93,7 @@ typedef enum { MUON_BF16 = 0, MUON_FP32 = 1, MUON_FP16 = 2 } muon_dtype_t;
  *           is rounded, so the inputs' size does not matter down to norms of about 1e-4 eps.
  *           Matrices of at most 128 rows (or columns) and 4096 columns (rows) run every
  *           iteration on chip.  Takes views, coefficients per iteration and 8-bit
- *           momentum (below); iterations are launched as MUON_SCHEDULE_STAGED. */
+ *           momentum (below). */
 typedef enum { MUON_MODE_FAST = 0, MUON_MODE_FP32_REF = 1, MUON_MODE_HALF = 2 } muon_mode_t;
 
 typedef struct { int64_t rows, cols; } muon_shape_t;
@@ -332,7 +332,7 @@ MUON_API muon_status_t muon_get_plan(muon_handle_t handle, int ns_steps, int* n_
  *                         of STAGED with one launch per step instead of 3 k),
  *                         else STAGED.
  * The small-matrix kernel (MUON_KERNEL_NS_SMALL) keeps precedence when its
- * conditions hold; FP32_REF and HALF handles always run staged.  Returns
+ * conditions hold; FP32_REF handles always run staged.  Returns
  * MUON_ERR_UNSUPPORTED if FUSED is asked of a handle that cannot run it.
  * The setting applies to later calls; it must not change while a captured graph
  * of the handle is replayed.

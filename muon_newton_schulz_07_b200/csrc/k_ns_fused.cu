@@ -172,27 +172,11 @@ __device__ __forceinline__ bool dependency(const NsParams& p, const FTile& f, co
   return true;
 }
 
-__device__ __forceinline__ void unpack8(const uint4& q, float* v) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __bfloat1622float2(h[i]);
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  uint4 q;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  return q;
-}
-
 // Issue the four K = 16 MMAs of one 64-deep k slice into the 256 columns at d_tmem.
+template <bool HALF>
 __device__ __forceinline__ void mma_slice(uint32_t d_tmem, uint32_t sa, uint32_t sb, bool mna, bool mnb,
                                           bool first) {
-  const uint32_t idesc = idesc_bf16_f32(2 * BM, BN, mna ? 1 : 0, mnb ? 1 : 0);
+  const uint32_t idesc = idesc_f16_f32(HALF, 2 * BM, BN, mna ? 1 : 0, mnb ? 1 : 0);
   // K-major: 16 k per step = 32 bytes along the swizzled row; MN-major: 16 k rows = 2 KB, the
   // two 64-wide M/N chunks 8 KB apart.
   const uint64_t adesc0 = mna ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
@@ -204,7 +188,7 @@ __device__ __forceinline__ void mma_slice(uint32_t d_tmem, uint32_t sa, uint32_t
     tc_mma_bf16_pair(d_tmem, adesc0 + astep * j, bdesc0 + bstep * j, idesc, (!first || j != 0) ? 1u : 0u);
 }
 
-template <bool WR>
+template <bool WR, bool HALF>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     ns_fused_kernel(const __grid_constant__ NsParams p) {
   constexpr int NST = FLayout<WR>::NST;
@@ -369,7 +353,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
             tc_fence_after();
             const uint32_t sa = smem_base + stage * SB;
-            mma_slice(d, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), kb == 0);
+            mma_slice<HALF>(d, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), kb == 0);
             tc_commit_pair_mc(empty_bar(stage), 0x3);  // frees the stage in both CTAs
             if (++stage == NST) {
               stage = 0;
@@ -394,7 +378,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
             tc_fence_after();
             const uint32_t sa = smem_base + stage * SB;
-            mma_slice(tmem_base, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), kb == 0);
+            mma_slice<HALF>(tmem_base, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), kb == 0);
             held[kb] = stage;
             if (++stage == NST) {
               stage = 0;
@@ -406,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           tc_fence_after();
           for (int kb = 0; kb < D; ++kb) {
             const uint32_t sa = smem_base + held[kb] * SB;
-            mma_slice(tmem_base + TILE, sa, sa + A_STAGE + B_STAGE, major_a(kb), major_b(kb, 1), kb == 0);
+            mma_slice<HALF>(tmem_base + TILE, sa, sa + A_STAGE + B_STAGE, major_a(kb), major_b(kb, 1), kb == 0);
             tc_commit_pair_mc(empty_bar(held[kb]), 0x3);
           }
           for (int kb = D; kb < kblocks; ++kb) {
@@ -416,8 +400,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
             tc_fence_after();
             const uint32_t sa = smem_base + stage * SB;
-            mma_slice(tmem_base, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), false);
-            mma_slice(tmem_base + TILE, sa, sa + A_STAGE + B_STAGE, major_a(kb), major_b(kb, 1), false);
+            mma_slice<HALF>(tmem_base, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), false);
+            mma_slice<HALF>(tmem_base + TILE, sa, sa + A_STAGE + B_STAGE, major_a(kb), major_b(kb, 1), false);
             tc_commit_pair_mc(empty_bar(stage), 0x3);
             if (++stage == NST) {
               stage = 0;
@@ -474,7 +458,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         W = static_cast<__nv_bfloat16*>(p.wptr[slot]);
         cw = p.wcoef[slot];
         tr = p.wtrans[slot] != 0;
-        ldw = tr ? G.m_real : G.n_real;
+        ldw = p.wld[slot];
       }
       const bool wread = fw && p.w_decay != 0.0f && gr0 < G.m_real;
       if (fw) {
@@ -533,13 +517,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       }
       tc_fence_after();
       float s = 1.0f;
-      if (f.it == 0 && f.kind != kPoly) {
+      if (!HALF && f.it == 0 && f.kind != kPoly) {  // (an fp16 X0 is normalised already)
         const float al = p.scal[2 * (G.scal_base + f.mat) + 1];
         s = (f.kind == kGram) ? al * al : al;
       }
-      const float c_acc = f.kind == kPoly ? p.c : 1.0f;
-      const float c_aux = f.kind == kPoly ? p.b : 0.0f;
-      const float cdiag = (f.kind == kPoly && gr < G.m_real) ? p.a : 0.0f;
+      const float c_acc = f.kind == kPoly ? p.coef[f.it][2] : f.kind == kGram ? p.gram : 1.0f;
+      const float c_aux = f.kind == kPoly ? p.coef[f.it][1] : 0.0f;
+      const float cdiag = (f.kind == kPoly && gr < G.m_real) ? p.coef[f.it][0] : 0.0f;
       const uint32_t tlane = static_cast<uint32_t>(quad * 32) << 16;
       const uint32_t tcol0 = nsub == 1 ? static_cast<uint32_t>(sl * TILE) : 0u;
 #pragma unroll 1
@@ -575,11 +559,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 32; i += 4)
                   *reinterpret_cast<float4*>(st32 + lane * F32_PITCH + i) =
-                      make_float4(bf16_round(s * v[i]), bf16_round(s * v[i + 1]), bf16_round(s * v[i + 2]),
-                                bf16_round(s * v[i + 3]));
+                      make_float4(Operand<HALF>::round(s * v[i]), Operand<HALF>::round(s * v[i + 1]), Operand<HALF>::round(s * v[i + 2]),
+                                Operand<HALF>::round(s * v[i + 3]));
               } else {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) st32[i * F32_PITCH + lane] = bf16_round(s * v[i]);
+                for (int i = 0; i < 32; ++i) st32[i * F32_PITCH + lane] = Operand<HALF>::round(s * v[i]);
               }
               __syncwarp();
 #pragma unroll
@@ -590,14 +574,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
                 float r8[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
                 if (wread) {
                   float w8[8];
-                  unpack8(pf[q], w8);
+                  unpack8<false>(pf[q], w8);
 #pragma unroll
                   for (int i = 0; i < 8; ++i) r8[i] = fmaf(p.w_decay, w8[i], cw * r8[i]);
                 } else {
 #pragma unroll
                   for (int i = 0; i < 8; ++i) r8[i] = cw * r8[i];
                 }
-                __stcs(reinterpret_cast<uint4*>(W + woff(gc0, rr)), pack8(r8));
+                __stcs(reinterpret_cast<uint4*>(W + woff(gc0, rr)), pack8<false>(r8));
               }
               __syncwarp();
             }
@@ -617,7 +601,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               float a8[8];
-              unpack8(*reinterpret_cast<const uint4*>(arow + ((q ^ swz) << 4)), a8);
+              unpack8<HALF>(*reinterpret_cast<const uint4*>(arow + ((q ^ swz) << 4)), a8);
 #pragma unroll
               for (int i = 0; i < 8; ++i) v[8 * q + i] = s * fmaf(c_acc, v[8 * q + i], c_aux * a8[i]);
             }
@@ -644,7 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(otile + ob + lane * 64 + ((q ^ swz) << 4)) = pack8(v + 8 * q);
+            *reinterpret_cast<uint4*>(otile + ob + lane * 64 + ((q ^ swz) << 4)) = pack8<HALF>(v + 8 * q);
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -776,7 +760,7 @@ long long check_fused_tiles(const NsParams& p) {
 
 namespace {
 
-template <bool WR>
+template <bool WR, bool HALF>
 cudaError_t launch_fused_kind(const NsParams& p, int num_sms, cudaStream_t s) {
   static std::atomic<unsigned long long> attr_set{0};
   static std::atomic<int> max_clusters[64];
@@ -787,7 +771,7 @@ cudaError_t launch_fused_kind(const NsParams& p, int num_sms, cudaStream_t s) {
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   const unsigned long long bit = 1ull << dev;
   if ((attr_set.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(ns_fused_kernel<WR>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    e = cudaFuncSetAttribute(ns_fused_kernel<WR, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     // Every pair must be resident at once (a tile may wait for a tile of any other pair): the
     // grid never exceeds the clusters of two that fit on the device together.
@@ -803,14 +787,14 @@ cudaError_t launch_fused_kind(const NsParams& p, int num_sms, cudaStream_t s) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    e = cudaOccupancyMaxActiveClusters(&n, ns_fused_kernel<WR>, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&n, ns_fused_kernel<WR, HALF>, &cfg);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
     max_clusters[dev].store(n);
     attr_set.fetch_or(bit);
   }
   const int pairs = std::min({num_sms / 2, max_clusters[dev].load(), p.t_end - p.t_begin});
-  ns_fused_kernel<WR><<<2 * pairs, kTcThreads, smem, s>>>(p);
+  ns_fused_kernel<WR, HALF><<<2 * pairs, kTcThreads, smem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -819,7 +803,8 @@ cudaError_t launch_fused_kind(const NsParams& p, int num_sms, cudaStream_t s) {
 cudaError_t launch_ns_fused(const NsParams& p, int num_sms, cudaStream_t s) {
   if (p.t_end <= p.t_begin) return cudaSuccess;
   const bool wide = p.upd_tw[0] > TILE || p.upd_tw[1] > TILE || p.sym_wide != 0;
-  return wide ? launch_fused_kind<true>(p, num_sms, s) : launch_fused_kind<false>(p, num_sms, s);
+  if (p.half) return wide ? launch_fused_kind<true, true>(p, num_sms, s) : launch_fused_kind<false, true>(p, num_sms, s);
+  return wide ? launch_fused_kind<true, false>(p, num_sms, s) : launch_fused_kind<false, false>(p, num_sms, s);
 }
 
 }  // namespace muon

@@ -42,6 +42,7 @@ __device__ __forceinline__ Where find(const ViewParams& p) {
   return w;
 }
 
+// The sum over the CTA, in every thread.
 __device__ __forceinline__ float block_sum(float v) {
   __shared__ float red[THREADS / 32];
 #pragma unroll
@@ -54,32 +55,95 @@ __device__ __forceinline__ float block_sum(float v) {
   return t;
 }
 
-// The four groups of eight stored elements a thread handles: rows of the tile when the storage
-// runs along X's rows, rows of the transposed tile otherwise.
+// The 32 stored elements a thread handles.  Where every stored row is 16-byte aligned, four groups of
+// eight: rows of the tile when the storage runs along X's rows, of the transposed tile otherwise.
 __device__ __forceinline__ void place(bool tr, int q, int& row, int& col) {
   const int c = threadIdx.x + q * THREADS;
   row = tr ? c >> 3 : c >> 4;          // stored row within the tile
   col = (tr ? c & 7 : c & 15) * 8;     // first stored element
 }
-
-__device__ __forceinline__ void load_tile(const ViewSeg& s, const Where& w, float (&v)[4][8]) {
-  const bool tr = s.src_tr != 0;
-  const int rows = tr ? s.n : s.m, cols = tr ? s.m : s.n;  // as stored
-  const int r0 = tr ? w.c0 : w.r0, c0 = tr ? w.r0 : w.c0;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    int r, c;
-    place(tr, q, r, c);
-    const int have = r0 + r < rows ? cols - (c0 + c) : 0;
-    load_eight(s.src, s.src_type, w.e * s.src_bs + (r0 + r) * s.src_ld + c0 + c, have, s.src_vec != 0, v[q]);
-  }
+// Otherwise single elements, a warp's 32 lanes side by side in a stored row.
+__device__ __forceinline__ void place_one(bool tr, int i, int& row, int& col) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  row = warp + 8 * (tr ? i >> 1 : i >> 2);
+  col = lane + 32 * (tr ? i & 1 : i & 3);
 }
 
-__global__ void __launch_bounds__(THREADS, 4) view_sumsq_kernel(const __grid_constant__ ViewParams p) {
+// A tile of the source (DST: of the destination, before it is updated) as a thread's 32 values:
+// groups of eight where `grouped`, single elements otherwise.  The loads of a thread are all
+// issued before any value is used.
+template <bool DST>
+__device__ __forceinline__ bool load_tile(const ViewSeg& s, const Where& w, float (&v)[4][8]) {
+  const bool tr = (DST ? s.dst_tr : s.src_tr) != 0;
+  const int type = DST ? s.dst_type : s.src_type;
+  const void* base = DST ? s.dst : s.src;
+  const long long ld = DST ? s.dst_ld : s.src_ld, bs = DST ? s.dst_bs : s.src_bs;
+  const bool vec = (DST ? s.dst_vec : s.src_vec) != 0;
+  const int rows = tr ? s.n : s.m, cols = tr ? s.m : s.n;  // as stored
+  const int r0 = tr ? w.c0 : w.r0, c0 = tr ? w.r0 : w.c0;
+  if (vec && r0 + (tr ? TC : TR) <= rows && c0 + (tr ? TR : TC) <= cols) {  // whole and aligned
+    const long long at = w.e * bs + r0 * ld + c0;
+    if (type != kViewF32) {
+      uint4 q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int r, c;
+        place(tr, i, r, c);
+        q[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + at + r * ld + c));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) widen8(q[i], type, v[i]);
+    } else {
+      float4 q[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int r, c;
+        place(tr, i, r, c);
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at + r * ld + c);
+        q[2 * i] = __ldg(p);
+        q[2 * i + 1] = __ldg(p + 1);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float* to = &v[i >> 1][(i & 1) * 4];
+        to[0] = q[i].x; to[1] = q[i].y; to[2] = q[i].z; to[3] = q[i].w;
+      }
+    }
+    return true;
+  }
+  if (vec) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      int r, c;
+      place(tr, q, r, c);
+      const int have = r0 + r < rows ? cols - (c0 + c) : 0;
+      load_eight(base, type, w.e * bs + (r0 + r) * ld + c0 + c, have, true, v[q]);
+    }
+    return true;
+  }
+  const long long at = w.e * bs + r0 * ld + c0;
+  auto each = [&](auto load) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      int r, c;
+      place_one(tr, i, r, c);
+      v[i >> 3][i & 7] = r0 + r < rows && c0 + c < cols ? load(at + r * ld + c) : 0.0f;
+    }
+  };
+  if (type == kViewF32)
+    each([&](long long i) { return __ldg(static_cast<const float*>(base) + i); });
+  else if (type == kViewBF16)
+    each([&](long long i) { return __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]); });
+  else
+    each([&](long long i) { return __half2float(static_cast<const __half*>(base)[i]); });
+  return false;
+}
+
+__global__ void __launch_bounds__(THREADS, 6) view_sumsq_kernel(const __grid_constant__ ViewParams p) {
   const Where w = find(p);
   const ViewSeg& s = p.seg[w.seg];
   float v[4][8];
-  load_tile(s, w, v);
+  load_tile<false>(s, w, v);
   float ss = 0.0f;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -94,7 +158,7 @@ __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_co
   const Where w = find(p);
   const ViewSeg& s = p.seg[w.seg];
   float v[4][8];
-  load_tile(s, w, v);
+  const bool grouped = load_tile<false>(s, w, v);
   const float* part = p.partials + s.part_begin + w.e * s.parts;
   float ss = 0.0f;
   for (int i = threadIdx.x; i < s.parts; i += THREADS) ss += part[i];
@@ -102,13 +166,24 @@ __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_co
   if (w.tile == 0 && threadIdx.x == 0) p.norms[s.caller_idx + w.e] = norm;
   const float mul = normaliser(norm, p.eps);
   __half* x = static_cast<__half*>(s.x) + static_cast<size_t>(w.e) * s.mp * s.np;
-  if (s.src_tr) {
+  const bool tr = s.src_tr != 0;
+  const bool staged = tr || !grouped;
+  if (staged) {
+    if (grouped) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      int r, c;
-      place(true, q, r, c);
+      for (int q = 0; q < 4; ++q) {
+        int r, c;
+        place(true, q, r, c);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) stage[c + i][r] = __float2half_rn(v[q][i] * mul);
+        for (int i = 0; i < 8; ++i) stage[c + i][r] = __float2half_rn(v[q][i] * mul);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        int r, c;
+        place_one(tr, i, r, c);
+        stage[tr ? c : r][tr ? r : c] = __float2half_rn(v[i >> 3][i & 7] * mul);
+      }
     }
     __syncthreads();
   }
@@ -120,8 +195,8 @@ __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_co
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       __half2 t;
-      if (s.src_tr)
-        t = __halves2half2(stage[r][c + 2 * i], stage[r][c + 2 * i + 1]);
+      if (staged)
+        t = *reinterpret_cast<const __half2*>(&stage[r][c + 2 * i]);
       else
         t = __floats2half2_rn(v[q][2 * i] * mul, v[q][2 * i + 1] * mul);
       h[i] = *reinterpret_cast<const uint32_t*>(&t);
@@ -134,42 +209,61 @@ __global__ void __launch_bounds__(THREADS, 3) view_write_kernel(const __grid_con
   __shared__ float stage[TR][TC + 1];
   const Where w = find(p);
   const ViewSeg& s = p.seg[w.seg];
-  const bool tr = s.dst_tr != 0;
+  const bool tr = s.dst_tr != 0, grouped = s.dst_vec != 0;
+  const bool staged = tr || !grouped;
   const __half* x = static_cast<const __half*>(s.x) + static_cast<size_t>(w.e) * s.mp * s.np;
+  float d[4][8];
+  if (p.decay != 0.0f) load_tile<true>(s, w, d);
   float o[4][8];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     int r, c;
     place(false, q, r, c);
     widen8(*reinterpret_cast<const uint4*>(x + static_cast<size_t>(w.r0 + r) * s.np + w.c0 + c), kViewF16, o[q]);
-    if (tr) {
+    if (staged) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) stage[r][c + i] = o[q][i];
     }
   }
+  if (staged) __syncthreads();
   const int rows = tr ? s.n : s.m, cols = tr ? s.m : s.n;  // as stored
   const int r0 = tr ? w.c0 : w.r0, c0 = tr ? w.r0 : w.c0;
-  if (tr) __syncthreads();
+  const long long at = w.e * s.dst_bs + r0 * s.dst_ld + c0;
+  if (!grouped) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      int r, c;
+      place_one(tr, i, r, c);
+      const float y = s.coef * stage[tr ? c : r][tr ? r : c];
+      o[i >> 3][i & 7] = p.decay != 0.0f ? fmaf(p.decay, d[i >> 3][i & 7], y) : y;
+    }
+    auto each = [&](auto store) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        int r, c;
+        place_one(tr, i, r, c);
+        if (r0 + r < rows && c0 + c < cols) store(at + r * s.dst_ld + c, o[i >> 3][i & 7]);
+      }
+    };
+    if (s.dst_type == kViewF32)
+      each([&](long long i, float y) { static_cast<float*>(s.dst)[i] = y; });
+    else if (s.dst_type == kViewBF16)
+      each([&](long long i, float y) { static_cast<__nv_bfloat16*>(s.dst)[i] = __float2bfloat16_rn(y); });
+    else
+      each([&](long long i, float y) { static_cast<__half*>(s.dst)[i] = __float2half_rn(y); });
+    return;
+  }
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     int r, c;
     place(tr, q, r, c);
     const int have = r0 + r < rows ? cols - (c0 + c) : 0;
-    const long long at = w.e * s.dst_bs + (r0 + r) * s.dst_ld + c0 + c;
-    if (tr) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[q][i] = stage[c + i][r];
+    for (int i = 0; i < 8; ++i) {
+      const float y = s.coef * (tr ? stage[c + i][r] : o[q][i]);
+      o[q][i] = p.decay != 0.0f ? fmaf(p.decay, d[q][i], y) : y;
     }
-    float d[8];
-    if (p.decay != 0.0f) {
-      load_eight(s.dst, s.dst_type, at, have, s.dst_vec != 0, d);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = fmaf(p.decay, d[i], s.coef * o[q][i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) d[i] = s.coef * o[q][i];
-    }
-    store_eight(s.dst, s.dst_type, at, have, s.dst_vec != 0, d);
+    store_eight(s.dst, s.dst_type, at + r * s.dst_ld + c, have, true, o[q]);
   }
 }
 

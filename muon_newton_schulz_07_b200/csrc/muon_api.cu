@@ -389,22 +389,23 @@ cudaError_t enqueue_front(muon_ctx* h, const void* const* src, void* const* mom,
   return cudaSuccess;
 }
 
+}  // namespace
+
 // Tile tables of the single-launch schedule (everything but the tensor maps, pointers and
 // hyper-parameters): Update tiles 256 x 512 when every group's padded width allows it (except in
 // the iteration that writes W), Gram and Poly two upper blocks per tile, and the first tile of
 // each (stage, group) within an iteration.
-void fused_tables(const Plan& P, int nslots, int k, bool fuse_write, NsParams* q) {
+void muon::fused_tables(const std::vector<const GroupPlan*>& groups, int nslots, int k, bool fuse_write, bool wide, NsParams* q) {
   std::memset(q, 0, sizeof(*q));
-  const int ng = static_cast<int>(P.groups.size());
-  bool wide = true;
-  for (const GroupPlan& gp : P.groups) wide = wide && gp.np % 512 == 0;
+  const int ng = static_cast<int>(groups.size());
+  for (const GroupPlan* gp : groups) wide = wide && gp->np % 512 == 0;
   q->upd_tw[0] = wide ? 512 : 256;
   q->upd_tw[1] = (wide && !fuse_write) ? 512 : 256;  // the Update that writes W keeps 256-wide tiles
   // Gram and Poly keep one 256 x 256 block per tile: two blocks per tile (256 x 512, one
   // accumulator, half of the epilogue exposed) measured 13 % (Gram) and 20 % (Poly) slower on d24
   q->sym_wide = 0;
   for (int g = 0; g < ng; ++g) {
-    const GroupPlan& gp = P.groups[g];
+    const GroupPlan& gp = *groups[g];
     NsGroup& G = q->g[g];
     G.cnt = gp.cnt;
     G.mp = gp.mp;
@@ -419,7 +420,7 @@ void fused_tables(const Plan& P, int nslots, int k, bool fuse_write, NsParams* q
     int off = 0;
     for (int kind = kGram; kind <= kUpdate; ++kind) {
       for (int g = 0; g < ng; ++g) {
-        const GroupPlan& gp = P.groups[g];
+        const GroupPlan& gp = *groups[g];
         const int T = gp.mp / 256;
         const int tpm = kind == kUpdate ? T * (gp.np / q->upd_tw[L]) : sym_tiles(T, q->sym_wide != 0);
         q->begin[L][kind][g] = off;
@@ -435,6 +436,32 @@ void fused_tables(const Plan& P, int nslots, int k, bool fuse_write, NsParams* q
   q->nslots = nslots;
   q->tiles_iter = k > 1 ? iter_tiles[0] : iter_tiles[1];
   q->total_tiles = (k - 1) * iter_tiles[0] + iter_tiles[1];
+}
+
+void muon::fused_maps(const std::vector<const GroupPlan*>& groups, NsParams* q) {
+  for (size_t g = 0; g < groups.size(); ++g) {
+    const GroupPlan& gp = *groups[g];
+    NsGroup& G = q->g[g];
+    for (int b = 0; b < 2; ++b) {
+      G.x_row[b] = gp.tm_x[b];
+      G.x_chk[b] = gp.tt_x[b];
+      G.x_st[b] = gp.ts_x[b];
+    }
+    G.a_row = gp.tm_a;
+    G.a_chk = gp.tt_a;
+    G.a_st = gp.ts_a;
+    G.b_row = gp.tm_b;
+    G.b_chk = gp.tt_b;
+    G.b_st = gp.ts_b;
+  }
+}
+
+namespace {
+
+std::vector<const GroupPlan*> all_groups(const Plan& P) {
+  std::vector<const GroupPlan*> v;
+  for (const GroupPlan& gp : P.groups) v.push_back(&gp);
+  return v;
 }
 
 // The parameter write can ride on the last Update launch when the parameters are bf16,
@@ -504,26 +531,15 @@ cudaError_t enqueue_ns(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st, i
     // every iteration in one launch: tiles of all 3k stages in one list, per-matrix counters
     NvtxRange range("muon: Newton-Schulz, every iteration in one launch");
     NsParams& q = h->ns;
-    fused_tables(P, h->n, k, fuse, &q);
-    const int ng = static_cast<int>(P.groups.size());
-    for (int g = 0; g < ng; ++g) {
-      const GroupPlan& gp = P.groups[g];
-      NsGroup& G = q.g[g];
-      for (int b = 0; b < 2; ++b) {
-        G.x_row[b] = gp.tm_x[b];
-        G.x_chk[b] = gp.tt_x[b];
-        G.x_st[b] = gp.ts_x[b];
-      }
-      G.a_row = gp.tm_a;
-      G.a_chk = gp.tt_a;
-      G.a_st = gp.ts_a;
-      G.b_row = gp.tm_b;
-      G.b_chk = gp.tt_b;
-      G.b_st = gp.ts_b;
+    const std::vector<const GroupPlan*> groups = all_groups(P);
+    fused_tables(groups, h->n, k, fuse, true, &q);
+    fused_maps(groups, &q);
+    q.gram = 1.0f;
+    for (int t = 0; t < k; ++t) {
+      q.coef[t][0] = hp->a;
+      q.coef[t][1] = hp->b;
+      q.coef[t][2] = hp->c;
     }
-    q.a = hp->a;
-    q.b = hp->b;
-    q.c = hp->c;
     q.scal = h->d_scal;
     q.status = h->d_status;
     q.deps = reinterpret_cast<unsigned int*>(h->ws + P.off_deps);
@@ -536,6 +552,7 @@ cudaError_t enqueue_ns(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st, i
           const float r = static_cast<float>(h->shapes[i].rows), c = static_cast<float>(h->shapes[i].cols);
           q.wptr[slot] = dst[i];
           q.wcoef[slot] = store_only ? 1.0f : -hp->lr * std::sqrt(std::max(1.0f, r / c));
+          q.wld[slot] = static_cast<int>(h->shapes[i].cols);
           q.wtrans[slot] = h->shapes[i].rows > h->shapes[i].cols ? 1 : 0;
         }
       }
@@ -932,7 +949,7 @@ muon_status_t muon_check_plan(const muon_shape_t* shapes, int n, int ns_steps, i
   }
   if (ns_steps >= 1 && P.groups.size() <= static_cast<size_t>(kTcMaxGroups)) {
     for (int fw = 0; fw < 2; ++fw) {
-      fused_tables(P, n, ns_steps, fw != 0, ns);
+      fused_tables(all_groups(P), n, ns_steps, fw != 0, true, ns);
       bad += check_fused_tiles(*ns);
     }
   }
@@ -947,7 +964,8 @@ muon_status_t muon_set_schedule(muon_handle_t h, int schedule) {
   if (schedule != MUON_SCHEDULE_AUTO && schedule != MUON_SCHEDULE_STAGED && schedule != MUON_SCHEDULE_FUSED &&
       schedule != MUON_SCHEDULE_SPLIT)
     return MUON_ERR_INVALID_ARG;
-  if ((schedule == MUON_SCHEDULE_FUSED || schedule == MUON_SCHEDULE_SPLIT) && !fused_possible(h, 1))
+  if ((schedule == MUON_SCHEDULE_FUSED || schedule == MUON_SCHEDULE_SPLIT) &&
+      !(h->mode == MUON_MODE_HALF ? half_fused_possible(h) : fused_possible(h, 1)))
     return MUON_ERR_UNSUPPORTED;
   h->schedule = schedule;
   return MUON_OK;

@@ -104,11 +104,18 @@ void trace_call_end(muon_ctx* h);
 // the caller's), from X buffer `cur` to `nxt`, Update tiles `tw` wide.
 void stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur, int nxt, int tw, TcGroup* G);
 
+// The single-launch schedule over these groups: tile tables (`wide`: with 256 x 512 Update tiles where
+// every padded width allows them), and tensor maps.
+void fused_tables(const std::vector<const GroupPlan*>& groups, int nslots, int k, bool fuse_write, bool wide,
+                  NsParams* q);
+void fused_maps(const std::vector<const GroupPlan*>& groups, NsParams* q);
+
 // muon_views.cu: the calls of muon_api.cu on a MUON_MODE_HALF handle
 muon_status_t half_step(muon_ctx* h, void* const* W, const void* const* G, void* const* M, const muon_hparams_t* hp,
                         cudaStream_t stream);
 muon_status_t half_orthogonalize(muon_ctx* h, const void* const* X, void* const* O, const muon_hparams_t* hp,
                                  cudaStream_t stream);
 int half_launches(const muon_ctx* h, int k);
+bool half_fused_possible(const muon_ctx* h);
 
 }  // namespace muon

@@ -412,4 +412,52 @@ template <typename T> __device__ __forceinline__ T from_f32(float x);
 template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
 template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
 
+// The 16-bit operand type of an instantiation: bf16 (MUON_MODE_FAST) or fp16 (MUON_MODE_HALF, whose
+// X, A and B' carry the power-of-two factors of muon_internal.h).
+template <bool HALF>
+struct Operand;
+template <>
+struct Operand<false> {
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack2(uint32_t q) {
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&q));
+  }
+  static __device__ __forceinline__ float widen(const uint8_t* p) {
+    return __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(p));
+  }
+  static __device__ __forceinline__ float round(float x) { return bf16_round(x); }
+};
+template <>
+struct Operand<true> {
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  static __device__ __forceinline__ float2 unpack2(uint32_t q) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&q));
+  }
+  static __device__ __forceinline__ float widen(const uint8_t* p) {
+    return __half2float(*reinterpret_cast<const __half*>(p));
+  }
+  static __device__ __forceinline__ float round(float x) { return __half2float(__float2half_rn(x)); }
+};
+template <bool HALF>
+__device__ __forceinline__ void unpack8(const uint4& q, float* v) {
+  const uint32_t* h = reinterpret_cast<const uint32_t*>(&q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = Operand<HALF>::unpack2(h[i]);
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+template <bool HALF>
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  return make_uint4(Operand<HALF>::pack2(v[0], v[1]), Operand<HALF>::pack2(v[2], v[3]),
+                    Operand<HALF>::pack2(v[4], v[5]), Operand<HALF>::pack2(v[6], v[7]));
+}
+
 }  // namespace muon

@@ -177,7 +177,9 @@ struct NsParams {
   // first tile of (stage, group) within an iteration, [other, last][stage][group];
   // [..][stage][ngroups] is the end of the stage
   int begin[2][3][kTcMaxGroups + 1];
-  float a, b, c;
+  int half;              // operands are fp16 (MUON_MODE_HALF), not bf16; X0 is normalised
+  float gram;            // A = gram * (the Gram product)
+  float coef[64][3];     // B' = coef[0] I + coef[1] A + coef[2] A A, by iteration
   const float* scal;
   unsigned int* status;
   unsigned int* deps;    // [3 k][nslots] completion counters, zero before the launch
@@ -185,6 +187,7 @@ struct NsParams {
   float w_decay;
   void* wptr[kTcMaxFused];
   float wcoef[kTcMaxFused];
+  int wld[kTcMaxFused];
   unsigned char wtrans[kTcMaxFused];
 };
 

@@ -199,11 +199,105 @@ bool result_fusable(const muon_ctx* h, const std::vector<Item>& items, int k) {
   return true;
 }
 
+std::vector<const GroupPlan*> tiled_groups(const muon_ctx* h) {
+  std::vector<const GroupPlan*> v;
+  for (const GroupPlan& gp : h->plan.groups)
+    if (!gp.skinny) v.push_back(&gp);
+  return v;
+}
+
+// 256 x 256 tiles of an Update over every group, and the CTA pairs that share them.
+long long update_tiles(const std::vector<const GroupPlan*>& groups) {
+  long long tiles = 0;
+  for (const GroupPlan* gp : groups) tiles += static_cast<long long>(gp->cnt) * (gp->mp / 256) * (gp->np / 256);
+  return tiles;
+}
+
+// Whether the k iterations of the groups that go through the workspace run as one launch.  AUTO
+// does so up to eight Update tiles a pair: there the launch boundaries (a ramp, a tail and a gap each)
+// cost more than the single launch's waits on completion counters.  Measured, five iterations,
+// one launch against one per stage: 4 x 768 x 768 207 and 242 us, 16 x 1024 x 1024 400 and 560, 48 x 768 x 768
+// 566 and 622; but 24 x 1536 x 1536 (12 tiles a pair) 1880 and 1750, 12 x 1536 x 6144 (23) 3090 and 2740.
+bool single_launch(const muon_ctx* h, int k) {
+  if (k < 1 || !half_fused_possible(h)) return false;
+  if (h->schedule != MUON_SCHEDULE_AUTO) return h->schedule != MUON_SCHEDULE_STAGED;
+  return update_tiles(tiled_groups(h)) <= 8ll * (h->num_sms / 2);
+}
+
+// 256 x 512 Update tiles only when there are more 256-wide ones than CTA pairs: below that a wide
+// tile leaves pairs idle and takes twice as long.
+bool wide_pays(const muon_ctx* h, const std::vector<const GroupPlan*>& groups) {
+  return update_tiles(groups) > h->num_sms / 2;
+}
+
+// Where the last Update writes matrix e of an item: destination, factor and layout by slot.
+template <typename Params>
+void fill_results(const muon_ctx* h, const std::vector<Item>& items, const muon_hparams_t* hp, bool store, Params* p) {
+  p->fuse_write = 1;
+  p->w_decay = store ? 0.0f : 1.0f - hp->lr * hp->weight_decay;
+  for (const Item& it : items) {
+    if (group_of(h, it.first).skinny) continue;
+    ViewSeg s;
+    fill_seg(h, it, store, hp->lr, &s);
+    for (int e = 0; e < it.count; ++e) {
+      const int slot = h->plan.scal_idx[it.first + e];
+      p->wptr[slot] = it.dst.data + static_cast<size_t>(e) * it.dst.bs * 2;
+      p->wcoef[slot] = s.coef;
+      p->wld[slot] = static_cast<int>(it.dst.ld);
+      p->wtrans[slot] = static_cast<unsigned char>(s.dst_tr);
+    }
+  }
+}
+
+// All iterations in one launch (or, for measurements, its tiles with a launch per stage).
+cudaError_t enqueue_single(muon_ctx* h, const std::vector<Item>& items, const muon_hparams_t* hp, bool store, bool fuse,
+                           cudaStream_t st) {
+  NvtxRange range("muon: Newton-Schulz, every iteration in one launch");
+  const std::vector<const GroupPlan*> groups = tiled_groups(h);
+  const int k = hp->ns_steps;
+  char* deps = h->ws + h->plan.off_deps;  // completion counters, zero before the launch
+  cudaError_t e = cudaMemsetAsync(deps, 0, sizeof(unsigned int) * 3 * k * static_cast<size_t>(h->n), st);
+  if (e != cudaSuccess) return e;
+  NsParams& q = h->ns;
+  fused_tables(groups, h->n, k, fuse, wide_pays(h, groups), &q);
+  fused_maps(groups, &q);
+  q.half = 1;
+  q.gram = kHalfA / (kHalfX * kHalfX);
+  for (int t = 0; t < k; ++t) {
+    float own[3];
+    const float* abc = coef_of(h, hp, t, own);
+    q.coef[t][0] = abc[0];
+    q.coef[t][1] = abc[1] * (1.0f / kHalfA);
+    q.coef[t][2] = abc[2] * (1.0f / (kHalfA * kHalfA));
+  }
+  q.scal = h->d_scal;
+  q.status = h->d_status;
+  q.deps = reinterpret_cast<unsigned int*>(deps);
+  q.timeout_ns = kTimeoutNs;
+  if (fuse) fill_results(h, items, hp, store, &q);
+  if (h->schedule != MUON_SCHEDULE_SPLIT) {
+    q.t_begin = 0;
+    q.t_end = q.total_tiles;
+    e = launch_ns_fused(q, h->num_sms, st);
+    if (e == cudaSuccess) trace(h, MUON_KERNEL_NS_FUSED, st);
+    return e;
+  }
+  for (int s = 0; s < 3 * k; ++s) {
+    const int it = s / 3, kind = s % 3, L = it == k - 1 ? 1 : 0;
+    q.t_begin = it * q.tiles_iter + q.begin[L][kind][0];
+    q.t_end = it * q.tiles_iter + q.begin[L][kind][q.ngroups];
+    e = launch_ns_fused(q, h->num_sms, st);
+    if (e != cudaSuccess) return e;
+    trace(h, MUON_KERNEL_GRAM + kind, st);
+  }
+  return cudaSuccess;
+}
+
 cudaError_t enqueue_tiles(muon_ctx* h, const std::vector<Item>& items, const muon_hparams_t* hp, bool store,
                           bool fuse, cudaStream_t st) {
-  std::vector<const GroupPlan*> groups;
-  for (const GroupPlan& gp : h->plan.groups)
-    if (!gp.skinny) groups.push_back(&gp);
+  const std::vector<const GroupPlan*> groups = tiled_groups(h);
+  if (groups.empty()) return cudaSuccess;
+  if (single_launch(h, hp->ns_steps)) return enqueue_single(h, items, hp, store, fuse, st);
   const int k = hp->ns_steps;
   for (int t = 0; t < k; ++t) {
     float own[3];
@@ -223,7 +317,7 @@ cudaError_t enqueue_tiles(muon_ctx* h, const std::vector<Item>& items, const muo
         const bool last = kind == kUpdate && t + 1 == k && fuse;
         // 256 x 512 Update tiles under the same rule as the bf16 path: every padded width allows
         // them and, where the launch writes the result, the k loops are long (mean m >= 2048)
-        bool wide = kind == kUpdate;
+        bool wide = kind == kUpdate && wide_pays(h, groups);
         double wsum = 0.0, wm = 0.0;
         for (int gi = 0; gi < ng; ++gi) {
           const GroupPlan& gp = *groups[g0 + gi];
@@ -241,22 +335,7 @@ cudaError_t enqueue_tiles(muon_ctx* h, const std::vector<Item>& items, const muo
           prm.c_diag = abc[0] * kHalfB;
         }
         if (kind == kUpdate) prm.c_acc = 1.0f / kHalfB;
-        if (last) {
-          prm.fuse_write = 1;
-          prm.w_decay = store ? 0.0f : 1.0f - hp->lr * hp->weight_decay;
-          for (const Item& it : items) {
-            if (group_of(h, it.first).skinny) continue;
-            ViewSeg s;
-            fill_seg(h, it, store, hp->lr, &s);
-            for (int e = 0; e < it.count; ++e) {
-              const int slot = h->plan.scal_idx[it.first + e];
-              prm.wptr[slot] = it.dst.data + static_cast<size_t>(e) * it.dst.bs * 2;
-              prm.wcoef[slot] = s.coef;
-              prm.wld[slot] = static_cast<int>(it.dst.ld);
-              prm.wtrans[slot] = static_cast<unsigned char>(s.dst_tr);
-            }
-          }
-        }
+        if (last) fill_results(h, items, hp, store, &prm);
         int tiles = 0;
         for (int gi = 0; gi < ng; ++gi) {
           TcGroup& G = prm.g[gi];
@@ -562,23 +641,29 @@ muon_status_t muon::half_step(muon_ctx* h, void* const* W, const void* const* G,
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
 
+bool muon::half_fused_possible(const muon_ctx* h) {
+  const size_t n = tiled_groups(h).size();
+  return n >= 1 && n <= static_cast<size_t>(kTcMaxGroups);
+}
+
 int muon::half_launches(const muon_ctx* h, int k) {
   // a muon_step: every matrix is a view of its own
-  int tiled = 0, tiled_groups = 0, skinny = 0;
+  int tiled = 0, ngroups = 0, skinny = 0;
   for (const GroupPlan& gp : h->plan.groups) {
     if (gp.skinny) {
       skinny += (gp.cnt + kSkinnySegs - 1) / kSkinnySegs;
     } else {
       tiled += gp.cnt;
-      ++tiled_groups;
+      ++ngroups;
     }
   }
   const int views = (tiled + kViewSegs - 1) / kViewSegs;
   bool fused = k >= 1 && h->dtype == MUON_BF16 && h->n <= kTcMaxFused;
   for (const GroupPlan& gp : h->plan.groups)
     if (!gp.skinny && (gp.m % 32 != 0 || gp.n % 32 != 0)) fused = false;
-  return (h->n + kStateSegs - 1) / kStateSegs + views + 3 * k * ((tiled_groups + kTcMaxGroups - 1) / kTcMaxGroups) +
-         (fused ? 0 : views) + skinny;
+  const int stages = single_launch(h, k) ? (h->schedule == MUON_SCHEDULE_SPLIT ? 3 * k : 1)
+                                         : 3 * k * ((ngroups + kTcMaxGroups - 1) / kTcMaxGroups);
+  return (h->n + kStateSegs - 1) / kStateSegs + views + stages + (fused ? 0 : views) + skinny;
 }
 
 extern "C" {

@@ -291,6 +291,24 @@ def test_half_is_nearer_than_fast():
     assert err["half"] * 4 <= err["fast"]
 
 
+@pytest.mark.parametrize("shapes", [[(331, 503), (7, 300, 300), (64, 128)], [(768, 512), (2, 512, 1024)], [(130, 2000)]], ids=str)
+def test_schedules_agree(shapes):
+    """One launch for every iteration, or one per stage: the same tiles and roundings, so the same bits."""
+    abc = [QUINTIC] * 2 + [SETTLE, (1.5, -0.5, 0.0)]
+    X = [random(s, torch.bfloat16, i) for i, s in enumerate(shapes)]
+    outs = []
+    for schedule in ("staged", "fused", "split", "auto"):
+        op = MuonStep(shapes, mode="half", schedule=schedule)
+        Os = [torch.empty_like(x) for x in X]
+        for _ in range(2):
+            op.orthogonalize(X, Os, abc=abc)
+        check(shapes, X, Os, abc, op, schedule)
+        outs.append(Os)
+        op.close()
+    for Os in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(Os, outs[0]))
+
+
 def test_captured_and_on_another_stream():
     shapes = [(12, 64, 96), (300, 256)]
     op = MuonStep(shapes, mode="half")
