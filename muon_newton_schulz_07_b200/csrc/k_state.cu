@@ -79,44 +79,39 @@ struct Range<kStateE4M3> {
   static constexpr float top = 448.0f;
 };
 
-// y scaled to the code's range -> the value its code stands for; r: 16 random bits.
+// Four values, scaled to the codes' range, as a word of codes; r: two words of 16 random bits each.
+// Conversions between integers and floats and floor() run at a quarter of the rate of an addition, so
+// they are additions here: adding 2^23 leaves an integer in the low bits, rounded as the addition is.
 template <int F, bool STOCHASTIC>
-__device__ __forceinline__ float to_grid(float y, uint32_t r) {
-  if (F == kStateInt8) {
-    if (!STOCHASTIC) return y;  // the conversion rounds
-    return fminf(fmaxf(floorf(__fadd_rn(y, static_cast<float>(r) * 0x1p-16f)), -127.0f), 127.0f);
-  }
-  if (!STOCHASTIC) return y;
-  const float size = fabsf(y);
-  // three bits stay below the leading one: add below the last kept bit, cut the rest off
-  const float normal = __uint_as_float((__float_as_uint(size) + (r << 4)) & ~0xFFFFFu);
-  const float small = floorf(__fadd_rn(size * 512.0f, static_cast<float>(r) * 0x1p-16f)) * 0x1p-9f;
-  return copysignf(fminf(size >= 0x1p-6f ? normal : small, 448.0f), y);
-}
-// four grid values (or, to nearest, four scaled values) as one word of codes
-template <int F>
-__device__ __forceinline__ uint32_t codes4(const float* y) {
-  if (F == kStateInt8) {
-    uint32_t b[4];
+__device__ __forceinline__ uint32_t encode4(const float* y, const uint32_t (&r)[2]) {
+  uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__fadd_rn(y[i], 12582912.0f));  // 1.5 * 2^23: rounds to even
-    return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t bits = (i & 1) ? r[i >> 1] >> 16 : r[i >> 1] & 0xFFFFu;
+    const float u = STOCHASTIC ? __fsub_rn(__uint_as_float(0x3F800000u | bits << 7), 1.0f) : 0.0f;  // bits / 2^16
+    if (F == kStateInt8) {
+      if (STOCHASTIC)
+        b[i] = __float_as_uint(__fadd_rd(fminf(fmaxf(__fadd_rn(y[i], u), -127.0f), 127.0f), 12582912.0f));
+      else
+        b[i] = __float_as_uint(__fadd_rn(y[i], 12582912.0f));  // 1.5 * 2^23: negative values too
+    } else if (STOCHASTIC) {
+      // e4m3 by its bits: the exponent rebiased from 127 to 7 and three bits below the leading one
+      // (add below the last kept bit, cut the rest off), multiples of 2^-9 below 2^-6; 126 is 448
+      const uint32_t size = __float_as_uint(y[i]) & 0x7FFFFFFFu;
+      const uint32_t normal = min((size + (bits << 4) - (120u << 23)) >> 20, 126u);
+      const uint32_t small = __float_as_uint(__fadd_rd(__fmaf_rn(__uint_as_float(size), 512.0f, u), 8388608.0f));
+      b[i] = (size >= 0x3C800000u ? normal : small & 0xFFu) | (__float_as_uint(y[i]) >> 31 << 7);
+    }
   }
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
-  return lo | hi << 16;
+  if (F == kStateE4M3 && !STOCHASTIC) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | hi << 16;
+  }
+  return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
 }
 
-// The 16 lanes of a unit agree on the largest magnitude (as bits: NaN above infinity above all) ...
-__device__ __forceinline__ uint32_t unit_top(const float (&x)[8]) {
-  uint32_t t = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-#pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) t = max(t, __shfl_xor_sync(0xffffffffu, t, o));
-  return t;
-}
-// ... and so on the factor and the scale.
+// Factor and scale of a block from its largest magnitude (as bits: NaN above infinity above all).
 template <int F>
 __device__ __forceinline__ void unit_scale(uint32_t top_bits, float& mul, float& scale) {
   const float t = __uint_as_float(top_bits);
@@ -133,11 +128,8 @@ __device__ __forceinline__ void unit_scale(uint32_t top_bits, float& mul, float&
 // ---------------------------------------------------------------- units
 
 struct Unit {
-  bool live;
   int row, col;        // the unit's row, its first column
-  int lane, have;      // lane of the unit; values of the unit
-  long long code_at;   // of the unit's first value, in the codes of the stack
-  long long scale_at;
+  int have;            // values of the unit (0: beyond the matrix)
 };
 struct Cta {
   int seg, e;
@@ -158,18 +150,32 @@ __device__ __forceinline__ Cta find(const StateParams& p) {
   c.first = static_cast<uint32_t>(at - c.e * s.unit_ctas) * kStateUnits;
   return c;
 }
-__device__ __forceinline__ Unit unit_of(const StateSeg& s, const Cta& c, int pass) {
-  Unit u;
-  const uint32_t at = c.first + pass * (THREADS / LANES) + (threadIdx.x / LANES);  // below 2^31 + 64
-  u.lane = threadIdx.x % LANES;
-  u.row = static_cast<int>(at / static_cast<uint32_t>(s.blocks));
-  u.live = u.row < s.rows;
-  u.col = static_cast<int>(at - static_cast<uint32_t>(u.row) * s.blocks) * kStateBlock;
-  u.have = u.live ? min(kStateBlock, s.cols - u.col) : 0;
-  const long long row = static_cast<long long>(c.e) * s.rows + u.row;
-  u.code_at = row * s.cols + u.col;
-  u.scale_at = static_cast<long long>(c.e) * s.rows * s.blocks + at;
-  return u;
+constexpr int UNITS = THREADS / LANES;  // of a pass
+// The units of this thread's 16 lanes, one a pass: one division, then steps of UNITS.
+__device__ __forceinline__ void units_of(const StateSeg& s, const Cta& c, Unit (&u)[PASSES]) {
+  const uint32_t at = c.first + threadIdx.x / LANES;  // below 2^31 + 64
+  uint32_t row = at / static_cast<uint32_t>(s.blocks), block = at - row * s.blocks;
+  const uint32_t rows = UNITS / static_cast<uint32_t>(s.blocks), blocks = UNITS - rows * s.blocks;
+#pragma unroll
+  for (int q = 0; q < PASSES; ++q) {
+    u[q].row = static_cast<int>(row);
+    u[q].col = static_cast<int>(block) * kStateBlock;
+    u[q].have = row < static_cast<uint32_t>(s.rows) ? min(kStateBlock, s.cols - u[q].col) : 0;
+    row += rows;
+    block += blocks;
+    if (block >= static_cast<uint32_t>(s.blocks)) {
+      block -= s.blocks;
+      ++row;
+    }
+  }
+}
+__device__ __forceinline__ int unit_lane() { return threadIdx.x % LANES; }
+// Of a unit's first value in the codes of the stack, and of its scale.
+__device__ __forceinline__ long long code_at(const StateSeg& s, const Cta& c, const Unit& u) {
+  return (static_cast<long long>(c.e) * s.rows + u.row) * s.cols + u.col;
+}
+__device__ __forceinline__ long long scale_at(const StateSeg& s, const Cta& c, const Unit& u) {
+  return (static_cast<long long>(c.e) * s.rows + u.row) * s.blocks + u.col / kStateBlock;
 }
 // Value i of a lane sits at this place of the unit: eight neighbours, or interleaved lanes.
 __device__ __forceinline__ int place(bool vec, int lane, int i) { return vec ? lane * 8 + i : lane + LANES * i; }
@@ -228,49 +234,76 @@ struct TypeOf<__half> { static constexpr int id = kViewF16; };
 // Store a lane's eight values.
 template <typename T>
 __device__ __forceinline__ void store_unit(T* base, bool vec, const Unit& u, const float (&x)[8]) {
+  const int lane = unit_lane();
   if (vec) {
-    if (u.lane * 8 < u.have) store_eight(base, TypeOf<T>::id, u.lane * 8, 8, true, x);
+    if (lane * 8 < u.have) store_eight(base, TypeOf<T>::id, lane * 8, 8, true, x);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = place(false, u.lane, i);
+      const int at = place(false, lane, i);
       if (at < u.have) store_one(base, TypeOf<T>::id, at, x[i]);
     }
   }
 }
 
-// Codes of a lane's eight values, to memory.
+// Write the four units of these 16 lanes.  The largest magnitudes of all four go through one
+// exchange: each step halves the units a lane still holds, so that quarter q of the lanes ends with
+// unit q's, divides once, and hands factor and scale back.
 template <int F, bool STOCHASTIC>
-__device__ __forceinline__ void write_unit(const StateSeg& s, bool vec, const Unit& u, uint32_t key, float (&x)[8]) {
-  float mul, scale;
-  const uint32_t top = unit_top(x);
-  unit_scale<F>(top, mul, scale);
-  const bool fine = top < 0x7F800000u;
-  uint8_t* codes = static_cast<uint8_t*>(s.codes) + u.code_at;
-  const unsigned long long at = static_cast<unsigned long long>(u.row) * s.cols + u.col;  // within the matrix
-  uint32_t r = 0;
+__device__ __forceinline__ void write_units(const StateSeg& s, const Cta& c, bool vec, const Unit (&u)[PASSES],
+                                            uint32_t key, float (&x)[PASSES][8]) {
+  const int lane = unit_lane();
+  uint32_t top[PASSES];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float y = fine ? __fmul_rn(x[i], mul) : 0.0f;
+  for (int q = 0; q < PASSES; ++q) {
+    top[q] = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top[q] = max(top[q], __float_as_uint(x[q][i]) & 0x7FFFFFFFu);
+  }
+  const bool hi8 = lane & 8, hi4 = lane & 4;
+  uint32_t a = hi8 ? top[2] : top[0], b = hi8 ? top[3] : top[1];
+  a = max(a, __shfl_xor_sync(0xffffffffu, hi8 ? top[0] : top[2], 8));
+  b = max(b, __shfl_xor_sync(0xffffffffu, hi8 ? top[1] : top[3], 8));
+  uint32_t t = max(hi4 ? b : a, __shfl_xor_sync(0xffffffffu, hi4 ? a : b, 4));
+  t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
+  t = max(t, __shfl_xor_sync(0xffffffffu, t, 1));
+  float my_mul, my_scale;
+  unit_scale<F>(t, my_mul, my_scale);
+#pragma unroll
+  for (int q = 0; q < PASSES; ++q) {
+    const float mul = __shfl_sync(0xffffffffu, my_mul, q * 4, LANES);
+    const bool fine = __shfl_sync(0xffffffffu, t, q * 4, LANES) < 0x7F800000u;
+    if (lane == q * 4 && u[q].have > 0) s.scales[scale_at(s, c, u[q])] = my_scale;
+    uint8_t* codes = static_cast<uint8_t*>(s.codes) + code_at(s, c, u[q]);
+    const unsigned long long at = static_cast<unsigned long long>(u[q].row) * s.cols + u[q].col;  // in the matrix
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[q][i] = fine ? __fmul_rn(x[q][i], mul) : 0.0f;
+    uint32_t r[4] = {0, 0, 0, 0};
     if (STOCHASTIC) {
-      const unsigned long long here = at + place(vec, u.lane, i);
-      if (!vec) r = pair_bits(key, here >> 1) >> (16 * (here & 1));
-      else if ((i & 1) == 0) r = pair_bits(key, here >> 1);  // the unit starts at an even place
-      else r >>= 16;
-    }
-    x[i] = to_grid<F, STOCHASTIC>(y, r & 0xFFFFu);
-  }
-  const uint32_t lo = codes4<F>(x), hi = codes4<F>(x + 4);
-  if (vec) {
-    if (u.lane * 8 < u.have) __stcs(reinterpret_cast<uint2*>(codes + u.lane * 8), make_uint2(lo, hi));
-  } else {
+      if (vec) {  // eight neighbours from an even place: four pairs
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int to = place(false, u.lane, i);
-      if (to < u.have) codes[to] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        for (int i = 0; i < 4; ++i) r[i] = pair_bits(key, (at + lane * 8) / 2 + i);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const unsigned long long here = at + place(false, lane, i);
+          const uint32_t h = pair_bits(key, here >> 1) >> (16 * (here & 1)) & 0xFFFFu;
+          r[i >> 1] |= h << (16 * (i & 1));
+        }
+      }
+    }
+    const uint32_t r0[2] = {r[0], r[1]}, r1[2] = {r[2], r[3]};
+    const uint32_t lo = encode4<F, STOCHASTIC>(x[q], r0), hi = encode4<F, STOCHASTIC>(x[q] + 4, r1);
+    if (vec) {
+      if (lane * 8 < u[q].have) __stcs(reinterpret_cast<uint2*>(codes + lane * 8), make_uint2(lo, hi));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int to = place(false, lane, i);
+        if (to < u[q].have) codes[to] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
+      }
     }
   }
-  if (u.live && u.lane == 0) s.scales[u.scale_at] = scale;
 }
 
 // The codes of a lane's eight values, as loaded.
@@ -278,20 +311,21 @@ struct Codes {
   uint32_t w[2];
   float scale;
 };
-__device__ __forceinline__ void load_codes(const StateSeg& s, bool vec, const Unit& u, Codes& c) {
-  const uint8_t* p = static_cast<const uint8_t*>(s.codes) + u.code_at;
+__device__ __forceinline__ void load_codes(const StateSeg& s, const Cta& cta, bool vec, const Unit& u, Codes& c) {
+  const int lane = unit_lane();
+  const uint8_t* p = static_cast<const uint8_t*>(s.codes) + code_at(s, cta, u);
   c.w[0] = c.w[1] = 0;
-  c.scale = u.live ? s.scales[u.scale_at] : 0.0f;
+  c.scale = u.have > 0 ? s.scales[scale_at(s, cta, u)] : 0.0f;
   if (vec) {
-    if (u.lane * 8 < u.have) {
-      const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p + u.lane * 8));
+    if (lane * 8 < u.have) {
+      const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p + lane * 8));
       c.w[0] = q.x;
       c.w[1] = q.y;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = place(false, u.lane, i);
+      const int at = place(false, lane, i);
       if (at < u.have) c.w[i >> 2] |= static_cast<uint32_t>(p[at]) << (8 * (i & 3));
     }
   }
@@ -311,12 +345,13 @@ template <typename T>
 __device__ __forceinline__ void load_values(const T* base, bool vec, const Unit& u, Eight<T>& x) {
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(x) / 4); ++i) reinterpret_cast<uint32_t*>(&x)[i] = 0;
+  const int lane = unit_lane();
   if (vec) {
-    if (u.lane * 8 < u.have) x.load(base + u.lane * 8);  // rows are multiples of 8: all or nothing
+    if (lane * 8 < u.have) x.load(base + lane * 8);  // rows are multiples of 8: all or nothing
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = place(false, u.lane, i);
+      const int at = place(false, lane, i);
       if (at < u.have) x.set(i, base + at);
     }
   }
@@ -337,19 +372,15 @@ __global__ void __launch_bounds__(THREADS) state_quantize_kernel(const __grid_co
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
   const uint32_t key = STOCHASTIC ? matrix_key(p.seed, static_cast<uint32_t>(s.mat_begin + c.e)) : 0u;
+  Unit u[PASSES];
+  units_of(s, c, u);
   Eight<T> raw[PASSES];
 #pragma unroll
-  for (int q = 0; q < PASSES; ++q) {
-    const Unit u = unit_of(s, c, q);
-    load_values<T>(in_row<T>(s, c, u), vec, u, raw[q]);
-  }
+  for (int q = 0; q < PASSES; ++q) load_values<T>(in_row<T>(s, c, u[q]), vec, u[q], raw[q]);
+  float x[PASSES][8];
 #pragma unroll
-  for (int q = 0; q < PASSES; ++q) {
-    const Unit u = unit_of(s, c, q);
-    float x[8];
-    raw[q].widen(x);
-    write_unit<F, STOCHASTIC>(s, vec, u, key, x);
-  }
+  for (int q = 0; q < PASSES; ++q) raw[q].widen(x[q]);
+  write_units<F, STOCHASTIC>(s, c, vec, u, key, x);
 }
 
 template <typename T, int F>
@@ -357,15 +388,16 @@ __global__ void __launch_bounds__(THREADS) state_dequantize_kernel(const __grid_
   const Cta c = find(p);
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
+  Unit u[PASSES];
+  units_of(s, c, u);
   Codes raw[PASSES];
 #pragma unroll
-  for (int q = 0; q < PASSES; ++q) load_codes(s, vec, unit_of(s, c, q), raw[q]);
+  for (int q = 0; q < PASSES; ++q) load_codes(s, c, vec, u[q], raw[q]);
 #pragma unroll
   for (int q = 0; q < PASSES; ++q) {
-    const Unit u = unit_of(s, c, q);
     float x[8];
     read_codes<F>(raw[q], x);
-    store_unit<T>(out_row<T>(s, c, u), vec, u, x);
+    store_unit<T>(out_row<T>(s, c, u[q]), vec, u[q], x);
   }
 }
 
@@ -373,46 +405,46 @@ __global__ void __launch_bounds__(THREADS) state_dequantize_kernel(const __grid_
 template <typename T, int F, bool STOCHASTIC>
 __global__ void __launch_bounds__(THREADS) state_momentum_kernel(const __grid_constant__ StateParams p) {
   __shared__ float red[THREADS / 32];
+  constexpr bool DENSE = F == kStateDense;
   const Cta c = find(p);
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
   const uint32_t key = STOCHASTIC ? matrix_key(p.seed, static_cast<uint32_t>(s.mat_begin + c.e)) : 0u;
   const float beta = p.beta, rest = __fsub_rn(1.0f, p.beta);
+  Unit u[PASSES];
+  units_of(s, c, u);
   Eight<T> raw[PASSES];
-  Codes codes[F == kStateDense ? 1 : PASSES];
-  Eight<T> dense[F == kStateDense ? PASSES : 1];
+  Codes codes[DENSE ? 1 : PASSES];
+  Eight<T> dense[DENSE ? PASSES : 1];
 #pragma unroll
   for (int q = 0; q < PASSES; ++q) {
-    const Unit u = unit_of(s, c, q);
-    load_values<T>(in_row<T>(s, c, u), vec, u, raw[q]);
-    if (F == kStateDense)
-      load_values<T>(static_cast<const T*>(s.codes) + u.code_at, vec, u, dense[F == kStateDense ? q : 0]);
+    load_values<T>(in_row<T>(s, c, u[q]), vec, u[q], raw[q]);
+    if (DENSE)
+      load_values<T>(static_cast<const T*>(s.codes) + code_at(s, c, u[q]), vec, u[q], dense[DENSE ? q : 0]);
     else
-      load_codes(s, vec, u, codes[F == kStateDense ? 0 : q]);
+      load_codes(s, c, vec, u[q], codes[DENSE ? 0 : q]);
   }
   float ss = 0.0f;
+  float m[PASSES][8];
 #pragma unroll
   for (int q = 0; q < PASSES; ++q) {
-    const Unit u = unit_of(s, c, q);
-    float g[8], m[8];
+    float g[8];
     raw[q].widen(g);
-    if (F == kStateDense)
-      dense[F == kStateDense ? q : 0].widen(m);
+    if (DENSE)
+      dense[DENSE ? q : 0].widen(m[q]);
     else
-      read_codes<F == kStateDense ? kStateInt8 : F>(codes[F == kStateDense ? 0 : q], m);
+      read_codes<DENSE ? kStateInt8 : F>(codes[DENSE ? 0 : q], m[q]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       g[i] = __fmul_rn(g[i], rest);
-      m[i] = __fadd_rn(__fmul_rn(m[i], beta), g[i]);
-      g[i] = p.nesterov ? __fadd_rn(g[i], __fmul_rn(m[i], beta)) : m[i];
+      m[q][i] = __fadd_rn(__fmul_rn(m[q][i], beta), g[i]);
+      g[i] = p.nesterov ? __fadd_rn(g[i], __fmul_rn(m[q][i], beta)) : m[q][i];
       ss = fmaf(g[i], g[i], ss);
     }
-    store_unit<T>(out_row<T>(s, c, u), vec, u, g);
-    if (F == kStateDense)
-      store_unit<T>(static_cast<T*>(s.codes) + u.code_at, vec, u, m);
-    else
-      write_unit<F == kStateDense ? kStateInt8 : F, STOCHASTIC>(s, vec, u, key, m);
+    store_unit<T>(out_row<T>(s, c, u[q]), vec, u[q], g);
+    if (DENSE) store_unit<T>(static_cast<T*>(s.codes) + code_at(s, c, u[q]), vec, u[q], m[q]);
   }
+  if (!DENSE) write_units<DENSE ? kStateInt8 : F, STOCHASTIC>(s, c, vec, u, key, m);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
