@@ -80,35 +80,49 @@ struct Range<kStateE4M3> {
 };
 
 // Four values, scaled to the codes' range, as a word of codes; r: two words of 16 random bits each.
-// Conversions between integers and floats and floor() run at a quarter of the rate of an addition, so
-// they are additions here: adding 2^23 leaves an integer in the low bits, rounded as the addition is.
+// The kernels that round stochastically are bound by the integer and logic pipe, whose rate is half
+// of the FMA pipe's (and conversions and floor() run at a quarter): so the random bits become a float by one
+// byte permutation and an addition, and rounding down is an addition that rounds down.
 template <int F, bool STOCHASTIC>
 __device__ __forceinline__ uint32_t encode4(const float* y, const uint32_t (&r)[2]) {
   uint32_t b[4];
+  float g[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t bits = (i & 1) ? r[i >> 1] >> 16 : r[i >> 1] & 0xFFFFu;
-    const float u = STOCHASTIC ? __fsub_rn(__uint_as_float(0x3F800000u | bits << 7), 1.0f) : 0.0f;  // bits / 2^16
+    // 2^23 + the 16 bits, as the bits of a float
+    const float bits = STOCHASTIC ? __uint_as_float(__byte_perm(r[i >> 1], 0x4B000000u, (i & 1) ? 0x7632 : 0x7610)) : 0.0f;
+    const float u = STOCHASTIC ? __fsub_rn(bits, 8388608.0f) : 0.0f;  // 2^16 u
     if (F == kStateInt8) {
       if (STOCHASTIC)
-        b[i] = __float_as_uint(__fadd_rd(fminf(fmaxf(__fadd_rn(y[i], u), -127.0f), 127.0f), 12582912.0f));
+        b[i] = __float_as_uint(__fadd_rd(fminf(fmaxf(__fmaf_rn(u, 0x1p-16f, y[i]), -127.0f), 127.0f), 12582912.0f));
       else
         b[i] = __float_as_uint(__fadd_rn(y[i], 12582912.0f));  // 1.5 * 2^23: negative values too
     } else if (STOCHASTIC) {
-      // e4m3 by its bits: the exponent rebiased from 127 to 7 and three bits below the leading one
-      // (add below the last kept bit, cut the rest off), multiples of 2^-9 below 2^-6; 126 is 448
-      const uint32_t size = __float_as_uint(y[i]) & 0x7FFFFFFFu;
-      const uint32_t normal = min((size + (bits << 4) - (120u << 23)) >> 20, 126u);
-      const uint32_t small = __float_as_uint(__fadd_rd(__fmaf_rn(__uint_as_float(size), 512.0f, u), 8388608.0f));
-      b[i] = (size >= 0x3C800000u ? normal : small & 0xFFu) | (__float_as_uint(y[i]) >> 31 << 7);
+      // The spacing at |y| is an eighth of its binade, and of 2^-6 below that.  |y| + u spacing is exact
+      // (or passes into the next binade, whose first code it then is), and adding 2^23 spacings,
+      // rounded down, and taking them off again leaves whole spacings.
+      const uint32_t bits_y = __float_as_uint(y[i]);
+      const float binade = __uint_as_float(max(bits_y & 0x7F800000u, 0x3C800000u));
+      const float z = __fmaf_rn(u, binade * 0x1p-19f, fabsf(y[i]));
+      const float v = __fsub_rn(__fadd_rd(z, binade * 0x1p20f), binade * 0x1p20f);
+      g[i] = __uint_as_float(__float_as_uint(v) | (bits_y & 0x80000000u));
+    } else {
+      g[i] = y[i];
     }
   }
-  if (F == kStateE4M3 && !STOCHASTIC) {
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(y[0], y[1]), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(y[2], y[3]), __NV_SATFINITE, __NV_E4M3);
+  if (F == kStateE4M3) {  // exact for values on the grid; 448 is the largest
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(g[0], g[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(g[2], g[3]), __NV_SATFINITE, __NV_E4M3);
     return lo | hi << 16;
   }
   return __byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410);
+}
+
+// max(a, |b|), NaN above all.
+__device__ __forceinline__ float max_size(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
 }
 
 // Factor and scale of a block from its largest magnitude (as bits: NaN above infinity above all).
@@ -256,9 +270,10 @@ __device__ __forceinline__ void write_units(const StateSeg& s, const Cta& c, boo
   uint32_t top[PASSES];
 #pragma unroll
   for (int q = 0; q < PASSES; ++q) {
-    top[q] = 0;
+    float m = fabsf(x[q][0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top[q] = max(top[q], __float_as_uint(x[q][i]) & 0x7FFFFFFFu);
+    for (int i = 1; i < 8; ++i) m = max_size(m, x[q][i]);
+    top[q] = __float_as_uint(m) & 0x7FFFFFFFu;
   }
   const bool hi8 = lane & 8, hi4 = lane & 4;
   uint32_t a = hi8 ? top[2] : top[0], b = hi8 ? top[3] : top[1];
@@ -277,7 +292,11 @@ __device__ __forceinline__ void write_units(const StateSeg& s, const Cta& c, boo
     uint8_t* codes = static_cast<uint8_t*>(s.codes) + code_at(s, c, u[q]);
     const unsigned long long at = static_cast<unsigned long long>(u[q].row) * s.cols + u[q].col;  // in the matrix
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[q][i] = fine ? __fmul_rn(x[q][i], mul) : 0.0f;
+    for (int i = 0; i < 8; ++i) x[q][i] = __fmul_rn(x[q][i], mul);
+    if (!fine) {  // rare: not finite
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[q][i] = 0.0f;
+    }
     uint32_t r[4] = {0, 0, 0, 0};
     if (STOCHASTIC) {
       if (vec) {  // eight neighbours from an even place: four pairs
