@@ -115,7 +115,7 @@ def lib() -> ctypes.CDLL:
         L.muon_profile_end.restype = st
         L.muon_set_schedule.argtypes = [_VP, ctypes.c_int]
         L.muon_set_schedule.restype = st
-        views, states, hpp = ctypes.POINTER(View), ctypes.POINTER(State), ctypes.POINTER(HParams)
+        views, states, hpp = _VP, _VP, ctypes.POINTER(HParams)  # arrays of View and State (see views, states)
         seed = ctypes.POINTER(ctypes.c_uint32)
         L.muon_set_coefficients.argtypes = [_VP, ctypes.POINTER(ctypes.c_float), ctypes.c_int]
         L.muon_set_coefficients.restype = st

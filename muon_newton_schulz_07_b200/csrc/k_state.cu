@@ -45,9 +45,9 @@ __host__ __device__ __forceinline__ uint32_t mixed(uint32_t h) {
   return h;
 }
 __device__ __forceinline__ uint32_t matrix_key(uint32_t seed, uint32_t matrix) { return mixed(mixed(seed) ^ matrix); }
-// The 32 bits that places 2 pair and 2 pair + 1 of a matrix share, the lower half first.
-__device__ __forceinline__ uint32_t pair_bits(uint32_t key, unsigned long long pair) {
-  return mixed(static_cast<uint32_t>(pair) + key + static_cast<uint32_t>(pair >> 32) * 0x9E3779B1u);
+// The 32 bits that places 2 pair and 2 pair + 1 of a matrix share, the lower half first: mixed(...) of
+__device__ __forceinline__ uint32_t pair_counter(uint32_t key, unsigned long long pair) {
+  return static_cast<uint32_t>(pair) + key + static_cast<uint32_t>(pair >> 32) * 0x9E3779B1u;
 }
 
 // ---------------------------------------------------------------- codes
@@ -89,12 +89,13 @@ __device__ __forceinline__ uint32_t encode4(const float* y, const uint32_t (&r)[
   float g[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    // 2^23 + the 16 bits, as the bits of a float
-    const float bits = STOCHASTIC ? __uint_as_float(__byte_perm(r[i >> 1], 0x4B000000u, (i & 1) ? 0x7632 : 0x7610)) : 0.0f;
-    const float u = STOCHASTIC ? __fsub_rn(bits, 8388608.0f) : 0.0f;  // 2^16 u
+    // the 16 bits below the leading one of 2^7 (int8) or 2^-16 (e4m3): taking that off leaves u, or 2^-23 u
+    constexpr uint32_t one = F == kStateInt8 ? 0x43000000u : 0x37800000u;
+    const uint32_t bits = STOCHASTIC ? __byte_perm(r[i >> 1], one, (i & 1) ? 0x7632 : 0x7610) : one;
+    const float u = STOCHASTIC ? __fsub_rn(__uint_as_float(bits), __uint_as_float(one)) : 0.0f;
     if (F == kStateInt8) {
       if (STOCHASTIC)
-        b[i] = __float_as_uint(__fadd_rd(fminf(fmaxf(__fmaf_rn(u, 0x1p-16f, y[i]), -127.0f), 127.0f), 12582912.0f));
+        b[i] = __float_as_uint(__fadd_rd(fminf(fmaxf(__fadd_rn(y[i], u), -127.0f), 127.0f), 12582912.0f));
       else
         b[i] = __float_as_uint(__fadd_rn(y[i], 12582912.0f));  // 1.5 * 2^23: negative values too
     } else if (STOCHASTIC) {
@@ -102,9 +103,9 @@ __device__ __forceinline__ uint32_t encode4(const float* y, const uint32_t (&r)[
       // (or passes into the next binade, whose first code it then is), and adding 2^23 spacings,
       // rounded down, and taking them off again leaves whole spacings.
       const uint32_t bits_y = __float_as_uint(y[i]);
-      const float binade = __uint_as_float(max(bits_y & 0x7F800000u, 0x3C800000u));
-      const float z = __fmaf_rn(u, binade * 0x1p-19f, fabsf(y[i]));
-      const float v = __fsub_rn(__fadd_rd(z, binade * 0x1p20f), binade * 0x1p20f);
+      const float whole = __uint_as_float(max(bits_y & 0x7F800000u, 0x3C800000u)) * 0x1p20f;  // 2^23 spacings
+      const float z = __fmaf_rn(u, whole, fabsf(y[i]));
+      const float v = __fsub_rn(__fadd_rd(z, whole), whole);
       g[i] = __uint_as_float(__float_as_uint(v) | (bits_y & 0x80000000u));
     } else {
       g[i] = y[i];
@@ -141,10 +142,6 @@ __device__ __forceinline__ void unit_scale(uint32_t top_bits, float& mul, float&
 
 // ---------------------------------------------------------------- units
 
-struct Unit {
-  int row, col;        // the unit's row, its first column
-  int have;            // values of the unit (0: beyond the matrix)
-};
 struct Cta {
   int seg, e;
   uint32_t first;      // first unit of this CTA in its matrix
@@ -164,33 +161,70 @@ __device__ __forceinline__ Cta find(const StateParams& p) {
   c.first = static_cast<uint32_t>(at - c.e * s.unit_ctas) * kStateUnits;
   return c;
 }
-constexpr int UNITS = THREADS / LANES;  // of a pass
-// The units of this thread's 16 lanes, one a pass: one division, then steps of UNITS.
-__device__ __forceinline__ void units_of(const StateSeg& s, const Cta& c, Unit (&u)[PASSES]) {
-  const uint32_t at = c.first + threadIdx.x / LANES;  // below 2^31 + 64
-  uint32_t row = at / static_cast<uint32_t>(s.blocks), block = at - row * s.blocks;
-  const uint32_t rows = UNITS / static_cast<uint32_t>(s.blocks), blocks = UNITS - rows * s.blocks;
+__device__ __forceinline__ int unit_lane() { return threadIdx.x % LANES; }
+constexpr uint32_t UNITS = THREADS / LANES;  // of a pass
+
+// Where the units of this thread's 16 lanes are, one a pass.  LINEAR: rows are whole blocks and every
+// side is contiguous, so unit i of a matrix is its values 128 i .. everywhere; a pass is a constant
+// further on, and passes beyond the matrix work on its last unit again without storing.  Otherwise
+// the row and column of a unit: one division, then steps.
+template <bool LINEAR>
+struct Sites {
+  uint32_t unit0, total;                        // LINEAR
+  int row[LINEAR ? 1 : PASSES], col[LINEAR ? 1 : PASSES], vals[LINEAR ? 1 : PASSES];
+  const StateSeg& s;
+  const Cta& c;
+  __device__ __forceinline__ Sites(const StateSeg& seg, const Cta& cta) : s(seg), c(cta) {
+    unit0 = cta.first + threadIdx.x / LANES;  // below 2^31 + 64
+    if (LINEAR) {
+      total = static_cast<uint32_t>(s.rows) * s.blocks;
+      return;
+    }
+    uint32_t r = unit0 / static_cast<uint32_t>(s.blocks), block = unit0 - r * s.blocks;
+    const uint32_t rows = UNITS / static_cast<uint32_t>(s.blocks), blocks = UNITS - rows * s.blocks;
 #pragma unroll
-  for (int q = 0; q < PASSES; ++q) {
-    u[q].row = static_cast<int>(row);
-    u[q].col = static_cast<int>(block) * kStateBlock;
-    u[q].have = row < static_cast<uint32_t>(s.rows) ? min(kStateBlock, s.cols - u[q].col) : 0;
-    row += rows;
-    block += blocks;
-    if (block >= static_cast<uint32_t>(s.blocks)) {
-      block -= s.blocks;
-      ++row;
+    for (int q = 0; q < (LINEAR ? 0 : PASSES); ++q) {
+      row[LINEAR ? 0 : q] = static_cast<int>(r);
+      col[LINEAR ? 0 : q] = static_cast<int>(block) * kStateBlock;
+      vals[LINEAR ? 0 : q] = r < static_cast<uint32_t>(s.rows) ? min(kStateBlock, s.cols - static_cast<int>(block) * kStateBlock) : 0;
+      r += rows;
+      block += blocks;
+      if (block >= static_cast<uint32_t>(s.blocks)) {
+        block -= s.blocks;
+        ++r;
+      }
     }
   }
-}
-__device__ __forceinline__ int unit_lane() { return threadIdx.x % LANES; }
-// Of a unit's first value in the codes of the stack, and of its scale.
-__device__ __forceinline__ long long code_at(const StateSeg& s, const Cta& c, const Unit& u) {
-  return (static_cast<long long>(c.e) * s.rows + u.row) * s.cols + u.col;
-}
-__device__ __forceinline__ long long scale_at(const StateSeg& s, const Cta& c, const Unit& u) {
-  return (static_cast<long long>(c.e) * s.rows + u.row) * s.blocks + u.col / kStateBlock;
-}
+  __device__ __forceinline__ uint32_t unit(int q) const { return min(unit0 + q * UNITS, total - 1); }
+  // values of the unit that exist (0: beyond the matrix)
+  __device__ __forceinline__ int have(int q) const {
+    return LINEAR ? (unit0 + q * UNITS < total ? kStateBlock : 0) : vals[LINEAR ? 0 : q];
+  }
+  // of the unit's first value: within the matrix, in the codes of the stack, and its scale
+  __device__ __forceinline__ unsigned long long place_of(int q) const {
+    return LINEAR ? static_cast<unsigned long long>(unit(q)) * kStateBlock
+                  : static_cast<unsigned long long>(row[LINEAR ? 0 : q]) * s.cols + col[LINEAR ? 0 : q];
+  }
+  __device__ __forceinline__ long long code_at(int q) const {
+    return static_cast<long long>(c.e) * s.rows * s.cols + place_of(q);
+  }
+  __device__ __forceinline__ long long scale_at(int q) const {
+    return static_cast<long long>(c.e) * s.rows * s.blocks +
+           (LINEAR ? unit(q) : static_cast<long long>(row[LINEAR ? 0 : q]) * s.blocks + col[LINEAR ? 0 : q] / kStateBlock);
+  }
+  __device__ __forceinline__ long long value_at(int q, long long ld, long long bs) const {
+    return LINEAR ? c.e * bs + static_cast<long long>(unit(q)) * kStateBlock
+                  : c.e * bs + row[LINEAR ? 0 : q] * ld + col[LINEAR ? 0 : q];
+  }
+  template <typename T>
+  __device__ __forceinline__ const T* in(int q) const {
+    return static_cast<const T*>(s.in) + value_at(q, s.in_ld, s.in_bs);
+  }
+  template <typename T>
+  __device__ __forceinline__ T* out(int q) const {
+    return static_cast<T*>(s.out) + value_at(q, s.out_ld, s.out_bs);
+  }
+};
 // Value i of a lane sits at this place of the unit: eight neighbours, or interleaved lanes.
 __device__ __forceinline__ int place(bool vec, int lane, int i) { return vec ? lane * 8 + i : lane + LANES * i; }
 
@@ -245,17 +279,36 @@ struct TypeOf<__nv_bfloat16> { static constexpr int id = kViewBF16; };
 template <>
 struct TypeOf<__half> { static constexpr int id = kViewF16; };
 
-// Store a lane's eight values.
-template <typename T>
-__device__ __forceinline__ void store_unit(T* base, bool vec, const Unit& u, const float (&x)[8]) {
+template <bool LINEAR, typename T>
+__device__ __forceinline__ void load_values(const T* base, bool vec, int have, Eight<T>& x) {
   const int lane = unit_lane();
+  if (LINEAR) {
+    x.load(base + lane * 8);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < static_cast<int>(sizeof(x) / 4); ++i) reinterpret_cast<uint32_t*>(&x)[i] = 0;
   if (vec) {
-    if (lane * 8 < u.have) store_eight(base, TypeOf<T>::id, lane * 8, 8, true, x);
+    if (lane * 8 < have) x.load(base + lane * 8);  // rows are multiples of 8: all or nothing
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int at = place(false, lane, i);
-      if (at < u.have) store_one(base, TypeOf<T>::id, at, x[i]);
+      if (at < have) x.set(i, base + at);
+    }
+  }
+}
+
+template <bool LINEAR, typename T>
+__device__ __forceinline__ void store_values(T* base, bool vec, int have, const float (&x)[8]) {
+  const int lane = unit_lane();
+  if (LINEAR || vec) {
+    if (lane * 8 < have) store_eight(base, TypeOf<T>::id, lane * 8, 8, true, x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = place(false, lane, i);
+      if (at < have) store_one(base, TypeOf<T>::id, at, x[i]);
     }
   }
 }
@@ -263,9 +316,9 @@ __device__ __forceinline__ void store_unit(T* base, bool vec, const Unit& u, con
 // Write the four units of these 16 lanes.  The largest magnitudes of all four go through one
 // exchange: each step halves the units a lane still holds, so that quarter q of the lanes ends with
 // unit q's, divides once, and hands factor and scale back.
-template <int F, bool STOCHASTIC>
-__device__ __forceinline__ void write_units(const StateSeg& s, const Cta& c, bool vec, const Unit (&u)[PASSES],
-                                            uint32_t key, float (&x)[PASSES][8]) {
+template <int F, bool STOCHASTIC, bool LINEAR>
+__device__ __forceinline__ void write_units(const Sites<LINEAR>& at, bool vec, uint32_t key, float (&x)[PASSES][8]) {
+  const StateSeg& s = at.s;
   const int lane = unit_lane();
   uint32_t top[PASSES];
 #pragma unroll
@@ -288,9 +341,9 @@ __device__ __forceinline__ void write_units(const StateSeg& s, const Cta& c, boo
   for (int q = 0; q < PASSES; ++q) {
     const float mul = __shfl_sync(0xffffffffu, my_mul, q * 4, LANES);
     const bool fine = __shfl_sync(0xffffffffu, t, q * 4, LANES) < 0x7F800000u;
-    if (lane == q * 4 && u[q].have > 0) s.scales[scale_at(s, c, u[q])] = my_scale;
-    uint8_t* codes = static_cast<uint8_t*>(s.codes) + code_at(s, c, u[q]);
-    const unsigned long long at = static_cast<unsigned long long>(u[q].row) * s.cols + u[q].col;  // in the matrix
+    const int have = at.have(q);
+    if (lane == q * 4 && have > 0) s.scales[at.scale_at(q)] = my_scale;
+    uint8_t* codes = static_cast<uint8_t*>(s.codes) + at.code_at(q);
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[q][i] = __fmul_rn(x[q][i], mul);
     if (!fine) {  // rare: not finite
@@ -299,27 +352,29 @@ __device__ __forceinline__ void write_units(const StateSeg& s, const Cta& c, boo
     }
     uint32_t r[4] = {0, 0, 0, 0};
     if (STOCHASTIC) {
-      if (vec) {  // eight neighbours from an even place: four pairs
+      const unsigned long long first = at.place_of(q);
+      if (LINEAR || vec) {  // eight neighbours from an even place: four pairs
+        const uint32_t counter = pair_counter(key, (first + lane * 8) / 2);  // (a multiple of 4: no carry below)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r[i] = pair_bits(key, (at + lane * 8) / 2 + i);
+        for (int i = 0; i < 4; ++i) r[i] = mixed(counter + i);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const unsigned long long here = at + place(false, lane, i);
-          const uint32_t h = pair_bits(key, here >> 1) >> (16 * (here & 1)) & 0xFFFFu;
+          const unsigned long long here = first + place(false, lane, i);
+          const uint32_t h = mixed(pair_counter(key, here >> 1)) >> (16 * (here & 1)) & 0xFFFFu;
           r[i >> 1] |= h << (16 * (i & 1));
         }
       }
     }
     const uint32_t r0[2] = {r[0], r[1]}, r1[2] = {r[2], r[3]};
     const uint32_t lo = encode4<F, STOCHASTIC>(x[q], r0), hi = encode4<F, STOCHASTIC>(x[q] + 4, r1);
-    if (vec) {
-      if (lane * 8 < u[q].have) __stcs(reinterpret_cast<uint2*>(codes + lane * 8), make_uint2(lo, hi));
+    if (LINEAR || vec) {
+      if (lane * 8 < have) __stcs(reinterpret_cast<uint2*>(codes + lane * 8), make_uint2(lo, hi));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const int to = place(false, lane, i);
-        if (to < u[q].have) codes[to] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        if (to < have) codes[to] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
       }
     }
   }
@@ -330,22 +385,23 @@ struct Codes {
   uint32_t w[2];
   float scale;
 };
-__device__ __forceinline__ void load_codes(const StateSeg& s, const Cta& cta, bool vec, const Unit& u, Codes& c) {
-  const int lane = unit_lane();
-  const uint8_t* p = static_cast<const uint8_t*>(s.codes) + code_at(s, cta, u);
+template <bool LINEAR>
+__device__ __forceinline__ void load_codes(const Sites<LINEAR>& at, int q, bool vec, Codes& c) {
+  const int lane = unit_lane(), have = at.have(q);
+  const uint8_t* p = static_cast<const uint8_t*>(at.s.codes) + at.code_at(q);
   c.w[0] = c.w[1] = 0;
-  c.scale = u.have > 0 ? s.scales[scale_at(s, cta, u)] : 0.0f;
-  if (vec) {
-    if (lane * 8 < u.have) {
-      const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p + lane * 8));
-      c.w[0] = q.x;
-      c.w[1] = q.y;
+  c.scale = LINEAR || have > 0 ? at.s.scales[at.scale_at(q)] : 0.0f;
+  if (LINEAR || vec) {
+    if (LINEAR || lane * 8 < have) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p + lane * 8));
+      c.w[0] = v.x;
+      c.w[1] = v.y;
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = place(false, lane, i);
-      if (at < u.have) c.w[i >> 2] |= static_cast<uint32_t>(p[at]) << (8 * (i & 3));
+      const int to = place(false, lane, i);
+      if (to < have) c.w[i >> 2] |= static_cast<uint32_t>(p[to]) << (8 * (i & 3));
     }
   }
 }
@@ -360,88 +416,77 @@ __device__ __forceinline__ void read_codes(const Codes& c, float (&x)[8]) {
   for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(x[i], c.scale);
 }
 
-template <typename T>
-__device__ __forceinline__ void load_values(const T* base, bool vec, const Unit& u, Eight<T>& x) {
-#pragma unroll
-  for (int i = 0; i < static_cast<int>(sizeof(x) / 4); ++i) reinterpret_cast<uint32_t*>(&x)[i] = 0;
-  const int lane = unit_lane();
-  if (vec) {
-    if (lane * 8 < u.have) x.load(base + lane * 8);  // rows are multiples of 8: all or nothing
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int at = place(false, lane, i);
-      if (at < u.have) x.set(i, base + at);
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ const T* in_row(const StateSeg& s, const Cta& c, const Unit& u) {
-  return static_cast<const T*>(s.in) + c.e * s.in_bs + u.row * s.in_ld + u.col;
-}
-template <typename T>
-__device__ __forceinline__ T* out_row(const StateSeg& s, const Cta& c, const Unit& u) {
-  return static_cast<T*>(s.out) + c.e * s.out_bs + u.row * s.out_ld + u.col;
-}
-
-template <typename T, int F, bool STOCHASTIC>
-__global__ void __launch_bounds__(THREADS) state_quantize_kernel(const __grid_constant__ StateParams p) {
+template <typename T, int F, bool STOCHASTIC, bool LINEAR>
+__global__ void __launch_bounds__(THREADS, LINEAR ? 4 : 1) state_quantize_kernel(const __grid_constant__ StateParams p) {
   const Cta c = find(p);
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
   const uint32_t key = STOCHASTIC ? matrix_key(p.seed, static_cast<uint32_t>(s.mat_begin + c.e)) : 0u;
-  Unit u[PASSES];
-  units_of(s, c, u);
+  const Sites<LINEAR> at(s, c);
   Eight<T> raw[PASSES];
 #pragma unroll
-  for (int q = 0; q < PASSES; ++q) load_values<T>(in_row<T>(s, c, u[q]), vec, u[q], raw[q]);
+  for (int q = 0; q < PASSES; ++q) load_values<LINEAR, T>(at.template in<T>(q), vec, at.have(q), raw[q]);
   float x[PASSES][8];
 #pragma unroll
   for (int q = 0; q < PASSES; ++q) raw[q].widen(x[q]);
-  write_units<F, STOCHASTIC>(s, c, vec, u, key, x);
+  write_units<F, STOCHASTIC, LINEAR>(at, vec, key, x);
 }
 
-template <typename T, int F>
-__global__ void __launch_bounds__(THREADS) state_dequantize_kernel(const __grid_constant__ StateParams p) {
+template <typename T, int F, bool LINEAR>
+__global__ void __launch_bounds__(THREADS, LINEAR ? 4 : 1) state_dequantize_kernel(const __grid_constant__ StateParams p) {
   const Cta c = find(p);
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
-  Unit u[PASSES];
-  units_of(s, c, u);
+  const Sites<LINEAR> at(s, c);
   Codes raw[PASSES];
 #pragma unroll
-  for (int q = 0; q < PASSES; ++q) load_codes(s, c, vec, u[q], raw[q]);
+  for (int q = 0; q < PASSES; ++q) load_codes<LINEAR>(at, q, vec, raw[q]);
 #pragma unroll
   for (int q = 0; q < PASSES; ++q) {
     float x[8];
     read_codes<F>(raw[q], x);
-    store_unit<T>(out_row<T>(s, c, u[q]), vec, u[q], x);
+    store_values<LINEAR, T>(at.template out<T>(q), vec, at.have(q), x);
   }
 }
 
+// The sum over the CTA, in thread 0.
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();  // `red` may be in use
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.0f;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) t += red[i];
+  }
+  return t;
+}
+
 // Momentum and Nesterov blend of one CTA's units; F = kStateDense keeps m in T.
-template <typename T, int F, bool STOCHASTIC>
-__global__ void __launch_bounds__(THREADS) state_momentum_kernel(const __grid_constant__ StateParams p) {
+template <typename T, int F, bool STOCHASTIC, bool LINEAR>
+__global__ void __launch_bounds__(THREADS, LINEAR && sizeof(T) == 2 ? 3 : 1)
+    state_momentum_kernel(const __grid_constant__ StateParams p) {
   __shared__ float red[THREADS / 32];
+  __shared__ bool last;
   constexpr bool DENSE = F == kStateDense;
   const Cta c = find(p);
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
   const uint32_t key = STOCHASTIC ? matrix_key(p.seed, static_cast<uint32_t>(s.mat_begin + c.e)) : 0u;
   const float beta = p.beta, rest = __fsub_rn(1.0f, p.beta);
-  Unit u[PASSES];
-  units_of(s, c, u);
+  const Sites<LINEAR> at(s, c);
   Eight<T> raw[PASSES];
   Codes codes[DENSE ? 1 : PASSES];
   Eight<T> dense[DENSE ? PASSES : 1];
 #pragma unroll
   for (int q = 0; q < PASSES; ++q) {
-    load_values<T>(in_row<T>(s, c, u[q]), vec, u[q], raw[q]);
+    load_values<LINEAR, T>(at.template in<T>(q), vec, at.have(q), raw[q]);
     if (DENSE)
-      load_values<T>(static_cast<const T*>(s.codes) + code_at(s, c, u[q]), vec, u[q], dense[DENSE ? q : 0]);
+      load_values<LINEAR, T>(static_cast<const T*>(s.codes) + at.code_at(q), vec, at.have(q), dense[DENSE ? q : 0]);
     else
-      load_codes(s, c, vec, u[q], codes[DENSE ? 0 : q]);
+      load_codes<LINEAR>(at, q, vec, codes[DENSE ? 0 : q]);
   }
   float ss = 0.0f;
   float m[PASSES][8];
@@ -453,77 +498,80 @@ __global__ void __launch_bounds__(THREADS) state_momentum_kernel(const __grid_co
       dense[DENSE ? q : 0].widen(m[q]);
     else
       read_codes<DENSE ? kStateInt8 : F>(codes[DENSE ? 0 : q], m[q]);
+    float part = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       g[i] = __fmul_rn(g[i], rest);
       m[q][i] = __fadd_rn(__fmul_rn(m[q][i], beta), g[i]);
-      g[i] = p.nesterov ? __fadd_rn(g[i], __fmul_rn(m[q][i], beta)) : m[q][i];
-      ss = fmaf(g[i], g[i], ss);
+      if (p.nesterov)
+        g[i] = __fadd_rn(g[i], __fmul_rn(m[q][i], beta));
+      else
+        g[i] = m[q][i];
+      part = fmaf(g[i], g[i], part);
     }
-    store_unit<T>(out_row<T>(s, c, u[q]), vec, u[q], g);
-    if (DENSE) store_unit<T>(static_cast<T*>(s.codes) + code_at(s, c, u[q]), vec, u[q], m[q]);
+    ss += at.have(q) > 0 ? part : 0.0f;
+    store_values<LINEAR, T>(at.template out<T>(q), vec, at.have(q), g);
+    if (DENSE) store_values<LINEAR, T>(static_cast<T*>(s.codes) + at.code_at(q), vec, at.have(q), m[q]);
   }
-  if (!DENSE) write_units<DENSE ? kStateInt8 : F, STOCHASTIC>(s, c, vec, u, key, m);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = ss;
-  __syncthreads();
+  if (!DENSE) write_units<DENSE ? kStateInt8 : F, STOCHASTIC, LINEAR>(at, vec, key, m);
+  ss = block_sum(ss, red);
+  if (threadIdx.x == 0) p.partials[blockIdx.x] = ss;
+  if (p.norms == nullptr) return;  // (a step: the next kernel adds the parts)
+  // The last CTA of a matrix adds its parts, in a fixed order.  The count wraps to 0 for the next call.
   if (threadIdx.x == 0) {
-    float t = 0.0f;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) t += red[i];
-    p.partials[blockIdx.x] = t;
+    __threadfence();
+    last = atomicInc(p.arrivals + s.caller_idx + c.e, static_cast<unsigned>(s.unit_ctas) - 1u) ==
+           static_cast<unsigned>(s.unit_ctas) - 1u;
   }
-}
-
-// The norms of one momentum launch: CTA j adds matrix j's partial sums in a fixed order.
-__global__ void __launch_bounds__(THREADS) state_norm_kernel(const __grid_constant__ StateParams p) {
-  __shared__ float red[THREADS / 32];
-  int at = static_cast<int>(blockIdx.x), seg = 0;
-  while (at >= p.seg[seg].count) at -= p.seg[seg++].count;
-  const StateSeg& s = p.seg[seg];
-  const float* part = p.partials + s.cta_begin + at * s.unit_ctas;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  const float* part = p.partials + s.cta_begin + c.e * s.unit_ctas;
   float t = 0.0f;
-  for (int i = threadIdx.x; i < s.unit_ctas; i += THREADS) t += part[i];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = t;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float n = 0.0f;
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) n += red[i];
-    p.norms[s.caller_idx + at] = sqrtf(n);
-  }
+  for (int i = threadIdx.x; i < s.unit_ctas; i += THREADS) t += __ldcg(part + i);
+  t = block_sum(t, red);
+  if (threadIdx.x == 0) p.norms[s.caller_idx + c.e] = sqrtf(t);
 }
 
-template <typename T, int F>
+template <typename T, int F, bool LINEAR>
 cudaError_t quantize(const StateParams& p, cudaStream_t s) {
   if (p.stochastic)
-    state_quantize_kernel<T, F, true><<<static_cast<unsigned>(p.total), THREADS, 0, s>>>(p);
+    state_quantize_kernel<T, F, true, LINEAR><<<p.total, THREADS, 0, s>>>(p);
   else
-    state_quantize_kernel<T, F, false><<<static_cast<unsigned>(p.total), THREADS, 0, s>>>(p);
+    state_quantize_kernel<T, F, false, LINEAR><<<p.total, THREADS, 0, s>>>(p);
   return cudaGetLastError();
+}
+template <typename T, int F>
+cudaError_t quantize(const StateParams& p, cudaStream_t s) {
+  return p.linear ? quantize<T, F, true>(p, s) : quantize<T, F, false>(p, s);
 }
 template <typename T>
 cudaError_t quantize(const StateParams& p, StateFormat f, cudaStream_t s) {
   return f == kStateInt8 ? quantize<T, kStateInt8>(p, s) : quantize<T, kStateE4M3>(p, s);
 }
+template <typename T, int F>
+cudaError_t dequantize(const StateParams& p, cudaStream_t s) {
+  if (p.linear)
+    state_dequantize_kernel<T, F, true><<<p.total, THREADS, 0, s>>>(p);
+  else
+    state_dequantize_kernel<T, F, false><<<p.total, THREADS, 0, s>>>(p);
+  return cudaGetLastError();
+}
 template <typename T>
 cudaError_t dequantize(const StateParams& p, StateFormat f, cudaStream_t s) {
-  if (f == kStateInt8)
-    state_dequantize_kernel<T, kStateInt8><<<static_cast<unsigned>(p.total), THREADS, 0, s>>>(p);
+  return f == kStateInt8 ? dequantize<T, kStateInt8>(p, s) : dequantize<T, kStateE4M3>(p, s);
+}
+template <typename T, int F, bool LINEAR>
+cudaError_t momentum(const StateParams& p, cudaStream_t s) {
+  if (F != kStateDense && p.stochastic)
+    state_momentum_kernel<T, F, F != kStateDense, LINEAR><<<p.total, THREADS, 0, s>>>(p);
   else
-    state_dequantize_kernel<T, kStateE4M3><<<static_cast<unsigned>(p.total), THREADS, 0, s>>>(p);
+    state_momentum_kernel<T, F, false, LINEAR><<<p.total, THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int F>
 cudaError_t momentum(const StateParams& p, cudaStream_t s) {
-  if (F != kStateDense && p.stochastic)
-    state_momentum_kernel<T, F, true><<<static_cast<unsigned>(p.total), THREADS, 0, s>>>(p);
-  else
-    state_momentum_kernel<T, F, false><<<static_cast<unsigned>(p.total), THREADS, 0, s>>>(p);
-  return cudaGetLastError();
+  return p.linear ? momentum<T, F, true>(p, s) : momentum<T, F, false>(p, s);
 }
 template <typename T>
 cudaError_t momentum(const StateParams& p, StateFormat f, cudaStream_t s) {
@@ -552,12 +600,7 @@ cudaError_t launch_state_dequantize(const StateParams& p, StateFormat f, cudaStr
 
 cudaError_t launch_state_momentum(const StateParams& p, StateFormat f, cudaStream_t s) {
   if (p.total <= 0) return cudaSuccess;
-  cudaError_t e = p.seg[0].in_type == kViewF32 ? momentum<float>(p, f, s) : momentum<__nv_bfloat16>(p, f, s);
-  if (e != cudaSuccess || p.norms == nullptr) return e;
-  int mats = 0;
-  for (int i = 0; i < p.nseg; ++i) mats += p.seg[i].count;
-  state_norm_kernel<<<mats, THREADS, 0, s>>>(p);
-  return cudaGetLastError();
+  return p.seg[0].in_type == kViewF32 ? momentum<float>(p, f, s) : momentum<__nv_bfloat16>(p, f, s);
 }
 
 }  // namespace muon

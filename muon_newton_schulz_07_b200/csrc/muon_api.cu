@@ -109,6 +109,8 @@ void make_plan(const muon_shape_t* shapes, int n, muon_dtype_t dtype, muon_mode_
   size_t off = 0;
   P->off_status = off;
   off = align_up(off + 64, 1024);
+  P->off_arrivals = off;  // CTAs of each matrix that have finished (the 8-bit momentum's norms); zero between calls
+  off = align_up(off + sizeof(unsigned int) * static_cast<size_t>(n), 1024);
   // the single-launch schedule's completion counters, [3 k][n] for k up to 64
   P->off_deps = off;
   off = align_up(P->off_deps + sizeof(unsigned int) * 3 * 64 * static_cast<size_t>(n), 1024);

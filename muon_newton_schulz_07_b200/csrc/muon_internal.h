@@ -331,6 +331,7 @@ struct StateSeg {
   long long in_ld, in_bs, out_ld, out_bs;
   int in_type, out_type;
   int vec;               // every row of every side is aligned for vector accesses
+  int linear;            // and whole blocks, the matrices and their rows back to back on every side
   int rows, cols, blocks;
   int count;
   int mat_begin;         // first matrix's number in the call (the random bits' key)
@@ -343,12 +344,14 @@ struct StateParams {
   StateSeg seg[kStateSegs];
   int nseg;
   int total;             // CTAs
+  int linear;            // every segment is: whole blocks, every side contiguous and aligned
   int stochastic;
   unsigned int seed;
   float beta;
   int nesterov;
   float* partials;       // momentum: one sum of squares per CTA
-  float* norms;
+  float* norms;          // momentum: nullptr, or where each matrix's last CTA puts its norm
+  unsigned int* arrivals;  // momentum with norms: per matrix, zero between calls
 };
 cudaError_t launch_state_quantize(const StateParams& p, StateFormat f, cudaStream_t s);
 cudaError_t launch_state_dequantize(const StateParams& p, StateFormat f, cudaStream_t s);

@@ -452,7 +452,7 @@ struct Rows {
   char* data;
   int type;
   long long ld, bs;
-  bool vec;
+  bool vec, linear;
 };
 muon_status_t make_rows(const muon_view_t& v, const muon_state_t& s, bool output, Rows* r) {
   if (v.data == nullptr || v.count != s.count) return MUON_ERR_INVALID_ARG;
@@ -472,6 +472,8 @@ muon_status_t make_rows(const muon_view_t& v, const muon_state_t& s, bool output
   }
   r->vec = (reinterpret_cast<uintptr_t>(v.data) & 15u) == 0 && s.cols % 8 == 0 &&
            (s.rows == 1 || r->ld * es % 16 == 0) && (s.count == 1 || r->bs * es % 16 == 0);
+  // back to back (a stack's stride may still differ: matrices are found by it)
+  r->linear = r->vec && s.cols % kStateBlock == 0 && (s.rows == 1 || r->ld == s.cols);
   return MUON_OK;
 }
 
@@ -486,12 +488,14 @@ void fill_state(const muon_state_t& s, const Rows* in, const Rows* out, int mat,
   g->mat_begin = mat;
   g->unit_ctas = static_cast<int>((s.rows * g->blocks + kStateUnits - 1) / kStateUnits);
   bool vec = (reinterpret_cast<uintptr_t>(s.codes) & 7u) == 0;
+  bool linear = vec && s.cols % kStateBlock == 0;
   if (in != nullptr) {
     g->in = in->data;
     g->in_ld = in->ld;
     g->in_bs = in->bs;
     g->in_type = in->type;
     vec = vec && in->vec;
+    linear = linear && in->linear;
   }
   if (out != nullptr) {
     g->out = out->data;
@@ -499,8 +503,10 @@ void fill_state(const muon_state_t& s, const Rows* in, const Rows* out, int mat,
     g->out_bs = out->bs;
     g->out_type = out->type;
     vec = vec && out->vec;
+    linear = linear && out->linear;
   }
   g->vec = vec ? 1 : 0;
+  g->linear = linear ? 1 : 0;
 }
 
 // Quantise (X read) or dequantise (X written).
@@ -525,10 +531,9 @@ muon_status_t convert(const muon_view_t* X, const muon_state_t* S, int n, muon_s
   while (j < n) {
     p.nseg = 0;
     p.total = 0;
+    p.linear = 1;
     p.stochastic = seed != nullptr;
     p.seed = seed != nullptr ? *seed : 0u;
-    p.partials = nullptr;
-    p.norms = nullptr;
     for (; j < n && p.nseg < kStateSegs; ++j) {
       StateSeg g;
       Rows rows;
@@ -537,6 +542,7 @@ muon_status_t convert(const muon_view_t* X, const muon_state_t* S, int n, muon_s
       const long long ctas = static_cast<long long>(g.unit_ctas) * g.count;
       if (p.total + ctas > 0x7fffffffll) break;  // (one state fits: check_state)
       g.cta_begin = p.total;
+      p.linear &= g.linear;
       p.seg[p.nseg++] = g;
       p.total += static_cast<int>(ctas);
       mat += g.count;
@@ -563,16 +569,19 @@ cudaError_t enqueue_momentum(muon_ctx* h, const std::vector<MomentumIn>& in, Sta
   while (j < in.size()) {
     p.nseg = 0;
     p.total = 0;
+    p.linear = 1;
     p.stochastic = seed != nullptr;
     p.seed = seed != nullptr ? *seed : 0u;
     p.beta = hp->beta;
     p.nesterov = hp->nesterov ? 1 : 0;
     p.partials = h->d_partials + part;
     p.norms = norms ? h->d_norms : nullptr;
+    p.arrivals = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_arrivals);
     for (; j < in.size() && p.nseg < kStateSegs; ++j) {
       StateSeg g;
       fill_state(in[j].state, &in[j].g, &in[j].u, in[j].first, &g);
-      if (f == kStateDense) g.vec = g.vec && (reinterpret_cast<uintptr_t>(g.codes) & 15u) == 0;
+      if (f == kStateDense && (reinterpret_cast<uintptr_t>(g.codes) & 15u) != 0) g.vec = g.linear = 0;
+      p.linear &= g.linear;
       g.caller_idx = in[j].first;
       g.cta_begin = p.total;
       if (items != nullptr) {

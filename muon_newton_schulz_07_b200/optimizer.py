@@ -28,29 +28,26 @@ def _entries(shapes):
     return out
 
 
-def _view(t, count):
-    """The tuple of binding.views for a matrix or a stack of them."""
-    st = t.stride()
-    if len(st) == 2:
-        return (t.data_ptr(), 1, 0, st[0], st[1], _VIEW_TYPES[t.dtype])
-    return (t.data_ptr(), count, st[0], st[1], st[2], _VIEW_TYPES[t.dtype])
-
-
 def _views(tensors, entries, device, name, dtype=None, by_rows=False):
     """Views of tensors that may be strided; dtype None: any of bf16, fp16 and fp32."""
     if len(tensors) != len(entries):
         raise ValueError(f"{name}: expected {len(entries)} tensors, got {len(tensors)}")
     out = []
     for t, (count, rows, cols, shape) in zip(tensors, entries):
-        if tuple(t.shape) != shape or t.device != device or (t.dtype != dtype if dtype else t.dtype not in _VIEW_TYPES):
+        dt = t.dtype
+        if t.shape != shape or t.device != device or (dt is not dtype if dtype else dt not in _VIEW_TYPES):
             raise ValueError(f"{name}: tensor {tuple(t.shape)} {t.dtype} {t.device} does not match {shape} "
                              f"{dtype or 'bf16, fp16 or fp32'} {device}")
-        by_row = t.stride(-1) == 1 or cols == 1
-        if not by_row and (by_rows or not (t.stride(-2) == 1 or rows == 1)):
-            raise ValueError(f"{name}: a tensor of strides {t.stride()} is not stored by rows"
+        st = t.stride()
+        if st[-1] != 1 and cols != 1 and (by_rows or not (st[-2] == 1 or rows == 1)):
+            raise ValueError(f"{name}: a tensor of strides {st} is not stored by rows"
                              + ("" if by_rows else " or by columns"))
-        out.append(_view(t, count))
+        out.append((t.data_ptr(), count, st[0] if len(st) == 3 else 0, st[-2], st[-1], _VIEW_TYPES[dt]))
     return B.views(out)
+
+
+def _stream(device, stream):
+    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
 
 
 class QuantizedState:
@@ -86,16 +83,16 @@ class QuantizedState:
                        for s in self.shapes]
 
     def _states(self):
-        code = self.FORMATS[self.fmt][1]
         out = []
+        code = self.FORMATS[self.fmt][1]
         for q, s, (count, rows, cols, shape) in zip(self.codes, self.scales, self._entries):
-            blocks = shape[:-1] + (-(-cols // self.BLOCK),)
-            if tuple(q.shape) != shape or q.dtype != code or not q.is_contiguous() or q.device != self.device:
+            if q.shape != shape or q.dtype is not code or q.device != self.device or not q.is_contiguous():
                 raise ValueError(f"codes: tensor {tuple(q.shape)} {q.dtype} {q.device} does not match {shape} {code} "
                                  f"{self.device} (contiguous)")
-            if tuple(s.shape) != blocks or s.dtype != torch.float32 or not s.is_contiguous() or s.device != self.device:
-                raise ValueError(f"scales: tensor {tuple(s.shape)} {s.dtype} {s.device} does not match {blocks} "
-                                 f"torch.float32 {self.device} (contiguous)")
+            if (s.shape[:-1] != shape[:-1] or s.shape[-1] != -(-cols // self.BLOCK) or s.dtype is not torch.float32
+                    or s.device != self.device or not s.is_contiguous()):
+                raise ValueError(f"scales: tensor {tuple(s.shape)} {s.dtype} {s.device} does not match {shape}, a scale "
+                                 f"for {self.BLOCK} columns, torch.float32 {self.device} (contiguous)")
             out.append((q.data_ptr(), s.data_ptr(), count, rows, cols))
         return B.states(out)
 
@@ -106,15 +103,20 @@ class QuantizedState:
 
     def write(self, X, seed=None, stream=None) -> None:
         """Quantise X (bf16, fp16 or fp32, stored by rows) into this state, on the current stream or `stream`."""
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        with torch.cuda.device(self.device):
-            B.muon_state_quantize(self._side(X, "X"), self._states(), len(self.shapes), self._fmt, seed, s.cuda_stream)
+        self._call(B.muon_state_quantize, self._side(X, "X"), self._states(), len(self.shapes), self._fmt, seed,
+                   _stream(self.device, stream))
 
     def read(self, out, stream=None) -> None:
         """Read this state back into the tensors of `out` (bf16, fp16 or fp32, stored by rows)."""
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        with torch.cuda.device(self.device):
-            B.muon_state_dequantize(self._states(), self._side(out, "out"), len(self.shapes), self._fmt, s.cuda_stream)
+        self._call(B.muon_state_dequantize, self._states(), self._side(out, "out"), len(self.shapes), self._fmt,
+                   _stream(self.device, stream))
+
+    def _call(self, f, *args):
+        if torch.cuda.current_device() == self.device.index:
+            f(*args)
+        else:  # the library launches on the current device
+            with torch.cuda.device(self.device):
+                f(*args)
 
 
 class MuonStep:
@@ -261,13 +263,12 @@ class MuonStep:
     def momentum(self, G, state, U, beta=0.95, nesterov=True, seed=None, norms=None, stream=None) -> torch.Tensor:
         """The momentum of a step on a QuantizedState, by itself: the state updated in place, the blended direction
         in U, its Frobenius norms (one a matrix, fp32) returned.  G and U: the handle's dtype, stored by rows; U may be G."""
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
+        s = _stream(self.device, stream)
         hp = B.make_hparams(0.0, beta, 0.0, 0.0, QUINTIC, nesterov, 0)
         g = _views(G, self._entries, self.device, "G", self.dtype, by_rows=True)
         u = _views(U, self._entries, self.device, "U", self.dtype, by_rows=True)
-        B.muon_momentum_state(self.handle, g, self._momentum_state(state), u, len(self.shapes), state._fmt, hp, seed,
-                              s.cuda_stream)
-        return self.norms(norms, stream=s)
+        B.muon_momentum_state(self.handle, g, self._momentum_state(state), u, len(self.shapes), state._fmt, hp, seed, s)
+        return self.norms(norms, stream=stream)
 
     def orthogonalize(self, X, O, eps=1e-7, abc=QUINTIC, ns_steps=None, stream=None):
         """O = the orthogonalised X, nothing else.
