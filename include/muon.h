@@ -245,8 +245,8 @@ MUON_API muon_status_t muon_momentum_state(muon_handle_t handle, const muon_view
 
 /*
  * The Muon step on 8-bit momentum (MUON_MODE_HALF): muon_step with M held in S.  W and G are views of the
- * handle's type (G with col_stride 1).  The direction is rounded to the
- * handle's type once before it is orthogonalised.
+ * handle's type (G with col_stride 1).  The direction stays in fp32 until it has been normalised
+ * (a first pass over G and the state takes the norms, a second one writes).
  */
 MUON_API muon_status_t muon_step_state(muon_handle_t handle, const muon_view_t* W, const muon_view_t* G,
                                        const muon_state_t* S, int n, muon_state_format_t format,

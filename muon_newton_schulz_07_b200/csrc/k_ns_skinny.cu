@@ -339,8 +339,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     for (int i = 0; i * 8 < p.slot_rows; ++i) t += total[(tid >> 3) + i];
     const float norm = sqrtf(t);
     if (!isfinite(norm)) poison[slot] = 1;
-    factor[slot] = normaliser(norm, p.eps);
-    if (first_mat + slot < p.total && rank == 0) {
+    factor[slot] = p.normalised ? 1.0f : normaliser(norm, p.eps);
+    if (first_mat + slot < p.total && rank == 0 && !p.normalised) {
       int s = 0;
       while (s + 1 < p.nseg && p.seg[s + 1].mat_begin <= first_mat + slot) ++s;
       p.norms[p.seg[s].caller_idx + first_mat + slot - p.seg[s].mat_begin] = norm;

@@ -464,8 +464,9 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
   return t;
 }
 
-// Momentum and Nesterov blend of one CTA's units; F = kStateDense keeps m in T.
-template <typename T, int F, bool STOCHASTIC, bool LINEAR>
+// Momentum and Nesterov blend of one CTA's units; F = kStateDense keeps m in T.  PASS says what a
+// launch does with u and m1 (see StatePass).
+template <typename T, int F, bool STOCHASTIC, bool LINEAR, int PASS>
 __global__ void __launch_bounds__(THREADS, LINEAR && sizeof(T) == 2 ? 3 : 1)
     state_momentum_kernel(const __grid_constant__ StateParams p) {
   __shared__ float red[THREADS / 32];
@@ -475,6 +476,7 @@ __global__ void __launch_bounds__(THREADS, LINEAR && sizeof(T) == 2 ? 3 : 1)
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
   const uint32_t key = STOCHASTIC ? matrix_key(p.seed, static_cast<uint32_t>(s.mat_begin + c.e)) : 0u;
+  const float mul = PASS == kPassStep ? normaliser(p.norms[s.caller_idx + c.e], p.eps) : 1.0f;
   const float beta = p.beta, rest = __fsub_rn(1.0f, p.beta);
   const Sites<LINEAR> at(s, c);
   Eight<T> raw[PASSES];
@@ -510,13 +512,18 @@ __global__ void __launch_bounds__(THREADS, LINEAR && sizeof(T) == 2 ? 3 : 1)
       part = fmaf(g[i], g[i], part);
     }
     ss += at.have(q) > 0 ? part : 0.0f;
-    store_values<LINEAR, T>(at.template out<T>(q), vec, at.have(q), g);
-    if (DENSE) store_values<LINEAR, T>(static_cast<T*>(s.codes) + at.code_at(q), vec, at.have(q), m[q]);
+    if (PASS == kPassStep) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) g[i] *= mul;
+      store_values<LINEAR, __half>(at.template out<__half>(q), vec, at.have(q), g);
+    }
+    if (PASS == kPassMomentum) store_values<LINEAR, T>(at.template out<T>(q), vec, at.have(q), g);
+    if (DENSE && PASS != kPassNorm) store_values<LINEAR, T>(static_cast<T*>(s.codes) + at.code_at(q), vec, at.have(q), m[q]);
   }
-  if (!DENSE) write_units<DENSE ? kStateInt8 : F, STOCHASTIC, LINEAR>(at, vec, key, m);
+  if (!DENSE && PASS != kPassNorm) write_units<DENSE ? kStateInt8 : F, STOCHASTIC, LINEAR>(at, vec, key, m);
+  if (PASS == kPassStep) return;
   ss = block_sum(ss, red);
   if (threadIdx.x == 0) p.partials[blockIdx.x] = ss;
-  if (p.norms == nullptr) return;  // (a step: the next kernel adds the parts)
   // The last CTA of a matrix adds its parts, in a fixed order.  The count wraps to 0 for the next call.
   if (threadIdx.x == 0) {
     __threadfence();
@@ -562,22 +569,29 @@ cudaError_t dequantize(const StateParams& p, StateFormat f, cudaStream_t s) {
   return f == kStateInt8 ? dequantize<T, kStateInt8>(p, s) : dequantize<T, kStateE4M3>(p, s);
 }
 template <typename T, int F, bool LINEAR>
-cudaError_t momentum(const StateParams& p, cudaStream_t s) {
-  if (F != kStateDense && p.stochastic)
-    state_momentum_kernel<T, F, F != kStateDense, LINEAR><<<p.total, THREADS, 0, s>>>(p);
+cudaError_t momentum(const StateParams& p, StatePass pass, cudaStream_t s) {
+  constexpr bool ROUNDS = F != kStateDense;
+  if (pass == kPassNorm)
+    state_momentum_kernel<T, F, false, LINEAR, kPassNorm><<<p.total, THREADS, 0, s>>>(p);
+  else if (ROUNDS && p.stochastic && pass == kPassStep)
+    state_momentum_kernel<T, F, ROUNDS, LINEAR, kPassStep><<<p.total, THREADS, 0, s>>>(p);
+  else if (ROUNDS && p.stochastic)
+    state_momentum_kernel<T, F, ROUNDS, LINEAR, kPassMomentum><<<p.total, THREADS, 0, s>>>(p);
+  else if (pass == kPassStep)
+    state_momentum_kernel<T, F, false, LINEAR, kPassStep><<<p.total, THREADS, 0, s>>>(p);
   else
-    state_momentum_kernel<T, F, false, LINEAR><<<p.total, THREADS, 0, s>>>(p);
+    state_momentum_kernel<T, F, false, LINEAR, kPassMomentum><<<p.total, THREADS, 0, s>>>(p);
   return cudaGetLastError();
 }
 template <typename T, int F>
-cudaError_t momentum(const StateParams& p, cudaStream_t s) {
-  return p.linear ? momentum<T, F, true>(p, s) : momentum<T, F, false>(p, s);
+cudaError_t momentum(const StateParams& p, StatePass pass, cudaStream_t s) {
+  return p.linear ? momentum<T, F, true>(p, pass, s) : momentum<T, F, false>(p, pass, s);
 }
 template <typename T>
-cudaError_t momentum(const StateParams& p, StateFormat f, cudaStream_t s) {
-  if (f == kStateInt8) return momentum<T, kStateInt8>(p, s);
-  if (f == kStateE4M3) return momentum<T, kStateE4M3>(p, s);
-  return momentum<T, kStateDense>(p, s);
+cudaError_t momentum(const StateParams& p, StateFormat f, StatePass pass, cudaStream_t s) {
+  if (f == kStateInt8) return momentum<T, kStateInt8>(p, pass, s);
+  if (f == kStateE4M3) return momentum<T, kStateE4M3>(p, pass, s);
+  return momentum<T, kStateDense>(p, pass, s);
 }
 
 }  // namespace
@@ -598,9 +612,9 @@ cudaError_t launch_state_dequantize(const StateParams& p, StateFormat f, cudaStr
   return dequantize<__half>(p, f, s);
 }
 
-cudaError_t launch_state_momentum(const StateParams& p, StateFormat f, cudaStream_t s) {
+cudaError_t launch_state_momentum(const StateParams& p, StateFormat f, StatePass pass, cudaStream_t s) {
   if (p.total <= 0) return cudaSuccess;
-  return p.seg[0].in_type == kViewF32 ? momentum<float>(p, f, s) : momentum<__nv_bfloat16>(p, f, s);
+  return p.seg[0].in_type == kViewF32 ? momentum<float>(p, f, pass, s) : momentum<__nv_bfloat16>(p, f, pass, s);
 }
 
 }  // namespace muon

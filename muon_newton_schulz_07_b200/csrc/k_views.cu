@@ -159,12 +159,15 @@ __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_co
   const ViewSeg& s = p.seg[w.seg];
   float v[4][8];
   const bool grouped = load_tile<false>(s, w, v);
-  const float* part = p.partials + s.part_begin + w.e * s.parts;
-  float ss = 0.0f;
-  for (int i = threadIdx.x; i < s.parts; i += THREADS) ss += part[i];
-  const float norm = sqrtf(block_sum(ss));
-  if (w.tile == 0 && threadIdx.x == 0) p.norms[s.caller_idx + w.e] = norm;
-  const float mul = normaliser(norm, p.eps);
+  float mul = 1.0f;
+  if (!p.normalised) {
+    const float* part = p.partials + s.part_begin + w.e * s.parts;
+    float ss = 0.0f;
+    for (int i = threadIdx.x; i < s.parts; i += THREADS) ss += part[i];
+    const float norm = sqrtf(block_sum(ss));
+    if (w.tile == 0 && threadIdx.x == 0) p.norms[s.caller_idx + w.e] = norm;
+    mul = normaliser(norm, p.eps);
+  }
   __half* x = static_cast<__half*>(s.x) + static_cast<size_t>(w.e) * s.mp * s.np;
   const bool tr = s.src_tr != 0;
   const bool staged = tr || !grouped;

@@ -51,7 +51,7 @@ bool type_ok(muon_dtype_t dtype, muon_mode_t mode) {
          (mode == MUON_MODE_FAST || mode == MUON_MODE_FP32_REF || mode == MUON_MODE_HALF);
 }
 
-void make_plan(const muon_shape_t* shapes, int n, muon_dtype_t dtype, muon_mode_t mode, Plan* P) {
+void make_plan(const muon_shape_t* shapes, int n, muon_mode_t mode, Plan* P) {
   const size_t elem = (mode == MUON_MODE_FP32_REF) ? 4 : 2;
   std::map<std::pair<long long, long long>, int> key_to_group;
   P->groups.clear();
@@ -130,16 +130,16 @@ void make_plan(const muon_shape_t* shapes, int n, muon_dtype_t dtype, muon_mode_
     gp.off_b = off;    off = align_up(off + ab, 1024);
   }
   if (mode == MUON_MODE_HALF) {
-    // U of each matrix, rows x cols in the handle's type: in the second X buffer, which nothing
-    // uses before the first update, or in a place of its own where there is none or it is too short
+    // A step's direction, fp16 in the caller's layout: in the second X buffer, which nothing uses
+    // before the first update, or in a place of its own where there is none
     P->off_u.assign(n, 0);
     for (int i = 0; i < n; ++i) {
       const GroupPlan& gp = P->groups[P->mat_group[i]];
-      if (dtype == MUON_BF16 && !gp.skinny) {
+      if (!gp.skinny) {
         P->off_u[i] = gp.off_x[1] + static_cast<size_t>(P->mat_slot[i]) * gp.mp * gp.np * elem;
       } else {
         P->off_u[i] = off;
-        off = align_up(off + static_cast<size_t>(shapes[i].rows) * shapes[i].cols * (dtype == MUON_BF16 ? 2 : 4), 1024);
+        off = align_up(off + static_cast<size_t>(shapes[i].rows) * shapes[i].cols * elem, 1024);
       }
     }
   }
@@ -782,7 +782,7 @@ muon_status_t muon_workspace_size(const muon_shape_t* shapes, int n, muon_dtype_
   if (bytes == nullptr || !shapes_ok(shapes, n)) return MUON_ERR_INVALID_ARG;
   if (!type_ok(dtype, mode)) return MUON_ERR_INVALID_ARG;
   Plan P;
-  make_plan(shapes, n, dtype, mode, &P);
+  make_plan(shapes, n, mode, &P);
   *bytes = P.total;
   return MUON_OK;
 }
@@ -810,7 +810,7 @@ muon_status_t muon_create(muon_handle_t* handle, const muon_shape_t* shapes, int
   h->mode = mode;
   h->n = n;
   h->shapes.assign(shapes, shapes + n);
-  make_plan(shapes, n, dtype, mode, &h->plan);
+  make_plan(shapes, n, mode, &h->plan);
   h->fuse_shapes_ok = n <= kTcMaxFused;
   for (const GroupPlan& gp : h->plan.groups)
     if (gp.m % 32 != 0 || gp.n % 32 != 0) h->fuse_shapes_ok = false;
@@ -935,7 +935,7 @@ muon_status_t muon_check_plan(const muon_shape_t* shapes, int n, int ns_steps, i
       num_sms > 4096)
     return MUON_ERR_INVALID_ARG;
   Plan P;
-  make_plan(shapes, n, MUON_BF16, MUON_MODE_FAST, &P);
+  make_plan(shapes, n, MUON_MODE_FAST, &P);
   std::vector<muon_shape_t> sh(shapes, shapes + n);
   long long bad = 0;
   EwParams* ew = new (std::nothrow) EwParams;

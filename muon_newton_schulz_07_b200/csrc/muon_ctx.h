@@ -40,7 +40,7 @@ struct Plan {
   std::vector<GroupPlan> groups;
   std::vector<int> mat_group, mat_slot, scal_idx;
   std::vector<int> ew_ntiles;
-  std::vector<size_t> off_u;  // MUON_MODE_HALF: each matrix's direction U in its own layout
+  std::vector<size_t> off_u;  // MUON_MODE_HALF: a step's normalised direction of each matrix, in the caller's layout
   size_t off_status, off_arrivals, off_deps, off_scal, off_norms, off_partials;
   size_t total;
 };

@@ -278,6 +278,7 @@ struct ViewParams {
   ViewSeg seg[kViewSegs];
   int nseg;
   int total;             // CTAs
+  int normalised;        // the source is 2^12 X already: no norm is taken
   float eps;
   float decay;           // 0: dst is not read
   float* partials;
@@ -308,6 +309,7 @@ struct SkinnyParams {
   int slots;                 // matrices in a tile
   int cluster;               // CTAs of a tile
   int width;                 // columns each CTA holds, a multiple of 64
+  int normalised;            // the source is 2^12 X already: no norm is taken
   int k;
   float coef[kMaxSteps][3];  // (a, b, c) of each iteration
   float eps;
@@ -350,13 +352,19 @@ struct StateParams {
   float beta;
   int nesterov;
   float* partials;       // momentum: one sum of squares per CTA
-  float* norms;          // momentum: nullptr, or where each matrix's last CTA puts its norm
-  unsigned int* arrivals;  // momentum with norms: per matrix, zero between calls
+  float eps;             // momentum, kPassStep
+  float* norms;          // momentum: each matrix's last CTA puts its norm there
+  unsigned int* arrivals;  // CTAs of each matrix that have, zero between calls
 };
 cudaError_t launch_state_quantize(const StateParams& p, StateFormat f, cudaStream_t s);
 cudaError_t launch_state_dequantize(const StateParams& p, StateFormat f, cudaStream_t s);
-// G, U and a dense momentum have one type, bf16 or fp32.
-cudaError_t launch_state_momentum(const StateParams& p, StateFormat f, cudaStream_t s);
+// What a momentum launch does: write u (in the type of G) and m1, with the norms; the norms alone,
+// leaving everything as it was; or, knowing the norms, write 2^12 u / (norm + eps) in fp16 and m1.  A step
+// runs the second and the third: u is then rounded once, after it has been normalised, where a pass that
+// wrote it first would have to keep it in 32 bits.
+enum StatePass : int { kPassMomentum = 0, kPassNorm = 1, kPassStep = 2 };
+// G and a dense momentum have one type, bf16 or fp32.
+cudaError_t launch_state_momentum(const StateParams& p, StateFormat f, StatePass pass, cudaStream_t s);
 
 // ------------------------------------------------------------------ fp32 reference GEMMs
 struct SgParams {

@@ -3,7 +3,8 @@
 // only checks, plans and enqueues.
 //
 // A HALF call enqueues, on the caller's stream and without any host sync:
-//   state_momentum_kernel   (steps only) m1 written back, u into the workspace in the caller's layout
+//   state_momentum_kernel   (steps only, twice) the norms; then m1 written back and the normalised u as
+//                           X0 itself, or in the caller's layout where it has to be transposed or padded
 //   view_sumsq_kernel       (orthogonaliser only) the norms' partial sums
 //   view_orient_kernel      X0, oriented and padded, fp16
 //   k x { Gram, Poly, Update }   tcgen05 kernels, the last Update writes the result when it can
@@ -34,6 +35,7 @@ struct Item {   // equal matrices of the call, consecutive in the handle's list
   int first, count;
   Side src, dst;
   int part_begin, parts;  // of the first matrix; partial sums of each matrix
+  bool is_x0;             // the source is X0 already
 };
 
 size_t type_bytes(int type) { return type == kViewF32 ? 4 : 2; }
@@ -145,13 +147,14 @@ void fill_seg(const muon_ctx* h, const Item& it, bool store, float lr, ViewSeg* 
 enum ViewPass { kSumsq, kOrient, kWrite };
 
 // One pass over the views of the groups that go through the workspace, as few launches as fit.
-cudaError_t view_pass(muon_ctx* h, std::vector<Item>& items, ViewPass pass, const muon_hparams_t* hp, bool store,
-                      int fin, cudaStream_t st) {
+cudaError_t view_pass(muon_ctx* h, const std::vector<Item>& items, ViewPass pass, const muon_hparams_t* hp, bool store,
+                      bool normalised, int fin, cudaStream_t st) {
   ViewParams& p = h->vw;
   size_t i = 0;
   while (i < items.size()) {
     p.nseg = 0;
     p.total = 0;
+    p.normalised = normalised ? 1 : 0;
     p.eps = hp->eps;
     p.decay = store ? 0.0f : 1.0f - hp->lr * hp->weight_decay;
     p.partials = h->d_partials;
@@ -159,7 +162,7 @@ cudaError_t view_pass(muon_ctx* h, std::vector<Item>& items, ViewPass pass, cons
     for (; i < items.size() && p.nseg < kViewSegs; ++i) {
       const Item& it = items[i];
       const GroupPlan& gp = group_of(h, it.first);
-      if (gp.skinny) continue;
+      if (gp.skinny || (pass == kOrient && it.is_x0)) continue;
       const int rows = pass == kOrient ? gp.mp : gp.m, cols = pass == kOrient ? gp.np : gp.n;
       const int tiles_c = (cols + kEwTileC - 1) / kEwTileC;
       const long long tiles = static_cast<long long>((rows + kEwTileR - 1) / kEwTileR) * tiles_c;
@@ -369,7 +372,7 @@ void skinny_layout(const GroupPlan& gp, int cnt, int num_sms, SkinnyParams* p) {
 }
 
 cudaError_t enqueue_skinny(muon_ctx* h, const std::vector<Item>& items, const muon_hparams_t* hp, bool store,
-                           cudaStream_t st) {
+                           bool normalised, cudaStream_t st) {
   for (size_t g = 0; g < h->plan.groups.size(); ++g) {
     const GroupPlan& gp = h->plan.groups[g];
     if (!gp.skinny) continue;
@@ -387,6 +390,7 @@ cudaError_t enqueue_skinny(muon_ctx* h, const std::vector<Item>& items, const mu
       }
       if (p.nseg == 0) break;
       skinny_layout(gp, p.total, h->num_sms, &p);
+      p.normalised = normalised ? 1 : 0;
       p.k = hp->ns_steps;
       for (int t = 0; t < p.k; ++t) {
         float own[3];
@@ -406,11 +410,13 @@ cudaError_t enqueue_skinny(muon_ctx* h, const std::vector<Item>& items, const mu
   return cudaSuccess;
 }
 
-// From sources in the caller's layout (and, where have_sums, their partial sums) to the results.
-cudaError_t half_run(muon_ctx* h, std::vector<Item>& items, const muon_hparams_t* hp, bool store, bool have_sums,
+// From sources in the caller's layout to the results.  `normalised`: the sources are 2^12 X already.
+cudaError_t half_run(muon_ctx* h, std::vector<Item>& items, const muon_hparams_t* hp, bool store, bool normalised,
                      cudaStream_t st) {
   const int k = hp->ns_steps;
-  if (!have_sums) {
+  cudaError_t e = cudaSuccess;
+  if (!normalised) {
+    // view_sumsq_kernel writes partial sums, one a tile, where view_orient_kernel looks for them
     int at = 0;
     for (Item& it : items) {
       const GroupPlan& gp = group_of(h, it.first);
@@ -418,22 +424,19 @@ cudaError_t half_run(muon_ctx* h, std::vector<Item>& items, const muon_hparams_t
       it.part_begin = at;
       at += it.parts * it.count;
     }
+    e = view_pass(h, items, kSumsq, hp, store, normalised, 0, st);
   }
-  cudaError_t e = cudaSuccess;
-  if (!have_sums) {
-    // view_sumsq_kernel writes partial tile sums where view_orient_kernel looks for them
-    e = view_pass(h, items, kSumsq, hp, store, 0, st);
-  }
-  if (e == cudaSuccess) e = view_pass(h, items, kOrient, hp, store, 0, st);
+  if (e == cudaSuccess) e = view_pass(h, items, kOrient, hp, store, normalised, 0, st);
   const bool fuse = result_fusable(h, items, k);
   if (e == cudaSuccess) e = enqueue_tiles(h, items, hp, store, fuse, st);
-  if (e == cudaSuccess && !fuse) e = view_pass(h, items, kWrite, hp, store, k & 1, st);
-  if (e == cudaSuccess) e = enqueue_skinny(h, items, hp, store, st);
+  if (e == cudaSuccess && !fuse) e = view_pass(h, items, kWrite, hp, store, normalised, k & 1, st);
+  if (e == cudaSuccess) e = enqueue_skinny(h, items, hp, store, normalised, st);
   return e;
 }
 
 // ---------------------------------------------------------------- state
 
+StateFormat format_of(muon_state_format_t f) { return f == MUON_STATE_INT8 ? kStateInt8 : kStateE4M3; }
 bool format_ok(muon_state_format_t f) { return f == MUON_STATE_INT8 || f == MUON_STATE_E4M3; }
 
 muon_status_t check_state(const muon_state_t& s) {
@@ -547,22 +550,23 @@ muon_status_t convert(const muon_view_t* X, const muon_state_t* S, int n, muon_s
       p.total += static_cast<int>(ctas);
       mat += g.count;
     }
-    const StateFormat f = format == MUON_STATE_INT8 ? kStateInt8 : kStateE4M3;
+    const StateFormat f = format_of(format);
     const cudaError_t e = write_state ? launch_state_quantize(p, f, st) : launch_state_dequantize(p, f, st);
     if (e != cudaSuccess) return MUON_ERR_CUDA;
   }
   return MUON_OK;
 }
 
-// The momentum of every item: G, the state or dense momentum, and U in `items`' source side.
+// A momentum's sources and results: G, the state (or, as its codes, the dense momentum), and U.
 struct MomentumIn {
-  muon_state_t state;   // codes: the dense momentum where dense
+  muon_state_t state;
   Rows g, u;
   int first;
 };
-cudaError_t enqueue_momentum(muon_ctx* h, const std::vector<MomentumIn>& in, StateFormat f, const muon_hparams_t* hp,
-                             const uint32_t* seed, bool norms, std::vector<Item>* items, cudaStream_t st) {
-  NvtxRange range("muon: momentum + norm");
+// One pass over every matrix of the call.
+cudaError_t momentum_pass(muon_ctx* h, const std::vector<MomentumIn>& in, StateFormat f, StatePass pass,
+                          const muon_hparams_t* hp, const uint32_t* seed, cudaStream_t st) {
+  NvtxRange range(pass == kPassNorm ? "muon: norm" : "muon: momentum");
   StateParams& p = h->st;
   size_t j = 0;
   int part = 0;
@@ -574,41 +578,50 @@ cudaError_t enqueue_momentum(muon_ctx* h, const std::vector<MomentumIn>& in, Sta
     p.seed = seed != nullptr ? *seed : 0u;
     p.beta = hp->beta;
     p.nesterov = hp->nesterov ? 1 : 0;
+    p.eps = hp->eps;
     p.partials = h->d_partials + part;
-    p.norms = norms ? h->d_norms : nullptr;
+    p.norms = h->d_norms;
     p.arrivals = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_arrivals);
     for (; j < in.size() && p.nseg < kStateSegs; ++j) {
       StateSeg g;
-      fill_state(in[j].state, &in[j].g, &in[j].u, in[j].first, &g);
+      fill_state(in[j].state, &in[j].g, pass == kPassNorm ? nullptr : &in[j].u, in[j].first, &g);
       if (f == kStateDense && (reinterpret_cast<uintptr_t>(g.codes) & 15u) != 0) g.vec = g.linear = 0;
       p.linear &= g.linear;
       g.caller_idx = in[j].first;
       g.cta_begin = p.total;
-      if (items != nullptr) {
-        (*items)[j].part_begin = part + p.total;
-        (*items)[j].parts = g.unit_ctas;
-      }
       p.seg[p.nseg++] = g;
       p.total += g.unit_ctas * g.count;  // (bounded by the workspace's partial sums)
     }
     part += p.total;
-    const cudaError_t e = launch_state_momentum(p, f, st);
+    const cudaError_t e = launch_state_momentum(p, f, pass, st);
     if (e != cudaSuccess) return e;
     trace(h, MUON_KERNEL_MOMENTUM_NORM, st);
   }
   return cudaSuccess;
 }
 
-// U's place in the workspace, as a view's side and as rows.
-void staged(muon_ctx* h, int mat, int count, Side* side, Rows* rows) {
+// Where a step's normalised direction goes: X0 itself where the caller's layout is X0's, else a place in
+// the workspace that the orientation or the on-chip kernel reads.
+void stage(muon_ctx* h, int mat, int count, Item* item, Rows* rows) {
+  const GroupPlan& gp = group_of(h, mat);
   const muon_shape_t& sh = h->shapes[mat];
-  const size_t es = h->dtype == MUON_BF16 ? 2 : 4;
-  muon_view_t v = contiguous(h->ws + h->plan.off_u[mat], sh, h->dtype);
+  item->is_x0 = !gp.skinny && !tall(h, mat) && gp.mp == gp.m && gp.np == gp.n;
+  const size_t at = item->is_x0 ? gp.off_x[0] + static_cast<size_t>(h->plan.mat_slot[mat]) * gp.mp * gp.np * 2
+                                : h->plan.off_u[mat];
+  muon_view_t v = contiguous(h->ws + at, sh, MUON_FP16);
   v.count = count;
-  if (count > 1) v.batch_stride = static_cast<int64_t>((h->plan.off_u[mat + 1] - h->plan.off_u[mat]) / es);
-  make_side(v, sh.rows, sh.cols, false, side);
+  if (count > 1 && !item->is_x0) v.batch_stride = static_cast<int64_t>((h->plan.off_u[mat + 1] - h->plan.off_u[mat]) / 2);
+  make_side(v, sh.rows, sh.cols, false, &item->src);
   const muon_state_t s{nullptr, nullptr, count, sh.rows, sh.cols};
   make_rows(v, s, false, rows);
+}
+
+cudaError_t run_step(muon_ctx* h, std::vector<Item>& items, const std::vector<MomentumIn>& in, StateFormat f,
+                     const muon_hparams_t* hp, const uint32_t* seed, cudaStream_t st) {
+  cudaError_t e = momentum_pass(h, in, f, kPassNorm, hp, nullptr, st);
+  if (e == cudaSuccess) e = momentum_pass(h, in, f, kPassStep, hp, seed, st);
+  if (e == cudaSuccess) e = half_run(h, items, hp, false, true, st);
+  return e;
 }
 
 }  // namespace
@@ -639,13 +652,12 @@ muon_status_t muon::half_step(muon_ctx* h, void* const* W, const void* const* G,
     muon_status_t r = make_side(w, sh.rows, sh.cols, true, &items[i].dst);
     if (r == MUON_OK) r = make_rows(g, in[i].state, false, &in[i].g);
     if (r != MUON_OK) return r;
-    staged(h, i, 1, &items[i].src, &in[i].u);
+    stage(h, i, 1, &items[i], &in[i].u);
   }
   DeviceGuard guard(h->device);
   NvtxRange range("muon_step");
   trace(h, -1, stream);
-  cudaError_t e = enqueue_momentum(h, in, kStateDense, hp, nullptr, false, &items, stream);
-  if (e == cudaSuccess) e = half_run(h, items, hp, false, true, stream);
+  const cudaError_t e = run_step(h, items, in, kStateDense, hp, nullptr, stream);
   trace_call_end(h);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
@@ -667,12 +679,19 @@ int muon::half_launches(const muon_ctx* h, int k) {
     }
   }
   const int views = (tiled + kViewSegs - 1) / kViewSegs;
+  int turned = 0;  // matrices whose direction is transposed or padded on its way to X0
+  for (int i = 0; i < h->n; ++i) {
+    const GroupPlan& gp = group_of(h, i);
+    turned += !gp.skinny && (tall(h, i) || gp.mp != gp.m || gp.np != gp.n);
+  }
   bool fused = k >= 1 && h->dtype == MUON_BF16 && h->n <= kTcMaxFused;
   for (const GroupPlan& gp : h->plan.groups)
     if (!gp.skinny && (gp.m % 32 != 0 || gp.n % 32 != 0)) fused = false;
-  const int stages = single_launch(h, k) ? (h->schedule == MUON_SCHEDULE_SPLIT ? 3 * k : 1)
-                                         : 3 * k * ((ngroups + kTcMaxGroups - 1) / kTcMaxGroups);
-  return (h->n + kStateSegs - 1) / kStateSegs + views + stages + (fused ? 0 : views) + skinny;
+  const int stages = ngroups == 0            ? 0
+                     : single_launch(h, k)   ? (h->schedule == MUON_SCHEDULE_SPLIT ? 3 * k : 1)
+                                             : 3 * k * ((ngroups + kTcMaxGroups - 1) / kTcMaxGroups);
+  return 2 * ((h->n + kStateSegs - 1) / kStateSegs) + (turned + kViewSegs - 1) / kViewSegs + stages +
+         (fused ? 0 : views) + skinny;
 }
 
 extern "C" {
@@ -748,8 +767,7 @@ muon_status_t muon_momentum_state(muon_handle_t h, const muon_view_t* G, const m
   }
   DeviceGuard guard(h->device);
   trace(h, -1, stream);
-  const cudaError_t e = enqueue_momentum(h, in, format == MUON_STATE_INT8 ? kStateInt8 : kStateE4M3, hp, seed, true,
-                                         nullptr, stream);
+  const cudaError_t e = momentum_pass(h, in, format_of(format), kPassMomentum, hp, seed, stream);
   trace_call_end(h);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }
@@ -779,14 +797,12 @@ muon_status_t muon_step_state(muon_handle_t h, const muon_view_t* W, const muon_
     if (r == MUON_OK) r = make_side(W[j], sh.rows, sh.cols, true, &items[j].dst);
     if (r != MUON_OK) return r;
     in[j].state = S[j];
-    staged(h, first[j], items[j].count, &items[j].src, &in[j].u);
+    stage(h, first[j], items[j].count, &items[j], &in[j].u);
   }
   DeviceGuard guard(h->device);
   NvtxRange range("muon_step_state");
   trace(h, -1, stream);
-  cudaError_t e = enqueue_momentum(h, in, format == MUON_STATE_INT8 ? kStateInt8 : kStateE4M3, hp, seed, false, &items,
-                                   stream);
-  if (e == cudaSuccess) e = half_run(h, items, hp, false, true, stream);
+  const cudaError_t e = run_step(h, items, in, format_of(format), hp, seed, stream);
   trace_call_end(h);
   return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
 }

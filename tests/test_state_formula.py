@@ -140,12 +140,11 @@ def test_null_handles_refused():
 
 
 def test_half_workspace():
-    """Groups of at most 128 rows and 4096 columns need no operand buffers; fp32 handles stage U in fp32."""
+    """Groups of at most 128 rows and 4096 columns need no operand buffers, the others the same as with bf16 operands."""
     few = B.muon_workspace_size([(64, 768)], B.MUON_BF16, B.MUON_MODE_HALF)
     assert few < B.muon_workspace_size([(64, 768)], B.MUON_BF16, B.MUON_MODE_FAST)
-    assert B.muon_workspace_size([(512, 768)], B.MUON_BF16, B.MUON_MODE_HALF) == \
-        B.muon_workspace_size([(512, 768)], B.MUON_BF16, B.MUON_MODE_FAST)
-    more = B.muon_workspace_size([(512, 768)], B.MUON_FP32, B.MUON_MODE_HALF)
-    assert more >= B.muon_workspace_size([(512, 768)], B.MUON_BF16, B.MUON_MODE_HALF) + 512 * 768 * 4
+    for dtype in (B.MUON_BF16, B.MUON_FP32):
+        assert B.muon_workspace_size([(512, 768)], dtype, B.MUON_MODE_HALF) == \
+            B.muon_workspace_size([(512, 768)], dtype, B.MUON_MODE_FAST)
     with pytest.raises(B.MuonError):
         B.muon_workspace_size([(512, 768)], B.MUON_FP16, B.MUON_MODE_HALF)
