@@ -61,18 +61,19 @@ template <bool WR>
 struct FLayout {
   static constexpr int NST = WR ? 3 : 5;
   static constexpr uint32_t SB = A_STAGE + (WR ? 2 : 1) * B_STAGE;
-  // Each epilogue warp owns one 8 KB block: its two store tiles, then its two A chunks.  The
-  // fp32 staging of the fused parameter write overlays the warp's own block only (a warp on a
+  // Each epilogue warp owns one 8 KB block: four tiles, each for a chunk of the polynomial's A and then
+  // for the result that leaves in its place.  The fp32 staging of the fused parameter write overlays the warp's own block only (a warp on a
   // parameter-writing tile has no store or A load of its own in flight), never another warp's:
   // the warps of a pair drift apart by up to two tiles, and a neighbour may still be reading
   // its A chunks of an earlier polynomial tile.
   static constexpr uint32_t EPI_OFFSET = NST * SB;
-  static constexpr uint32_t EPI_WARP_BYTES = 2 * EPI_OUT_BYTES + 2 * EPI_AUX_BYTES;
+  static constexpr uint32_t EPI_WARP_BYTES = 4 * EPI_OUT_BYTES;
   static constexpr uint32_t BAR_OFFSET = EPI_OFFSET + EPI_WARPS * EPI_WARP_BYTES;
   static constexpr size_t SMEM_BYTES = 1024 + BAR_OFFSET + BAR_BYTES;
   static_assert(EPI_F32_BYTES <= EPI_WARP_BYTES, "fp32 staging must fit the warp's own block");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
-  static_assert(2 * NST + 5 + 2 * EPI_WARPS <= BAR_BYTES / 8, "barriers must fit their region");
+  static_assert(EPI_AUX_BYTES == EPI_OUT_BYTES, "a chunk of A and its result share a tile");
+  static_assert(2 * NST + 5 + EPI_WARPS <= BAR_BYTES / 8, "barriers must fit their region");
 };
 constexpr unsigned int ARRIVALS_PER_TILE = 2 * EPI_WARPS;   // epilogue warps of both CTAs
 static_assert(sizeof(NsParams) <= 32764, "kernel parameters are limited to 32764 bytes");
@@ -206,7 +207,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   auto acce_bar = [&](int a) { return bar0 + 8u * (2 * NST + 2 + a); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  auto aux_bar = [&](int w, int j) { return bar0 + 8u * (2 * NST + 5 + 2 * w + j); };
+  auto aux_bar = [&](int w) { return bar0 + 8u * (2 * NST + 5 + w); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();           // 0: issues the MMAs; 1: its peer
@@ -222,8 +223,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       mbar_init(accf_bar(a), 1);                    // one multicast commit
       mbar_init(acce_bar(a), ARRIVALS_PER_TILE);    // every epilogue warp of both CTAs
     }
-    for (int w = 0; w < EPI_WARPS; ++w)
-      for (int j = 0; j < 2; ++j) mbar_init(aux_bar(w, j), 1);  // the warp's arrive.expect_tx
+    for (int w = 0; w < EPI_WARPS; ++w) mbar_init(aux_bar(w), 1);  // the warp's arrive.expect_tx
     *abort_flag = 0;
     fence_barrier_init();
   }
@@ -429,15 +429,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     uint8_t* wblock = smem + EPI_OFFSET + e * EPI_WARP_BYTES;  // this warp's own epilogue block
     uint8_t* otile = wblock;
     const uint32_t otile_u32 = smem_u32(otile);
-    const uint8_t* abuf = wblock + 2 * EPI_OUT_BYTES;  // this warp's two A chunks
-    const uint32_t abuf_u32 = smem_u32(abuf);
-    uint32_t naux = 0, nissued = 0;   // A chunks consumed / requested (their buffers alternate)
+    uint32_t naux = 0, nissued = 0;   // sets of four A chunks consumed / requested
     float* st32 = reinterpret_cast<float*>(wblock);
     const int sub_r = lane >> 2, sub_c = (lane & 3) * 8;
     const int swz = (lane >> 1) & 3;  // 64-byte swizzle of this lane's staging row
     uint32_t uses[2] = {0u, 0u};
     int next_slot = 0;
-    int nchunk = 0;                   // chunks stored so far (alternates the staging tiles)
     bool ok = true;
     for (int t = p.t_begin + cl; t < p.t_end && ok; t += ncl) {
       const FTile f = decode(p, t);
@@ -471,17 +468,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       };
       // column (within the tile) of chunk c of half h for this warp
       auto chunk_col = [&](int h, int c) { return h * TILE + cbase + c * 32; };
-      const int nchunks = 4 * nsub;     // this warp's chunks of the tile, j = 4 h + c
-      auto aux_issue = [&](int j) {     // lane 0: chunk j of this warp into buffer (naux + j) & 1
-        const uint32_t n = naux + static_cast<uint32_t>(j);
+      // lane 0: the four chunks of A under half h, into the tiles their results will leave from
+      auto aux_issue = [&](int h) {
+        bulk_wait_read<0>();  // the tiles' last stores have been read
         ++nissued;
-        mbar_arrive_expect_tx(aux_bar(e, n & 1), EPI_AUX_BYTES);
-        tma_load_3d(abuf_u32 + (n & 1) * EPI_AUX_BYTES, &G.a_st, aux_bar(e, n & 1), f.col0 + chunk_col(j >> 2, j & 3),
-                    gr0, f.mat);
+        mbar_arrive_expect_tx(aux_bar(e), 4 * EPI_AUX_BYTES);
+        for (int c = 0; c < 4; ++c)
+          tma_load_3d(otile_u32 + c * EPI_OUT_BYTES, &G.a_st, aux_bar(e), f.col0 + chunk_col(h, c), gr0, f.mat);
       };
       if (aux) {
         // A is this round's Gram output, written by other pairs: wait for it as the producer
-        // does, then fetch the first two chunks by TMA
+        // does, then fetch this warp's chunks by TMA
         const unsigned int* dep;
         unsigned int target;
         bool dok = true;
@@ -490,7 +487,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           if (dok) {
             fence_proxy_async_global();
             aux_issue(0);
-            aux_issue(1);
           }
         }
         ok = __shfl_sync(0xffffffffu, dok ? 1 : 0, 0) != 0;
@@ -530,116 +526,130 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       for (int h = 0; h < nsub; ++h) {
         const int slot = nsub == 1 ? sl : h;
         const uint32_t acce_leader = map_to_rank(acce_bar(slot), 0);
+        if (fw) {
 #pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          const int colw = chunk_col(h, c);
-          const int gc0 = f.col0 + colw;
-          float v[32];
-          __syncwarp();
-          tmem_ld_32cols(tmem_base + tlane + tcol0 + static_cast<uint32_t>(colw), v);
-          if (c == 3) {
-            // this warp's part of the slot has been read: hand it back to the MMA issuer
-            tc_fence_before();
+          for (int c = 0; c < 4; ++c) {
+            const int colw = chunk_col(h, c);
+            const int gc0 = f.col0 + colw;
+            float v[32];
             __syncwarp();
-            if (lane == 0) mbar_arrive_remote(acce_leader);
-          }
-          uint4 nx[4];
-          if (has_pre) {
-            if (c + 1 < 4)
-              pre_load(chunk_col(h, c + 1), nx);
-            else if (h + 1 < nsub)
-              pre_load(chunk_col(h + 1, 0), nx);
-          }
-          if (fw) {
-            // Last Update: write the parameters instead of X_k (no chunk straddles the padding:
-            // real dimensions are multiples of 32), from X_k as its bf16 store would hold it, so
-            // the write is exactly param_write_kernel's on the stored X_k.
-            if (gr0 < G.m_real && gc0 < G.n_real) {
-              if (!tr) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4)
-                  *reinterpret_cast<float4*>(st32 + lane * F32_PITCH + i) =
-                      make_float4(Operand<HALF>::round(s * v[i]), Operand<HALF>::round(s * v[i + 1]), Operand<HALF>::round(s * v[i + 2]),
-                                Operand<HALF>::round(s * v[i + 3]));
-              } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) st32[i * F32_PITCH + lane] = Operand<HALF>::round(s * v[i]);
-              }
+            tmem_ld_32cols(tmem_base + tlane + tcol0 + static_cast<uint32_t>(colw), v);
+            if (c == 3) {
+              // this warp's part of the slot has been read: hand it back to the MMA issuer
+              tc_fence_before();
               __syncwarp();
+              if (lane == 0) mbar_arrive_remote(acce_leader);
+            }
+            uint4 nx[4];
+            if (has_pre) {
+              if (c + 1 < 4)
+                pre_load(chunk_col(h, c + 1), nx);
+              else if (h + 1 < nsub)
+                pre_load(chunk_col(h + 1, 0), nx);
+            }
+            {
+              // Last Update: write the parameters instead of X_k (no chunk straddles the padding:
+              // real dimensions are multiples of 32), from X_k as its bf16 store would hold it, so
+              // the write is exactly param_write_kernel's on the stored X_k.
+              if (gr0 < G.m_real && gc0 < G.n_real) {
+                if (!tr) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int rr = q * 8 + sub_r;
-                const float4 o0 = *reinterpret_cast<const float4*>(st32 + rr * F32_PITCH + sub_c);
-                const float4 o1 = *reinterpret_cast<const float4*>(st32 + rr * F32_PITCH + sub_c + 4);
-                float r8[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
-                if (wread) {
-                  float w8[8];
-                  unpack8<false>(pf[q], w8);
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) r8[i] = fmaf(p.w_decay, w8[i], cw * r8[i]);
+                  for (int i = 0; i < 32; i += 4)
+                    *reinterpret_cast<float4*>(st32 + lane * F32_PITCH + i) =
+                        make_float4(Operand<HALF>::round(s * v[i]), Operand<HALF>::round(s * v[i + 1]), Operand<HALF>::round(s * v[i + 2]),
+                                  Operand<HALF>::round(s * v[i + 3]));
                 } else {
 #pragma unroll
-                  for (int i = 0; i < 8; ++i) r8[i] = cw * r8[i];
+                  for (int i = 0; i < 32; ++i) st32[i * F32_PITCH + lane] = Operand<HALF>::round(s * v[i]);
                 }
-                __stcs(reinterpret_cast<uint4*>(W + woff(gc0, rr)), pack8<false>(r8));
-              }
-              __syncwarp();
-            }
+                __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 4; ++q) pf[q] = nx[q];
-            continue;
+                for (int q = 0; q < 4; ++q) {
+                  const int rr = q * 8 + sub_r;
+                  const float4 o0 = *reinterpret_cast<const float4*>(st32 + rr * F32_PITCH + sub_c);
+                  const float4 o1 = *reinterpret_cast<const float4*>(st32 + rr * F32_PITCH + sub_c + 4);
+                  float r8[8] = {o0.x, o0.y, o0.z, o0.w, o1.x, o1.y, o1.z, o1.w};
+                  if (wread) {
+                    float w8[8];
+                    unpack8<false>(pf[q], w8);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r8[i] = fmaf(p.w_decay, w8[i], cw * r8[i]);
+                  } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) r8[i] = cw * r8[i];
+                  }
+                  __stcs(reinterpret_cast<uint4*>(W + woff(gc0, rr)), pack8<false>(r8));
+                }
+                __syncwarp();
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q) pf[q] = nx[q];
+            }
           }
+        } else {
+          // This warp's part of the half, 32 rows x 128 columns, in two reads, then the slot handed
+          // back and four chunks stored from four tiles.  Chunk by chunk, each waiting for the last one's
+          // read and store, took 0.6 k cycles a tile longer, which a stage of few tiles cannot hide.
           if (aux) {
-            // this lane's row of the chunk of A (64-byte rows, 64-byte swizzle, as TMA wrote them)
-            const int j = 4 * h + c;
-            const uint32_t n = naux + static_cast<uint32_t>(j);
-            if (!mbar_wait_bounded(aux_bar(e, n & 1), (n >> 1) & 1u, tmo, abort_flag, p.status)) {
+            if (lane == 0 && h > 0) aux_issue(h);
+            if (!mbar_wait_bounded(aux_bar(e), naux & 1u, tmo, abort_flag, p.status)) {
               ok = false;
               break;
             }
-            const uint8_t* arow = abuf + (n & 1) * EPI_AUX_BYTES + lane * 64;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              float a8[8];
-              unpack8<HALF>(*reinterpret_cast<const uint4*>(arow + ((q ^ swz) << 4)), a8);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) v[8 * q + i] = s * fmaf(c_acc, v[8 * q + i], c_aux * a8[i]);
-            }
-            // every lane has used its row: the buffer may take the chunk two ahead
-            __syncwarp();
-            if (lane == 0 && j + 2 < nchunks) {
-              fence_async_smem();
-              aux_issue(j + 2);
-            }
+            ++naux;
           } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = s * c_acc * v[i];
+            if (lane == 0) bulk_wait_read<0>();  // the tiles' last stores have been read
           }
-          if (gc0 == gr0) {
-            // the chunk on the diagonal: the polynomial adds a on the real diagonal (B' = a I + ...)
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (gc0 + i == gr) v[i] += cdiag;
-          }
-          // the store issued two chunks ago used this staging tile: wait until it has been read
-          const uint32_t ob = (nchunk & 1) * EPI_OUT_BYTES;
-          ++nchunk;
-          if (lane == 0) bulk_wait_read<1>();
           __syncwarp();
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
-            *reinterpret_cast<uint4*>(otile + ob + lane * 64 + ((q ^ swz) << 4)) = pack8<HALF>(v + 8 * q);
+          for (int cc = 0; cc < 4; cc += 2) {
+            float v[64];
+            tmem_ld_64cols(tmem_base + tlane + tcol0 + static_cast<uint32_t>(chunk_col(h, cc)), v);
+            if (cc == 2) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive_remote(acce_leader);
+            }
+#pragma unroll
+            for (int c = cc; c < cc + 2; ++c) {
+              const int gc0 = f.col0 + chunk_col(h, c);
+              uint8_t* row = otile + c * EPI_OUT_BYTES + lane * 64;  // 64-byte rows, 64-byte swizzle
+              float* x = v + 32 * (c - cc);
+              if (aux) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  float a8[8];  // this lane's row of the chunk of A, as TMA wrote it
+                  unpack8<HALF>(*reinterpret_cast<const uint4*>(row + ((q ^ swz) << 4)), a8);
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) x[8 * q + i] = s * fmaf(c_acc, x[8 * q + i], c_aux * a8[i]);
+                }
+              } else {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = s * c_acc * x[i];
+              }
+              if (gc0 == gr0) {
+                // the chunk on the diagonal: the polynomial adds a on the real diagonal (B' = a I + ...)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (gc0 + i == gr) x[i] += cdiag;
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(row + ((q ^ swz) << 4)) = pack8<HALF>(x + 8 * q);
+            }
+          }
           fence_async_smem();
           __syncwarp();
           if (lane == 0) {
-            tma_store_3d(out_map, otile_u32 + ob, gc0, gr0, f.mat);
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              tma_store_3d(out_map, otile_u32 + c * EPI_OUT_BYTES, f.col0 + chunk_col(h, c), gr0, f.mat);
             bulk_commit();
           }
         }
         if (!ok) break;
       }
       if (!ok) break;
-      if (aux) naux += static_cast<uint32_t>(nchunks);
       if (nsub == 1) {
         ++uses[sl];
       } else {
@@ -662,10 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     if (lane == 0) bulk_wait_all();
     // after an early exit, A chunks may still be on their way into this warp's buffers: wait
     // (bounded) for them before the CTA leaves
-    if (lane == 0) {
-      for (uint32_t n = naux; n < nissued; ++n)
-        (void)mbar_wait_bounded(aux_bar(e, n & 1), (n >> 1) & 1u, tmo, nullptr, p.status);
-    }
+    if (lane == 0 && naux < nissued) (void)mbar_wait_bounded(aux_bar(e), naux & 1u, tmo, nullptr, p.status);
     __syncwarp();
   }
 

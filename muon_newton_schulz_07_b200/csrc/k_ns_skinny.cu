@@ -97,6 +97,11 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
   asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
   return v;
 }
+// 16 bytes from global to shared memory without passing through registers.
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI) : "memory"); }
 
 // 8 x 8 transposition of 16-bit values: q[k] holds eight values of row k, then of column k.
@@ -231,10 +236,12 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   }
 
   // ---------------------------------------------------------------- X0 into shared memory
-  // In blocks of 8 rows x 8 columns, eight 16-byte loads of 16-bit sources each: rows of the
+  // In blocks of 8 rows x 8 columns, eight 16-byte copies of 16-bit sources each: rows of the
   // storage are rows of the block or, for transposed storage, its columns.  Eight lanes take
-  // neighbouring columns and a thread always the same rows, so of one matrix.  16-bit values wait
-  // for their norm in shared memory as they came; fp32 ones are read again.
+  // neighbouring columns and a thread always the same rows, so of one matrix.  A block's copies go,
+  // all of a thread's blocks at once (cp.async), to the eight places its rows will have; there the values
+  // wait for their norm, and are transposed on their way through the conversion.  fp32 sources
+  // are read twice instead.
   const int groups = p.width / 8;                // a multiple of 8
   const int ig = (tid >> 3) & 15;                // rows 8 ig .. 8 ig + 7
   const int i0 = (ig * 8) & (p.slot_rows - 1);   // the first of them, within the matrix
@@ -265,10 +272,6 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   // Blocks that reach over the matrix's edge or whose rows are not aligned go value by value, in
   // loops: this code runs once per tile, and what it costs is fetching its instructions.
   auto whole = [&](const Block& b, bool vec) { return vec && b.rows >= 8 && b.have >= 8; };
-  auto x_value = [&](int u, bool tr, int k, int i) {  // value i of storage row k of block (ig, u), in X
-    const int row = ig * 8 + (tr ? i : k), at = tr ? k : i;
-    return reinterpret_cast<uint16_t*>(xbuf + group_at(row, u) + at * 2);
-  };
   const bool src_tr = sg.src_tr != 0, src_vec = sg.src_vec != 0;
   if (warp < EPI_WARPS) {
     float ss = 0.0f;
@@ -276,46 +279,63 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
 #pragma unroll 1
     for (int u = u0; u < groups; u += EPI / 16) {
       const Block b = block_of(u, src_tr, sg.src_ld, sg.src_bs);
-      if (b.rows <= 0) {
-        if (!wide_src) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = make_uint4(0, 0, 0, 0);
-        }
-      } else if (!whole(b, src_vec)) {
+      if (wide_src) {
+        if (whole(b, src_vec)) {
+          const float* src = static_cast<const float*>(sg.src) + b.at;
+          float4 q[8];
 #pragma unroll 1
-        for (int i = 0; i < 64; ++i) {
-          const int k = i >> 3, c = i & 7;
-          const bool there = k < b.rows && c < b.have;
-          const float v = there ? load_one(sg.src, sg.src_type, b.at + k * b.ld + c) : 0.0f;
-          ss = fmaf(v, v, ss);
-          if (!wide_src) *x_value(u, src_tr, k, c) = there ? static_cast<const uint16_t*>(sg.src)[b.at + k * b.ld + c] : 0;
-        }
-      } else if (wide_src) {
-        const float* src = static_cast<const float*>(sg.src) + b.at;
-        float4 q[8];
+          for (int h = 0; h < 8; h += 4) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) q[k] = __ldg(reinterpret_cast<const float4*>(src + (k >> 1) * b.ld + (k & 1) * 4));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) ss = fmaf(q[k].x, q[k].x, fmaf(q[k].y, q[k].y, fmaf(q[k].z, q[k].z, fmaf(q[k].w, q[k].w, ss))));
+            src += 4 * b.ld;
+          }
+        } else {
 #pragma unroll 1
-        for (int h = 0; h < 8; h += 4) {
+          for (int i = 0; i < 64 && b.rows > 0; ++i) {
+            const int k = i >> 3, c = i & 7;
+            const float v = k < b.rows && c < b.have ? static_cast<const float*>(sg.src)[b.at + k * b.ld + c] : 0.0f;
+            ss = fmaf(v, v, ss);
+          }
+        }
+      } else if (whole(b, src_vec)) {
+        const uint16_t* src = static_cast<const uint16_t*>(sg.src) + b.at;
+        if (!src_tr) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) q[k] = __ldg(reinterpret_cast<const float4*>(src + (k >> 1) * b.ld + (k & 1) * 4));
+          for (int k = 0; k < 8; ++k) copy_async16(xaddr + group_at(ig * 8 + k, u), src + k * b.ld);
+        } else {  // 64 bytes of a row by a warp, the next by its neighbour: through L1
+          uint4 q[8];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) ss = fmaf(q[k].x, q[k].x, fmaf(q[k].y, q[k].y, fmaf(q[k].z, q[k].z, fmaf(q[k].w, q[k].w, ss))));
-          src += 4 * b.ld;
+          for (int k = 0; k < 8; ++k) q[k] = __ldg(reinterpret_cast<const uint4*>(src + k * b.ld));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = q[k];
         }
       } else {
-        uint4 q[8];
-        const uint16_t* src = static_cast<const uint16_t*>(sg.src) + b.at;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) q[k] = __ldg(reinterpret_cast<const uint4*>(src + k * b.ld));
+        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = make_uint4(0, 0, 0, 0);
+#pragma unroll 1
+        for (int i = 0; i < 64 && b.rows > 0; ++i) {
+          const int k = i >> 3, c = i & 7;
+          if (k < b.rows && c < b.have)
+            *reinterpret_cast<uint16_t*>(xbuf + group_at(ig * 8 + k, u) + c * 2) =
+                static_cast<const uint16_t*>(sg.src)[b.at + k * b.ld + c];
+        }
+      }
+    }
+    if (!wide_src) {
+      copy_async_wait();  // a thread reads only what it copied itself
+#pragma unroll 1
+      for (int u = u0; u < groups; u += EPI / 16) {
         if (sg.src_type == kViewBF16) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) squares8<kViewBF16>(q[k], ss2);
+          for (int k = 0; k < 8; ++k)
+            squares8<kViewBF16>(*reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u)), ss2);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) squares8<kViewF16>(q[k], ss2);
+          for (int k = 0; k < 8; ++k)
+            squares8<kViewF16>(*reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u)), ss2);
         }
-        if (src_tr) transpose8(q);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = q[k];
       }
     }
     ss += ss2.x + ss2.y;
@@ -352,8 +372,11 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     const float f = out ? 0.0f : factor[slot_l];
 #pragma unroll 1
     for (int u = u0; u < groups; u += EPI / 16) {
-      if (wide_src) {
-        const Block b = block_of(u, src_tr, sg.src_ld, sg.src_bs);
+      const Block b = block_of(u, src_tr, sg.src_ld, sg.src_bs);
+      if (out || b.rows <= 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = make_uint4(0, 0, 0, 0);
+      } else if (wide_src) {
         const bool full = whole(b, src_vec);
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {  // (fp32: the second read, an L2 hit)
@@ -366,31 +389,29 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
               v[i] = k < b.rows && i < b.have ? static_cast<const float*>(sg.src)[b.at + k * b.ld + i] : 0.0f;
           }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] = out ? 0.0f : v[i] * f;
+          for (int i = 0; i < 8; ++i) v[i] *= f;
           if (!src_tr) {
             *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = pack8h(v);
           } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) *x_value(u, true, k, i) = __half_as_ushort(__float2half_rn(v[i]));
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<__half*>(xbuf + group_at(ig * 8 + i, u) + k * 2) = __float2half_rn(v[i]);
           }
         }
-      } else if (out) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = make_uint4(0, 0, 0, 0);
       } else {
+        uint4 q[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) q[k] = *reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u));
         if (sg.src_type == kViewBF16) {
-#pragma unroll 4
-          for (int k = 0; k < 8; ++k) {
-            uint4* at = reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u));
-            *at = rescale8<kViewBF16, kViewF16>(*at, f);
-          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) q[k] = rescale8<kViewBF16, kViewF16>(q[k], f);
         } else {
-#pragma unroll 4
-          for (int k = 0; k < 8; ++k) {
-            uint4* at = reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u));
-            *at = rescale8<kViewF16, kViewF16>(*at, f);
-          }
+#pragma unroll
+          for (int k = 0; k < 8; ++k) q[k] = rescale8<kViewF16, kViewF16>(q[k], f);
         }
+        if (src_tr) transpose8(q);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = q[k];
       }
     }
   }
@@ -704,7 +725,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
             const int k = i >> 3, c = i & 7;
             if (k < b.rows && c < b.have) {
               const long long at = b.at + k * b.ld + c;
-              const float x = coef * __half2float(__ushort_as_half(*x_value(u, dst_tr, k, c)));
+              const int row = ig * 8 + (dst_tr ? c : k), col = dst_tr ? k : c;
+              const float x = coef * __half2float(*reinterpret_cast<const __half*>(xbuf + group_at(row, u) + col * 2));
               const float w = p.decay != 0.0f ? load_one(sg.dst, sg.dst_type, at) : 0.0f;
               store_one(sg.dst, sg.dst_type, at, p.decay != 0.0f ? fmaf(p.decay, w, x) : x);
             }
