@@ -292,11 +292,13 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
             src += 4 * b.ld;
           }
         } else {
-#pragma unroll 1
-          for (int i = 0; i < 64 && b.rows > 0; ++i) {
-            const int k = i >> 3, c = i & 7;
-            const float v = k < b.rows && c < b.have ? static_cast<const float*>(sg.src)[b.at + k * b.ld + c] : 0.0f;
-            ss = fmaf(v, v, ss);
+#pragma unroll 2
+          for (int k = 0; k < min(b.rows, 8); ++k) {
+            float v[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) v[c] = c < b.have ? static_cast<const float*>(sg.src)[b.at + k * b.ld + c] : 0.0f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) ss = fmaf(v[c], v[c], ss);
           }
         }
       } else if (whole(b, src_vec)) {
@@ -312,14 +314,14 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
           for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = q[k];
         }
       } else {
+#pragma unroll 2
+        for (int k = 0; k < 8; ++k) {
+          uint32_t w[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) = make_uint4(0, 0, 0, 0);
-#pragma unroll 1
-        for (int i = 0; i < 64 && b.rows > 0; ++i) {
-          const int k = i >> 3, c = i & 7;
-          if (k < b.rows && c < b.have)
-            *reinterpret_cast<uint16_t*>(xbuf + group_at(ig * 8 + k, u) + c * 2) =
-                static_cast<const uint16_t*>(sg.src)[b.at + k * b.ld + c];
+          for (int c = 0; c < 8; ++c)
+            w[c] = k < b.rows && c < b.have ? static_cast<const uint16_t*>(sg.src)[b.at + k * b.ld + c] : 0u;
+          *reinterpret_cast<uint4*>(xbuf + group_at(ig * 8 + k, u)) =
+              make_uint4(w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16);
         }
       }
     }
@@ -721,14 +723,17 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
           for (int k = 0; k < 8; ++k) write_eight(sg.dst, sg.dst_type, b.at + k * b.ld, q[k], coef, p.decay);
         } else {
 #pragma unroll 1
-          for (int i = 0; i < 64; ++i) {
-            const int k = i >> 3, c = i & 7;
-            if (k < b.rows && c < b.have) {
-              const long long at = b.at + k * b.ld + c;
+          for (int k = 0; k < min(b.rows, 8); ++k) {
+            float w[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              w[c] = p.decay != 0.0f && c < b.have ? load_one(sg.dst, sg.dst_type, b.at + k * b.ld + c) : 0.0f;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
               const int row = ig * 8 + (dst_tr ? c : k), col = dst_tr ? k : c;
               const float x = coef * __half2float(*reinterpret_cast<const __half*>(xbuf + group_at(row, u) + col * 2));
-              const float w = p.decay != 0.0f ? load_one(sg.dst, sg.dst_type, at) : 0.0f;
-              store_one(sg.dst, sg.dst_type, at, p.decay != 0.0f ? fmaf(p.decay, w, x) : x);
+              if (c < b.have)
+                store_one(sg.dst, sg.dst_type, b.at + k * b.ld + c, p.decay != 0.0f ? fmaf(p.decay, w[c], x) : x);
             }
           }
         }

@@ -47,27 +47,21 @@ constexpr uint32_t CHUNK = 16384;  // one 64-deep slice of a 128-row (or 128-col
 constexpr size_t SMEM_BYTES = 1024 + BAR_OFF + 64;
 constexpr int THREADS = 256;        // 8 warps, two per TMEM lane quadrant
 
-__device__ __forceinline__ uint4 pack8(const float* v) {
-  uint4 q;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&q);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-  return q;
-}
-
 // 32 values of row r (0..127), columns 32 ch .. 32 ch + 31, into a K-major 128-row operand.
+template <bool HALF>
 __device__ __forceinline__ void put_kmajor(uint8_t* buf, int r, int ch, const float* v) {
   const int kc = ch >> 1, u0 = (ch & 1) * 4;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    *reinterpret_cast<uint4*>(buf + kc * CHUNK + r * 128 + (((u0 + q) ^ (r & 7)) << 4)) = pack8(v + 8 * q);
+    *reinterpret_cast<uint4*>(buf + kc * CHUNK + r * 128 + (((u0 + q) ^ (r & 7)) << 4)) = pack8<HALF>(v + 8 * q);
 }
 
 // Issue one 256 x 256 x 256 product into TMEM columns d_col (even CTA, one thread).
+template <bool HALF>
 __device__ __forceinline__ void issue_product(uint32_t tmem, uint32_t d_col, uint32_t a_addr, bool a_mn,
                                               uint32_t b_addr, bool b_mn, uint32_t bar) {
   tc_fence_after();
-  const uint32_t idesc = idesc_bf16_f32(256, 256, a_mn ? 1 : 0, b_mn ? 1 : 0);
+  const uint32_t idesc = idesc_f16_f32(HALF, 256, 256, a_mn ? 1 : 0, b_mn ? 1 : 0);
 #pragma unroll 1
   for (int kb = 0; kb < 4; ++kb) {
     // K-major: 16 k per step = 32 bytes along the swizzled row; MN-major: 16 k rows = 2 KB,
@@ -83,6 +77,7 @@ __device__ __forceinline__ void issue_product(uint32_t tmem, uint32_t d_col, uin
   tc_commit_pair_mc(bar, 0x3);  // both CTAs learn that the product is in TMEM
 }
 
+template <bool HALF>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     ns_small_kernel(const __grid_constant__ SmallParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -140,7 +135,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
     while (g + 1 < p.ngroups && p.g[g + 1].mat_begin <= m) ++g;
     const SmGroup& G = p.g[g];
     const int mat = m - G.mat_begin;
-    const float alpha = p.scal[2 * (G.scal_base + mat) + 1];
+    const float alpha = HALF ? 1.0f : p.scal[2 * (G.scal_base + mat) + 1];  // (an fp16 X0 is normalised already)
 
     // X0: this CTA's rows (K-major) and columns (MN-major), each CTA from its own barrier.
     if (threadIdx.x == 0 && ok) {
@@ -160,10 +155,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll 1
     for (int it = 1; it <= p.k; ++it) {
       const bool first = it == 1, last = it == p.k;
+      const float ca = p.coef[it - 1][0], cb = p.coef[it - 1][1], cc = p.coef[it - 1][2];
       // ---------------------------------------------------------------- A = s X X^T
-      if (issuer && ok) issue_product(tmem, 0, sbase + XROW_OFF, false, sbase + XROW_OFF, false, mma_bar);
+      if (issuer && ok) issue_product<HALF>(tmem, 0, sbase + XROW_OFF, false, sbase + XROW_OFF, false, mma_bar);
       wait_product();
-      const float sg = first ? alpha * alpha : 1.0f;
+      const float sg = HALF ? p.gram : first ? alpha * alpha : 1.0f;
       if (ok) {
 #pragma unroll 1
         for (int c = 0; c < 4; ++c) {
@@ -172,13 +168,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           tmem_ld_32cols(t_row + ch * 32, v);
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= sg;
-          put_kmajor(smem + ABUF_OFF, r, ch, v);
+          put_kmajor<HALF>(smem + ABUF_OFF, r, ch, v);
         }
       }
       fence_async_smem();
       sync_pair();
       // ---------------------------------------------------------------- B' = a I + b A + c A A
-      if (issuer && ok) issue_product(tmem, 256, sbase + ABUF_OFF, false, sbase + ABUF_OFF, false, mma_bar);
+      if (issuer && ok) issue_product<HALF>(tmem, 256, sbase + ABUF_OFF, false, sbase + ABUF_OFF, false, mma_bar);
       wait_product();
       if (ok) {
 #pragma unroll 1
@@ -191,17 +187,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
           for (int i = 0; i < 32; ++i) {
             // b A uses the bf16 A that A A was formed from, so that B' is the polynomial of one
             // matrix (the rounded A); mixing the unrounded A in spoils the quintic's cancellation.
-            const float ar = __bfloat162float(__float2bfloat16_rn(sg * av[i]));
+            const float ar = Operand<HALF>::round(sg * av[i]);
             const int col = ch * 32 + i;
-            aa[i] = p.c * aa[i] + p.b * ar + ((col == gr && gr < G.m_real) ? p.a : 0.0f);
+            aa[i] = cc * aa[i] + cb * ar + ((col == gr && gr < G.m_real) ? ca : 0.0f);
           }
-          put_kmajor(smem + ABUF_OFF, r, ch, aa);  // the products reading ABUF have completed
+          put_kmajor<HALF>(smem + ABUF_OFF, r, ch, aa);  // the products reading ABUF have completed
         }
       }
       fence_async_smem();
       sync_pair();
       // ---------------------------------------------------------------- X' = s B' X
-      if (issuer && ok) issue_product(tmem, 0, sbase + ABUF_OFF, false, sbase + XCOL_OFF, true, mma_bar);
+      if (issuer && ok) issue_product<HALF>(tmem, 0, sbase + ABUF_OFF, false, sbase + XCOL_OFF, true, mma_bar);
       wait_product();
       const float su = first ? alpha : 1.0f;
       if (ok) {
@@ -213,21 +209,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] *= su;
           if (!last) {
-            put_kmajor(smem + XROW_OFF, r, ch, v);
+            put_kmajor<HALF>(smem + XROW_OFF, r, ch, v);
             // columns 32 ch.. of row gr, in the XCOL of CTA `half`
             const int cw = ch * 32 - half * 128;
             const int cc = cw >> 6, u0 = (cw & 63) >> 3;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
               const uint32_t off = kb_r * CHUNK + cc * 8192 + rr * 128 + (((u0 + q) ^ (rr & 7)) << 4);
-              st_cluster_v4(xcol_base + off, pack8(v + 8 * q));
+              st_cluster_v4(xcol_base + off, pack8<HALF>(v + 8 * q));
             }
           } else {
-            __nv_bfloat16* out = static_cast<__nv_bfloat16*>(G.out) +
+            uint16_t* out = static_cast<uint16_t*>(G.out) +
                                  static_cast<size_t>(mat) * kSmallTile * kSmallTile +
                                  static_cast<size_t>(gr) * kSmallTile + ch * 32;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(out)[q] = pack8(v + 8 * q);
+            for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(out)[q] = pack8<HALF>(v + 8 * q);
           }
         }
       }
@@ -249,8 +245,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(THREADS, 1)
 
 size_t small_smem_bytes() { return SMEM_BYTES; }
 
-cudaError_t launch_ns_small(const SmallParams& p, int num_sms, cudaStream_t s) {
-  if (p.total <= 0) return cudaSuccess;
+namespace {
+template <bool HALF>
+cudaError_t launch(const SmallParams& p, int num_sms, cudaStream_t s) {
   // The shared-memory limit is a property of the function on each device: set it once per device.
   static std::atomic<unsigned long long> attr_set{0};
   int dev = 0;
@@ -258,14 +255,20 @@ cudaError_t launch_ns_small(const SmallParams& p, int num_sms, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if ((attr_set.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(ns_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(ns_small_kernel<HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(SMEM_BYTES));
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(bit);
   }
   const int grid = 2 * std::min(num_sms / 2, p.total);
-  ns_small_kernel<<<grid, THREADS, SMEM_BYTES, s>>>(p);
+  ns_small_kernel<HALF><<<grid, THREADS, SMEM_BYTES, s>>>(p);
   return cudaGetLastError();
+}
+}  // namespace
+
+cudaError_t launch_ns_small(const SmallParams& p, int num_sms, cudaStream_t s) {
+  if (p.total <= 0) return cudaSuccess;
+  return p.half ? launch<true>(p, num_sms, s) : launch<false>(p, num_sms, s);
 }
 
 }  // namespace muon

@@ -440,6 +440,24 @@ void muon::fused_tables(const std::vector<const GroupPlan*>& groups, int nslots,
   q->total_tiles = (k - 1) * iter_tiles[0] + iter_tiles[1];
 }
 
+void muon::small_groups(const muon_ctx* h, const std::vector<const GroupPlan*>& groups, int fin, SmallParams* p) {
+  int mats = 0;
+  for (size_t g = 0; g < groups.size(); ++g) {
+    const GroupPlan& gp = *groups[g];
+    SmGroup& G = p->g[g];
+    G.tm_row = gp.tm_x[0];
+    G.tm_col = gp.tt_x[0];
+    G.out = h->ws + gp.off_x[fin];
+    G.mat_begin = mats;
+    G.cnt = gp.cnt;
+    G.scal_base = gp.scal_base;
+    G.m_real = gp.m;
+    mats += gp.cnt;
+  }
+  p->ngroups = static_cast<int>(groups.size());
+  p->total = mats;
+}
+
 void muon::fused_maps(const std::vector<const GroupPlan*>& groups, NsParams* q) {
   for (size_t g = 0; g < groups.size(); ++g) {
     const GroupPlan& gp = *groups[g];
@@ -499,25 +517,13 @@ cudaError_t enqueue_ns(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st, i
     *fused = false;
     SmallParams& sp = h->sm;
     std::memset(&sp, 0, sizeof(sp));
-    int mats = 0;
-    for (size_t g = 0; g < P.groups.size(); ++g) {
-      const GroupPlan& gp = P.groups[g];
-      SmGroup& G = sp.g[g];
-      G.tm_row = gp.tm_x[0];
-      G.tm_col = gp.tt_x[0];
-      G.out = h->ws + gp.off_x[k & 1];
-      G.mat_begin = mats;
-      G.cnt = gp.cnt;
-      G.scal_base = gp.scal_base;
-      G.m_real = gp.m;
-      mats += gp.cnt;
-    }
-    sp.ngroups = static_cast<int>(P.groups.size());
-    sp.total = mats;
+    small_groups(h, all_groups(P), k & 1, &sp);
     sp.k = k;
-    sp.a = hp->a;
-    sp.b = hp->b;
-    sp.c = hp->c;
+    for (int t = 0; t < k; ++t) {
+      sp.coef[t][0] = hp->a;
+      sp.coef[t][1] = hp->b;
+      sp.coef[t][2] = hp->c;
+    }
     sp.scal = h->d_scal;
     sp.status = h->d_status;
     sp.timeout_ns = kTimeoutNs;

@@ -109,6 +109,8 @@ void stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur, int 
 void fused_tables(const std::vector<const GroupPlan*>& groups, int nslots, int k, bool fuse_write, bool wide,
                   NsParams* q);
 void fused_maps(const std::vector<const GroupPlan*>& groups, NsParams* q);
+// The small-matrix kernel's groups, X_k into buffer `fin`.
+void small_groups(const muon_ctx* h, const std::vector<const GroupPlan*>& groups, int fin, SmallParams* p);
 
 // muon_views.cu: the calls of muon_api.cu on a MUON_MODE_HALF handle
 muon_status_t half_step(muon_ctx* h, void* const* W, const void* const* G, void* const* M, const muon_hparams_t* hp,

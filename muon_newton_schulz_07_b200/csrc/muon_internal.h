@@ -228,7 +228,9 @@ struct SmallParams {
   int ngroups;
   int total;            // matrices in the launch
   int k;                // Newton-Schulz iterations, >= 1
-  float a, b, c;
+  int half;             // operands are fp16 (MUON_MODE_HALF), not bf16; X0 is normalised
+  float gram;           // A = gram * (the Gram product)
+  float coef[64][3];    // B' = coef[0] I + coef[1] A + coef[2] A A, by iteration
   const float* scal;    // per matrix {||U||, 1/(||U||+eps)}
   unsigned int* status;
   unsigned long long timeout_ns;

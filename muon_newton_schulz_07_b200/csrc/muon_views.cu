@@ -111,8 +111,23 @@ bool steps_ok(const muon_ctx* h, const muon_hparams_t* hp) {
   return h->coef.empty() || static_cast<size_t>(hp->ns_steps) * 3 <= h->coef.size();
 }
 
+// The factors of A and B' in a kernel that runs every iteration.
+template <typename Params>
+void fill_iterations(const muon_ctx* h, const muon_hparams_t* hp, Params* p) {
+  p->gram = kHalfA / (kHalfX * kHalfX);
+  for (int t = 0; t < hp->ns_steps; ++t) {
+    float own[3];
+    const float* abc = coef_of(h, hp, t, own);
+    p->coef[t][0] = abc[0];
+    p->coef[t][1] = abc[1] * (1.0f / kHalfA);
+    p->coef[t][2] = abc[2] * (1.0f / (kHalfA * kHalfA));
+  }
+}
+
 const GroupPlan& group_of(const muon_ctx* h, int mat) { return h->plan.groups[h->plan.mat_group[mat]]; }
 bool tall(const muon_ctx* h, int mat) { return h->shapes[mat].rows > h->shapes[mat].cols; }
+
+bool small_tiles(const muon_ctx* h, int k);
 
 // A view segment without its place in a launch.  `store`: the result is O itself, else the step
 // of the parameters.
@@ -192,7 +207,7 @@ cudaError_t view_pass(muon_ctx* h, const std::vector<Item>& items, ViewPass pass
 // The last Update can write the result itself when every destination of the workspace groups is
 // bf16 with aligned rows and every real dimension is a multiple of 32.
 bool result_fusable(const muon_ctx* h, const std::vector<Item>& items, int k) {
-  if (k < 1 || h->n > kTcMaxFused) return false;
+  if (k < 1 || h->n > kTcMaxFused || small_tiles(h, k)) return false;
   for (const Item& it : items) {
     const GroupPlan& gp = group_of(h, it.first);
     if (gp.skinny) continue;
@@ -207,6 +222,32 @@ std::vector<const GroupPlan*> tiled_groups(const muon_ctx* h) {
   for (const GroupPlan& gp : h->plan.groups)
     if (!gp.skinny) v.push_back(&gp);
   return v;
+}
+
+// Whether every group that goes through the workspace is one 256 x 256 tile a matrix, which the
+// small-matrix kernel iterates on chip.
+bool small_tiles(const muon_ctx* h, int k) {
+  const std::vector<const GroupPlan*> groups = tiled_groups(h);
+  if (k < 1 || groups.empty() || groups.size() > static_cast<size_t>(kTcMaxGroups)) return false;
+  for (const GroupPlan* gp : groups)
+    if (gp->mp != kSmallTile || gp->np != kSmallTile) return false;
+  return true;
+}
+
+cudaError_t enqueue_small(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st) {
+  NvtxRange range("muon: Newton-Schulz, all iterations (small matrices)");
+  SmallParams& sp = h->sm;
+  std::memset(&sp, 0, sizeof(sp));
+  small_groups(h, tiled_groups(h), hp->ns_steps & 1, &sp);
+  sp.k = hp->ns_steps;
+  sp.half = 1;
+  fill_iterations(h, hp, &sp);
+  sp.scal = h->d_scal;
+  sp.status = h->d_status;
+  sp.timeout_ns = kTimeoutNs;
+  const cudaError_t e = launch_ns_small(sp, h->num_sms, st);
+  if (e == cudaSuccess) trace(h, MUON_KERNEL_NS_SMALL, st);
+  return e;
 }
 
 // 256 x 256 tiles of an Update over every group, and the CTA pairs that share them.
@@ -265,14 +306,7 @@ cudaError_t enqueue_single(muon_ctx* h, const std::vector<Item>& items, const mu
   fused_tables(groups, h->n, k, fuse, wide_pays(h, groups), &q);
   fused_maps(groups, &q);
   q.half = 1;
-  q.gram = kHalfA / (kHalfX * kHalfX);
-  for (int t = 0; t < k; ++t) {
-    float own[3];
-    const float* abc = coef_of(h, hp, t, own);
-    q.coef[t][0] = abc[0];
-    q.coef[t][1] = abc[1] * (1.0f / kHalfA);
-    q.coef[t][2] = abc[2] * (1.0f / (kHalfA * kHalfA));
-  }
+  fill_iterations(h, hp, &q);
   q.scal = h->d_scal;
   q.status = h->d_status;
   q.deps = reinterpret_cast<unsigned int*>(deps);
@@ -300,6 +334,7 @@ cudaError_t enqueue_tiles(muon_ctx* h, const std::vector<Item>& items, const muo
                           bool fuse, cudaStream_t st) {
   const std::vector<const GroupPlan*> groups = tiled_groups(h);
   if (groups.empty()) return cudaSuccess;
+  if (small_tiles(h, hp->ns_steps)) return enqueue_small(h, hp, st);
   if (single_launch(h, hp->ns_steps)) return enqueue_single(h, items, hp, store, fuse, st);
   const int k = hp->ns_steps;
   for (int t = 0; t < k; ++t) {
@@ -684,10 +719,11 @@ int muon::half_launches(const muon_ctx* h, int k) {
     const GroupPlan& gp = group_of(h, i);
     turned += !gp.skinny && (tall(h, i) || gp.mp != gp.m || gp.np != gp.n);
   }
-  bool fused = k >= 1 && h->dtype == MUON_BF16 && h->n <= kTcMaxFused;
+  bool fused = k >= 1 && h->dtype == MUON_BF16 && h->n <= kTcMaxFused && !small_tiles(h, k);
   for (const GroupPlan& gp : h->plan.groups)
     if (!gp.skinny && (gp.m % 32 != 0 || gp.n % 32 != 0)) fused = false;
   const int stages = ngroups == 0            ? 0
+                     : small_tiles(h, k)     ? 1
                      : single_launch(h, k)   ? (h->schedule == MUON_SCHEDULE_SPLIT ? 3 * k : 1)
                                              : 3 * k * ((ngroups + kTcMaxGroups - 1) / kTcMaxGroups);
   return 2 * ((h->n + kStateSegs - 1) / kStateSegs) + (turned + kViewSegs - 1) / kViewSegs + stages +

@@ -74,7 +74,7 @@ def check(shapes, X, Os, abc, op, what=""):
 
 ON_CHIP = [(1, 1), (1, 7), (7, 1), (5, 3), (8, 64), (64, 768), (128, 128), (100, 333), (333, 100), (17, 769), (128, 1024),
            (31, 2000), (4096, 128), (3, 4096), (128, 700)]
-TILED = [(129, 130), (331, 503), (640, 256), (256, 1024), (100, 4097), (300, 1), (5000, 2)]
+TILED = [(129, 130), (256, 256), (155, 221), (331, 503), (640, 256), (256, 1024), (100, 4097), (300, 1), (5000, 2)]
 
 
 @pytest.mark.parametrize("shape", ON_CHIP, ids=str)
@@ -170,7 +170,7 @@ def test_in_place_and_mixed_sets():
 
 
 def test_more_views_and_groups_than_a_launch_takes():
-    shapes = [(130 + 2 * (i % 9), 200) for i in range(110)] + [(16, 40 + i % 2) for i in range(150)]
+    shapes = [(130 + 2 * (i % 9), 300) for i in range(110)] + [(16, 40 + i % 2) for i in range(150)]
     op = MuonStep(shapes, mode="half")
     X = [random(s, torch.bfloat16, i) for i, s in enumerate(shapes)]
     Os = [torch.empty_like(x) for x in X]
