@@ -91,8 +91,8 @@ typedef enum { MUON_BF16 = 0, MUON_FP32 = 1, MUON_FP16 = 2 } muon_dtype_t;
  *           whose singular values stay below 4 are in range (the usual ones stay below 1.3);
  *           beyond that a matrix comes out not finite.  X is normalised before it
  *           is rounded, so the inputs' size does not matter down to norms of about 1e-4 eps.
- *           Matrices of at most 128 rows (or columns) and 4096 columns (rows) run every
- *           iteration on chip.  Takes views, coefficients per iteration and 8-bit
+ *           Matrices of at most 128 rows (or columns) and 4096 columns (rows), or of fewer
+ *           rows and as many times more columns, run every iteration on chip.  Takes views, coefficients per iteration and 8-bit
  *           momentum (below). */
 typedef enum { MUON_MODE_FAST = 0, MUON_MODE_FP32_REF = 1, MUON_MODE_HALF = 2 } muon_mode_t;
 

@@ -9,9 +9,10 @@
 // for the whole iteration, and the matrix is read from and written to global memory in the
 // caller's own layout, once each (fp32 sources twice: the second read is an L2 hit).
 //
-// Several small matrices share a tile: a matrix takes h rows, h the power of two >= m (8 at least), and
-// up to 128 / h of them make the tile's X a stack whose A is masked to its h x h diagonal blocks.
-// B' is then block diagonal and B' X the stack of the updates.  A matrix that is not finite would reach
+// A matrix of h rows, h the power of two >= m (8 at least), fills the 128 rows as F column ranges below
+// each other (a 64 x 768 matrix is 128 x 384): the Gram product's h x h diagonal blocks then add up to its A,
+// and the update multiplies each range by the same B', a block diagonal of F copies.  And several
+// matrices share a tile in the same way, each with diagonal blocks of its own.  A matrix that is not finite would reach
 // its neighbours through 0 x NaN, so its rows are taken out of the tile (and its output is NaN) as
 // soon as its norm or a diagonal entry of its A says so.
 //
@@ -102,6 +103,17 @@ __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+__device__ __forceinline__ float4 ld_shared_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, %0;" ::"n"(EPI) : "memory"); }
 
 // 8 x 8 transposition of 16-bit values: q[k] holds eight values of row k, then of column k.
@@ -191,9 +203,10 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile = static_cast<int>(blockIdx.x) / C;
   const int lh = __ffs(p.slot_rows) - 1;         // log2 of the rows of a matrix in the tile
-  const int used = p.slots << lh;                // rows of the tile in use
+  const int lf = __ffs(p.folds) - 1;             // log2 of the column ranges a matrix is cut into
+  const int ls = lh + lf;                        // log2 of the tile's rows that hold a matrix
+  const int used = p.slots << ls;                // rows of the tile in use
   const int used16 = (used + 15) & ~15;
-  const int col0 = rank * p.width;               // this CTA's first column
   const int first_mat = tile * p.slots;
   const int nblk = (p.width + 127) / 128;
   const uint64_t tmo = p.timeout_ns;
@@ -245,7 +258,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   const int groups = p.width / 8;                // a multiple of 8
   const int ig = (tid >> 3) & 15;                // rows 8 ig .. 8 ig + 7
   const int i0 = (ig * 8) & (p.slot_rows - 1);   // the first of them, within the matrix
-  const int slot_l = (ig * 8) >> lh;
+  const int slot_l = (ig * 8) >> ls;             // the matrix of the tile
+  const int col0 = ((((ig * 8) >> lh) & (p.folds - 1)) * C + rank) * p.width;  // first column of those rows
   int seg = 0, e = -1;                           // view of those rows, and matrix within it (-1: none)
   if (ig * 8 < used && first_mat + slot_l < p.total && i0 < p.m) {
     while (seg + 1 < p.nseg && p.seg[seg + 1].mat_begin <= first_mat + slot_l) ++seg;
@@ -355,10 +369,10 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     total[tid] = t;
   }
   __syncthreads();
-  if (tid < 128 && (tid & (p.slot_rows - 1)) == 0 && tid < used) {  // one thread a matrix
-    const int slot = tid >> lh;
+  if (tid < 128 && (tid & ((1 << ls) - 1)) == 0 && tid < used) {  // one thread a matrix
+    const int slot = tid >> ls;
     float t = 0.0f;
-    for (int i = 0; i * 8 < p.slot_rows; ++i) t += total[(tid >> 3) + i];
+    for (int i = 0; i < (1 << ls) / 8; ++i) t += total[(tid >> 3) + i];
     const float norm = sqrtf(t);
     if (!isfinite(norm)) poison[slot] = 1;
     factor[slot] = p.normalised ? 1.0f : normaliser(norm, p.eps);
@@ -507,13 +521,13 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
     const int r = quad * 32 + lane;                       // this thread's row of the tile
     const int ca0 = part4 * 32;                           // its columns of A, and of a block of the update
     const bool active = quad * 32 < used;                 // rows that hold a matrix (warp-uniform)
-    const int slot = r < used ? r >> lh : -1;             // -1: no matrix, the row stays 0
+    const int slot = r < used ? r >> ls : -1;             // its matrix (-1: none, the row stays 0)
     const uint32_t t_row = tmem + (static_cast<uint32_t>(quad * 32) << 16);
     uint32_t uses = 0;                                    // parity of upd_full
-    uint32_t own = 0;                                     // columns ca0 + i of the row's own matrix, a bit each
-    for (int i = 0; i < 32; ++i) own |= static_cast<uint32_t>(((ca0 + i) >> lh) == slot) << i;
+    uint32_t own = 0;                                     // columns ca0 + i of the row's own block, a bit each
+    for (int i = 0; i < 32; ++i) own |= static_cast<uint32_t>(((ca0 + i) >> lh) == (r < used ? r >> lh : -1)) << i;
     constexpr float kGram = kHalfA / (kHalfX * kHalfX);
-    // keep the row's own matrix; of 32 rows and more, rows are all in or all out
+    // keep the row's own block; of 32 rows and more, rows are all in or all out
     auto masked = [&](float (&v)[32]) {
       if (own == 0xffffffffu) return;
 #pragma unroll
@@ -536,6 +550,41 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
       {
         float v[32];
         if (ok && (active || C > 1)) tmem_ld_32cols(t_row + T_A + ca0, v);
+        if (p.folds > 1) {
+          // The matrix's A is the sum of its column ranges' blocks: through the place of A, fp32, each row
+          // its h columns in groups of four.  Of h >= 32 a warp's 32 columns are all its rows' own or none.
+          const int lq = lh - 2, q0 = (ca0 & (p.slot_rows - 1)) >> 2, swz = r & min(7, (1 << lq) - 1);
+          const uint32_t mine = aaddr + (r << lq) * 16;                      // this row
+          const uint32_t first = aaddr + ((((r >> ls) << ls) + (r & (p.slot_rows - 1))) << lq) * 16;  // in the first block
+          const uint32_t step = (p.slot_rows << lq) * 16;                    // to the next block
+          const bool all = own == 0xffffffffu;
+          if (ok && own != 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (all || ((own >> (4 * i)) & 1u))
+                st_shared_v4(mine + ((lh >= 5 ? q0 + i : i & ((1 << lq) - 1)) ^ swz) * 16, v[4 * i], v[4 * i + 1], v[4 * i + 2],
+                             v[4 * i + 3]);
+            }
+          }
+          epi_sync();
+          if (ok && own != 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+#pragma unroll 1
+            for (int f = 0; f < p.folds; ++f) {
+              const uint32_t from = first + f * step;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (all || ((own >> (4 * i)) & 1u)) {
+                  const float4 t = ld_shared_v4(from + ((lh >= 5 ? q0 + i : i & ((1 << lq) - 1)) ^ swz) * 16);
+                  v[4 * i] += t.x; v[4 * i + 1] += t.y; v[4 * i + 2] += t.z; v[4 * i + 3] += t.w;
+                }
+              }
+            }
+          }
+          epi_sync();
+          if (C == 2 && tid == 0 && ok) mbar_arrive_remote(map_to_rank(peer_free, rank ^ 1));  // the place is free
+        }
         if (C > 1) {
           // Each CTA sends every owner its share of the owner's rows; the owner adds its own and the
           // others' in a fixed order, rounds once, and copies its rows of A to the others.
@@ -544,7 +593,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
             mbar_arrive_expect_tx(rows_full, (C - 1) * rows_c * 256);
           }
           __syncwarp();
-          if (C == 2 && it > 0) wait_on(peer_free, par ^ 1);
+          if (C == 2 && p.folds > 1) wait_on(peer_free, par);
+          else if (C == 2 && it > 0) wait_on(peer_free, par ^ 1);
           if (ok && owner != rank) {
             const uint32_t bar = map_to_rank(share_full, owner);
             const uint32_t to = map_to_rank(share_base + share_at(rank, ca0 >> 2), owner);
@@ -614,7 +664,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
       wait_on(aa_full, par);
       if (C > 1) wait_on(peer_got, par);  // the rows of A that this CTA copied have been read
       epi_sync();
-      if (C == 2 && tid == 0 && ok) mbar_arrive_remote(map_to_rank(peer_free, rank ^ 1));  // A has been read
+      if (C == 2 && p.folds == 1 && tid == 0 && ok)
+        mbar_arrive_remote(map_to_rank(peer_free, rank ^ 1));  // A has been read
       if (ok && active) {
         const bool out = slot >= 0 && poison[slot] != 0;
         float v[32];

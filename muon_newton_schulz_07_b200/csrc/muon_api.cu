@@ -72,7 +72,7 @@ void make_plan(const muon_shape_t* shapes, int n, muon_mode_t mode, Plan* P) {
       gp.mp = round_up(m, kPad);
       gp.np = round_up(nn, kPad);
       gp.cnt = 0;
-      gp.skinny = mode == MUON_MODE_HALF && m <= kSkinnyRows && nn <= kSkinnyCluster * kSkinnyColsPart;
+      gp.skinny = mode == MUON_MODE_HALF && skinny_fits(m, nn);
       P->groups.push_back(gp);
     } else {
       g = it->second;

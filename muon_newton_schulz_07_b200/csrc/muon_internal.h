@@ -299,6 +299,15 @@ constexpr int kSkinnyRows = 128;       // most rows (of the oriented matrix)
 constexpr int kSkinnyColsOne = 768;    // most columns of one CTA, or of each of two
 constexpr int kSkinnyColsPart = 512;   // most columns of each CTA of a larger cluster
 constexpr int kSkinnyCluster = 8;      // most CTAs of a cluster
+inline int skinny_block(int m) {       // rows of a block
+  int h = 8;
+  while (h < m) h *= 2;
+  return h;
+}
+// Whether matrices of m rows and n columns (m <= n) fit.
+inline bool skinny_fits(long long m, long long n) {
+  return m <= kSkinnyRows && n <= static_cast<long long>(kSkinnyRows / skinny_block(static_cast<int>(m))) * kSkinnyCluster * kSkinnyColsPart;
+}
 constexpr int kSkinnySegs = 64;
 constexpr int kMaxSteps = 64;
 
@@ -307,10 +316,11 @@ struct SkinnyParams {
   int nseg;
   int total;                 // matrices
   int m, n;
-  int slot_rows;             // rows of the tile each matrix takes: a power of two >= m, 8 at least
-  int slots;                 // matrices in a tile
+  int slot_rows;             // rows of a block of the tile: a power of two >= m, 8 at least
+  int folds;                 // blocks below each other that hold a matrix, each a range of its columns
+  int slots;                 // matrices in a tile; slots * folds * slot_rows <= 128
   int cluster;               // CTAs of a tile
-  int width;                 // columns each CTA holds, a multiple of 64
+  int width;                 // columns of a block that each CTA holds, a multiple of 64
   int normalised;            // the source is 2^12 X already: no norm is taken
   int k;
   float coef[kMaxSteps][3];  // (a, b, c) of each iteration

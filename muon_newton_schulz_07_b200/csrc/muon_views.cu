@@ -391,19 +391,39 @@ cudaError_t enqueue_tiles(muon_ctx* h, const std::vector<Item>& items, const muo
   return cudaSuccess;
 }
 
-// How a group of `cnt` m x n matrices is laid over clusters.
+// How `cnt` m x n matrices are laid over tiles and clusters: how many share a tile, into how many column
+// ranges of at least 64 each is cut, and the fewest CTAs that hold them, by what the waves of tiles would take.
+// Measured, an iteration of a tile takes about 7 k cycles for the A -> B' chain, 6 k more to add up
+// the A of a cluster, 2.7 k more to add up column ranges, and 1.6 k for each 128 columns (1.15 k in the
+// update, the rest its share of loading and storing the tile): 12 of 64 x 768 take 45 us in two ranges and
+// 47 in one, 9 of 25 x 626 51 us in four and 83 in one.
 void skinny_layout(const GroupPlan& gp, int cnt, int num_sms, SkinnyParams* p) {
   p->m = gp.m;
   p->n = gp.n;
-  p->slot_rows = 8;
-  while (p->slot_rows < gp.m) p->slot_rows *= 2;
+  p->slot_rows = skinny_block(gp.m);
   const int most = kSkinnyRows / p->slot_rows;
-  p->cluster = 1;
-  while (gp.n > p->cluster * (p->cluster <= 2 ? kSkinnyColsOne : kSkinnyColsPart)) p->cluster *= 2;
-  // one matrix a tile while there are SMs for it, then as many as fit
-  const int room = std::max(1, num_sms / p->cluster);
-  p->slots = std::min(most, (cnt + room - 1) / room);
-  p->width = ((gp.n + p->cluster - 1) / p->cluster + 63) / 64 * 64;
+  double best = -1.0;
+  for (int slots = 1; slots <= most; slots *= 2) {
+    for (int folds = 1; folds <= most / slots && (folds == 1 || (gp.n + folds - 1) / folds >= 64); folds *= 2) {
+      int cluster = 1;
+      while (cluster <= kSkinnyCluster &&
+             gp.n > static_cast<long long>(folds) * cluster * (cluster <= 2 ? kSkinnyColsOne : kSkinnyColsPart))
+        cluster *= 2;
+      if (cluster > kSkinnyCluster) continue;
+      const int width = ((gp.n + folds * cluster - 1) / (folds * cluster) + 63) / 64 * 64;
+      const long long ctas = (static_cast<long long>(cnt) + slots - 1) / slots * cluster;
+      const double waves = static_cast<double>((ctas + num_sms - 1) / num_sms);
+      const double cost =
+          waves * (7.0 + (cluster > 1 ? 6.0 : 0.0) + (folds > 1 ? 2.7 : 0.0) + 1.6 * ((width + 127) / 128));
+      if (best < 0.0 || cost < best) {
+        best = cost;
+        p->slots = slots;
+        p->folds = folds;
+        p->cluster = cluster;
+        p->width = width;
+      }
+    }
+  }
 }
 
 cudaError_t enqueue_skinny(muon_ctx* h, const std::vector<Item>& items, const muon_hparams_t* hp, bool store,

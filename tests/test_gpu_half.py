@@ -73,7 +73,8 @@ def check(shapes, X, Os, abc, op, what=""):
 
 
 ON_CHIP = [(1, 1), (1, 7), (7, 1), (5, 3), (8, 64), (64, 768), (128, 128), (100, 333), (333, 100), (17, 769), (128, 1024),
-           (31, 2000), (4096, 128), (3, 4096), (128, 700)]
+           (31, 2000), (4096, 128), (3, 4096), (128, 700), (2, 1441), (60, 8000), (25, 626), (16, 20001), (64, 1600),
+           (33, 4000), (5, 60001)]
 TILED = [(129, 130), (256, 256), (155, 221), (331, 503), (640, 256), (256, 1024), (100, 4097), (300, 1), (5000, 2)]
 
 
@@ -88,7 +89,7 @@ def test_one_matrix_on_chip(shape, kind):
 
 
 @pytest.mark.parametrize("stack", [(2, 64, 64), (12, 64, 768), (300, 20, 70), (37, 128, 256), (700, 1, 9), (200, 3, 500),
-                                   (60, 1536, 128), (5, 33, 3000), (320, 64, 128)], ids=str)
+                                   (60, 1536, 128), (5, 33, 3000), (320, 64, 128), (9, 25, 626), (32, 11, 993), (50, 4000, 16), (200, 64, 768)], ids=str)
 def test_stacks_on_chip(stack):
     op = MuonStep([stack], mode="half")
     X, Os = [random(stack, torch.bfloat16, 2)], [torch.empty(stack, dtype=torch.bfloat16, device="cuda")]
