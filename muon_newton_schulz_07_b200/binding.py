@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmuon.so")
 
@@ -58,14 +59,9 @@ class HParams(ctypes.Structure):
     ]
 
 
-class View(ctypes.Structure):
-    _fields_ = [("data", ctypes.c_void_p), ("count", ctypes.c_int64), ("batch_stride", ctypes.c_int64),
-                ("row_stride", ctypes.c_int64), ("col_stride", ctypes.c_int64), ("dtype", ctypes.c_int)]
-
-
-class State(ctypes.Structure):
-    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("count", ctypes.c_int64),
-                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+# Packed rather than ctypes structures: a call on a small matrix is bounded by what the host does for it.
+_View = struct.Struct("Pqqqqi4x")   # muon_view_t: data, count, batch_stride, row_stride, col_stride, dtype
+_State = struct.Struct("PPqqq")     # muon_state_t: codes, scales, count, rows, cols
 
 
 _lib = None
@@ -115,7 +111,7 @@ def lib() -> ctypes.CDLL:
         L.muon_profile_end.restype = st
         L.muon_set_schedule.argtypes = [_VP, ctypes.c_int]
         L.muon_set_schedule.restype = st
-        views, states, hpp = _VP, _VP, ctypes.POINTER(HParams)  # arrays of View and State (see views, states)
+        views, states, hpp = _VP, _VP, ctypes.POINTER(HParams)  # what views() and states() pack
         seed = ctypes.POINTER(ctypes.c_uint32)
         L.muon_set_coefficients.argtypes = [_VP, ctypes.POINTER(ctypes.c_float), ctypes.c_int]
         L.muon_set_coefficients.restype = st
@@ -269,13 +265,13 @@ def _seed(seed):
 
 
 def views(items):
-    """Array of View from (data, count, batch_stride, row_stride, col_stride, dtype) tuples."""
-    return (View * max(len(items), 1))(*items)
+    """muon_view_t array of (data, count, batch_stride, row_stride, col_stride, dtype) tuples."""
+    return b"".join([_View.pack(v[0] or 0, *v[1:]) for v in items])
 
 
 def states(items):
-    """Array of State from (codes, scales, count, rows, cols) tuples."""
-    return (State * max(len(items), 1))(*items)
+    """muon_state_t array of (codes, scales, count, rows, cols) tuples."""
+    return b"".join([_State.pack(s[0] or 0, s[1] or 0, *s[2:]) for s in items])
 
 
 def muon_set_coefficients(handle: int, abc) -> None:
@@ -286,25 +282,25 @@ def muon_set_coefficients(handle: int, abc) -> None:
 
 
 def muon_orthogonalize_views(handle: int, X, O, n: int, hp: HParams, stream: int) -> None:
-    _check(lib().muon_orthogonalize_views(handle, X, O, n, ctypes.byref(hp), ctypes.c_void_p(stream)),
+    _check(lib().muon_orthogonalize_views(handle, X, O, n, ctypes.byref(hp), stream),
            "muon_orthogonalize_views")
 
 
 def muon_state_quantize(X, S, n: int, fmt: int, seed, stream: int) -> None:
-    _check(lib().muon_state_quantize(X, S, n, fmt, _seed(seed), ctypes.c_void_p(stream)), "muon_state_quantize")
+    _check(lib().muon_state_quantize(X, S, n, fmt, _seed(seed), stream), "muon_state_quantize")
 
 
 def muon_state_dequantize(S, X, n: int, fmt: int, stream: int) -> None:
-    _check(lib().muon_state_dequantize(S, X, n, fmt, ctypes.c_void_p(stream)), "muon_state_dequantize")
+    _check(lib().muon_state_dequantize(S, X, n, fmt, stream), "muon_state_dequantize")
 
 
 def muon_momentum_state(handle: int, G, S, U, n: int, fmt: int, hp: HParams, seed, stream: int) -> None:
-    _check(lib().muon_momentum_state(handle, G, S, U, n, fmt, ctypes.byref(hp), _seed(seed), ctypes.c_void_p(stream)),
+    _check(lib().muon_momentum_state(handle, G, S, U, n, fmt, ctypes.byref(hp), _seed(seed), stream),
            "muon_momentum_state")
 
 
 def muon_step_state(handle: int, W, G, S, n: int, fmt: int, hp: HParams, seed, stream: int) -> None:
-    _check(lib().muon_step_state(handle, W, G, S, n, fmt, ctypes.byref(hp), _seed(seed), ctypes.c_void_p(stream)),
+    _check(lib().muon_step_state(handle, W, G, S, n, fmt, ctypes.byref(hp), _seed(seed), stream),
            "muon_step_state")
 
 
@@ -321,5 +317,5 @@ def muon_adamw_step(P, G, M, V, numel, dtype: int, hp: AdamWHParams, stream: int
     f.restype = ctypes.c_int
     n = len(numel)
     sizes = (ctypes.c_int64 * max(n, 1))(*[int(x) for x in numel])
-    _check(f(_ptrs(P), _ptrs(G), _ptrs(M), _ptrs(V), sizes, n, dtype, ctypes.byref(hp), ctypes.c_void_p(stream)),
+    _check(f(_ptrs(P), _ptrs(G), _ptrs(M), _ptrs(V), sizes, n, dtype, ctypes.byref(hp), stream),
            "muon_adamw_step")

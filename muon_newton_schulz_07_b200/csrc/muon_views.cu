@@ -584,7 +584,7 @@ muon_status_t convert(const muon_view_t* X, const muon_state_t* S, int n, muon_s
     mats += S[j].count;
     if (mats > 0x7fffffffll) return MUON_ERR_UNSUPPORTED;
   }
-  static thread_local StateParams p;  // ~16 KB: kept off the stack
+  static thread_local StateParams p;  // 4 KB that need no clearing
   int j = 0, mat = 0;
   while (j < n) {
     p.nseg = 0;

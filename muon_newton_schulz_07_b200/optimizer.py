@@ -39,15 +39,26 @@ def _views(tensors, entries, device, name, dtype=None, by_rows=False):
             raise ValueError(f"{name}: tensor {tuple(t.shape)} {t.dtype} {t.device} does not match {shape} "
                              f"{dtype or 'bf16, fp16 or fp32'} {device}")
         st = t.stride()
-        if st[-1] != 1 and cols != 1 and (by_rows or not (st[-2] == 1 or rows == 1)):
+        bs, rs, cs = st if len(st) == 3 else (0,) + st
+        if cs != 1 and cols != 1 and (by_rows or not (rs == 1 or rows == 1)):
             raise ValueError(f"{name}: a tensor of strides {st} is not stored by rows"
                              + ("" if by_rows else " or by columns"))
-        out.append((t.data_ptr(), count, st[0] if len(st) == 3 else 0, st[-2], st[-1], _VIEW_TYPES[dt]))
+        out.append((t.data_ptr(), count, bs, rs, cs, _VIEW_TYPES[dt]))
     return B.views(out)
 
 
+def _device(device):
+    dev = torch.device(device if device is not None else "cuda")
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    return dev
+
+
 def _stream(device, stream):
-    return (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream(device).cuda_stream, without a Stream object (2 us of a call's 10 on the host)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 class QuantizedState:
@@ -74,30 +85,27 @@ class QuantizedState:
         self._fmt, code = self.FORMATS[fmt]
         self._entries = _entries(shapes)
         self.shapes = [e[3] for e in self._entries]
-        dev = torch.device(device if device is not None else "cuda")
-        if dev.type == "cuda" and dev.index is None:
-            dev = torch.device("cuda", torch.cuda.current_device())
-        self.device = dev
+        self._scale_shapes = [s[:-1] + (-(-s[-1] // self.BLOCK),) for s in self.shapes]
+        self.device = dev = _device(device)
         self.codes = [torch.zeros(s, dtype=torch.uint8, device=dev).view(code) for s in self.shapes]
-        self.scales = [torch.zeros(s[:-1] + (-(-s[-1] // self.BLOCK),), dtype=torch.float32, device=dev)
-                       for s in self.shapes]
+        self.scales = [torch.zeros(s, dtype=torch.float32, device=dev) for s in self._scale_shapes]
 
     def _states(self):
         out = []
-        code = self.FORMATS[self.fmt][1]
-        for q, s, (count, rows, cols, shape) in zip(self.codes, self.scales, self._entries):
-            if q.shape != shape or q.dtype is not code or q.device != self.device or not q.is_contiguous():
+        code, device = self.FORMATS[self.fmt][1], self.device
+        for q, s, (count, rows, cols, shape), scales in zip(self.codes, self.scales, self._entries, self._scale_shapes,
+                                                             strict=True):
+            if q.shape != shape or q.dtype is not code or q.device != device or not q.is_contiguous():
                 raise ValueError(f"codes: tensor {tuple(q.shape)} {q.dtype} {q.device} does not match {shape} {code} "
                                  f"{self.device} (contiguous)")
-            if (s.shape[:-1] != shape[:-1] or s.shape[-1] != -(-cols // self.BLOCK) or s.dtype is not torch.float32
-                    or s.device != self.device or not s.is_contiguous()):
+            if s.shape != scales or s.dtype is not torch.float32 or s.device != device or not s.is_contiguous():
                 raise ValueError(f"scales: tensor {tuple(s.shape)} {s.dtype} {s.device} does not match {shape}, a scale "
                                  f"for {self.BLOCK} columns, torch.float32 {self.device} (contiguous)")
             out.append((q.data_ptr(), s.data_ptr(), count, rows, cols))
         return B.states(out)
 
     def _side(self, tensors, name):
-        if tensors and any(t.dtype != tensors[0].dtype for t in tensors):
+        if len(tensors) > 1 and any(t.dtype is not tensors[0].dtype for t in tensors):
             raise ValueError(f"{name}: tensors of one call have one dtype")
         return _views(tensors, self._entries, self.device, name, by_rows=True)
 
@@ -140,7 +148,7 @@ class MuonStep:
         matrices = [(rows, cols) for count, rows, cols, _ in self._entries for _ in range(count)]
         self.mode = mode
         self.dtype = dtype
-        self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        self.device = _device(device)
         self._dt = B.MUON_BF16 if dtype == torch.bfloat16 else B.MUON_FP32
         self._mode = {"fast": B.MUON_MODE_FAST, "half": B.MUON_MODE_HALF, "fp32_ref": B.MUON_MODE_FP32_REF}[mode]
         nbytes = B.muon_workspace_size(matrices, self._dt, self._mode)
@@ -207,15 +215,15 @@ class MuonStep:
             raise ValueError("seed is for a QuantizedState")
         if quantized and self.mode != "half":
             raise ValueError("a QuantizedState needs mode='half'")
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
         if quantized:
             states = self._momentum_state(M)
             w = _views(W, self._entries, self.device, "W", self.dtype)
             g = _views(G, self._entries, self.device, "G", self.dtype, by_rows=True)
             abc, ns_steps = self._coefficients(abc, ns_steps)
             hp = B.make_hparams(lr, beta, weight_decay, eps, abc, nesterov, ns_steps)
-            B.muon_step_state(self.handle, w, g, states, len(self.shapes), M._fmt, hp, seed, s.cuda_stream)
+            B.muon_step_state(self.handle, w, g, states, len(self.shapes), M._fmt, hp, seed, _stream(self.device, stream))
             return
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
         abc, ns_steps = self._coefficients(abc, ns_steps)
         hp = B.make_hparams(lr, beta, weight_decay, eps, abc, nesterov, ns_steps)
         B.muon_step(self.handle, self._check(W, "W"), self._check(G, "G"), self._check(M, "M"), hp, s.cuda_stream)
@@ -276,14 +284,14 @@ class MuonStep:
         In mode "half" X and O may be views stored by rows or by columns (slices, stacks, transposed tensors) of
         bf16, fp16 or fp32, O may be X itself, and abc may be a list with one coefficient triple per iteration.
         """
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
         if self.mode == "half":
             x = _views(X, self._entries, self.device, "X")
             o = _views(O, self._entries, self.device, "O")
             abc, ns_steps = self._coefficients(abc, ns_steps)
             hp = B.make_hparams(0.0, 0.0, 0.0, eps, abc, False, ns_steps)
-            B.muon_orthogonalize_views(self.handle, x, o, len(self.shapes), hp, s.cuda_stream)
+            B.muon_orthogonalize_views(self.handle, x, o, len(self.shapes), hp, _stream(self.device, stream))
             return
+        s = stream if stream is not None else torch.cuda.current_stream(self.device)
         abc, ns_steps = self._coefficients(abc, ns_steps)
         hp = B.make_hparams(0.0, 0.0, 0.0, eps, abc, False, ns_steps)
         B.muon_orthogonalize(self.handle, self._check(X, "X"), self._check(O, "O"), hp, s.cuda_stream)
@@ -296,8 +304,7 @@ class MuonStep:
             else:  # memory of the stream that writes it
                 with torch.cuda.stream(stream):
                     out = torch.empty(self._n, dtype=torch.float32, device=self.device)
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
-        B.muon_get_norms(self.handle, out.data_ptr(), s.cuda_stream)
+        B.muon_get_norms(self.handle, out.data_ptr(), _stream(self.device, stream))
         return out
 
     def status(self, stream=None) -> int:
