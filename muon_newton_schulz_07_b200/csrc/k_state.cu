@@ -19,8 +19,8 @@
 // for the momentum).  A unit is one block of one row, 16 lanes of 8 values; consecutive units are
 // consecutive in memory, so a CTA of 64 units streams up to 8192 contiguous values whatever the
 // row length, and a thread has the loads of all four of its units in flight before it computes.
-// Rows that are not a multiple of 8 long (or not aligned) interleave the 16 lanes instead, one
-// value each, which keeps the accesses of a half-warp contiguous.
+// Rows that are not whole blocks back to back interleave the 16 lanes instead, four values each where
+// rows are multiples of 4 and aligned so, else one, which keeps the accesses of a half-warp contiguous.
 #include <cuda_fp8.h>
 
 #include "muon_view.cuh"
@@ -225,8 +225,10 @@ struct Sites {
     return static_cast<T*>(s.out) + value_at(q, s.out_ld, s.out_bs);
   }
 };
-// Value i of a lane sits at this place of the unit: eight neighbours, or interleaved lanes.
-__device__ __forceinline__ int place(bool vec, int lane, int i) { return vec ? lane * 8 + i : lane + LANES * i; }
+// Value i of a lane sits at this place of the unit: eight neighbours (LINEAR), two runs of four (vec), or
+// single values.
+__device__ __forceinline__ int run(int lane, int h) { return (lane + LANES * h) * 4; }
+__device__ __forceinline__ int single(int lane, int i) { return lane + LANES * i; }
 
 // Eight values of a stored row as they come from memory (widened only when they are used, so that
 // the loads of several units can be in flight).
@@ -240,6 +242,10 @@ struct Eight<float> {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
   }
+  __device__ __forceinline__ void load4(int h, const float* p) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
+    v[4 * h] = a.x; v[4 * h + 1] = a.y; v[4 * h + 2] = a.z; v[4 * h + 3] = a.w;
+  }
   __device__ __forceinline__ void set(int i, const float* p) { v[i] = __ldcs(p); }
   __device__ __forceinline__ void widen(float (&x)[8]) const {
 #pragma unroll
@@ -252,6 +258,10 @@ struct Eight16 {
   __device__ __forceinline__ void load(const T* p) {
     const uint4 q = __ldcs(reinterpret_cast<const uint4*>(p));
     w[0] = q.x; w[1] = q.y; w[2] = q.z; w[3] = q.w;
+  }
+  __device__ __forceinline__ void load4(int h, const T* p) {
+    const uint2 q = __ldcs(reinterpret_cast<const uint2*>(p));
+    w[2 * h] = q.x; w[2 * h + 1] = q.y;
   }
   __device__ __forceinline__ void set(int i, const T* p) {
     const uint32_t b = __ldcs(reinterpret_cast<const unsigned short*>(p));
@@ -289,11 +299,13 @@ __device__ __forceinline__ void load_values(const T* base, bool vec, int have, E
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(x) / 4); ++i) reinterpret_cast<uint32_t*>(&x)[i] = 0;
   if (vec) {
-    if (lane * 8 < have) x.load(base + lane * 8);  // rows are multiples of 8: all or nothing
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (run(lane, h) < have) x.load4(h, base + run(lane, h));  // rows are multiples of 4: all or nothing
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = place(false, lane, i);
+      const int at = single(lane, i);
       if (at < have) x.set(i, base + at);
     }
   }
@@ -302,12 +314,26 @@ __device__ __forceinline__ void load_values(const T* base, bool vec, int have, E
 template <bool LINEAR, typename T>
 __device__ __forceinline__ void store_values(T* base, bool vec, int have, const float (&x)[8]) {
   const int lane = unit_lane();
-  if (LINEAR || vec) {
+  if (LINEAR) {
     if (lane * 8 < have) store_eight(base, TypeOf<T>::id, lane * 8, 8, true, x);
+  } else if (vec) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float* v = x + 4 * h;
+      if (run(lane, h) >= have) continue;
+      if (TypeOf<T>::id == kViewF32) {
+        *reinterpret_cast<float4*>(base + run(lane, h)) = make_float4(v[0], v[1], v[2], v[3]);
+      } else {
+        alignas(8) T q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store_one(q, TypeOf<T>::id, i, v[i]);
+        *reinterpret_cast<uint2*>(base + run(lane, h)) = *reinterpret_cast<const uint2*>(q);
+      }
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = place(false, lane, i);
+      const int at = single(lane, i);
       if (at < have) store_one(base, TypeOf<T>::id, at, x[i]);
     }
   }
@@ -353,14 +379,21 @@ __device__ __forceinline__ void write_units(const Sites<LINEAR>& at, bool vec, u
     uint32_t r[4] = {0, 0, 0, 0};
     if (STOCHASTIC) {
       const unsigned long long first = at.place_of(q);
-      if (LINEAR || vec) {  // eight neighbours from an even place: four pairs
+      if (LINEAR) {  // eight neighbours from an even place: four pairs
         const uint32_t counter = pair_counter(key, (first + lane * 8) / 2);  // (a multiple of 4: no carry below)
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] = mixed(counter + i);
+      } else if (vec) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t counter = pair_counter(key, (first + run(lane, h)) / 2);  // (even)
+          r[2 * h] = mixed(counter);
+          r[2 * h + 1] = mixed(counter + 1);
+        }
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const unsigned long long here = first + place(false, lane, i);
+          const unsigned long long here = first + single(lane, i);
           const uint32_t h = mixed(pair_counter(key, here >> 1)) >> (16 * (here & 1)) & 0xFFFFu;
           r[i >> 1] |= h << (16 * (i & 1));
         }
@@ -368,12 +401,15 @@ __device__ __forceinline__ void write_units(const Sites<LINEAR>& at, bool vec, u
     }
     const uint32_t r0[2] = {r[0], r[1]}, r1[2] = {r[2], r[3]};
     const uint32_t lo = encode4<F, STOCHASTIC>(x[q], r0), hi = encode4<F, STOCHASTIC>(x[q] + 4, r1);
-    if (LINEAR || vec) {
+    if (LINEAR) {
       if (lane * 8 < have) __stcs(reinterpret_cast<uint2*>(codes + lane * 8), make_uint2(lo, hi));
+    } else if (vec) {
+      if (run(lane, 0) < have) __stcs(reinterpret_cast<uint32_t*>(codes + run(lane, 0)), lo);
+      if (run(lane, 1) < have) __stcs(reinterpret_cast<uint32_t*>(codes + run(lane, 1)), hi);
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int to = place(false, lane, i);
+        const int to = single(lane, i);
         if (to < have) codes[to] = static_cast<uint8_t>((i < 4 ? lo : hi) >> (8 * (i & 3)));
       }
     }
@@ -391,16 +427,18 @@ __device__ __forceinline__ void load_codes(const Sites<LINEAR>& at, int q, bool 
   const uint8_t* p = static_cast<const uint8_t*>(at.s.codes) + at.code_at(q);
   c.w[0] = c.w[1] = 0;
   c.scale = LINEAR || have > 0 ? at.s.scales[at.scale_at(q)] : 0.0f;
-  if (LINEAR || vec) {
-    if (LINEAR || lane * 8 < have) {
-      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p + lane * 8));
-      c.w[0] = v.x;
-      c.w[1] = v.y;
-    }
+  if (LINEAR) {
+    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p + lane * 8));
+    c.w[0] = v.x;
+    c.w[1] = v.y;
+  } else if (vec) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (run(lane, h) < have) c.w[h] = __ldcs(reinterpret_cast<const uint32_t*>(p + run(lane, h)));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int to = place(false, lane, i);
+      const int to = single(lane, i);
       if (to < have) c.w[i >> 2] |= static_cast<uint32_t>(p[to]) << (8 * (i & 3));
     }
   }

@@ -344,7 +344,7 @@ struct StateSeg {
   float* scales;
   long long in_ld, in_bs, out_ld, out_bs;
   int in_type, out_type;
-  int vec;               // every row of every side is aligned for vector accesses
+  int vec;               // every row of every side is a multiple of 4 long and aligned to 4 values
   int linear;            // and whole blocks, the matrices and their rows back to back on every side
   int rows, cols, blocks;
   int count;

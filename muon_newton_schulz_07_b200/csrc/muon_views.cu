@@ -528,10 +528,11 @@ muon_status_t make_rows(const muon_view_t& v, const muon_state_t& s, bool output
     const bool b = (s.count == 1 || r->bs >= s.cols) && (s.rows == 1 || r->ld >= (s.count - 1) * r->bs + s.cols);
     if (!a && !b) return MUON_ERR_INVALID_ARG;
   }
-  r->vec = (reinterpret_cast<uintptr_t>(v.data) & 15u) == 0 && s.cols % 8 == 0 &&
-           (s.rows == 1 || r->ld * es % 16 == 0) && (s.count == 1 || r->bs * es % 16 == 0);
+  r->vec = reinterpret_cast<uintptr_t>(v.data) % (4 * es) == 0 && s.cols % 4 == 0 &&
+           (s.rows == 1 || r->ld % 4 == 0) && (s.count == 1 || r->bs % 4 == 0);
   // back to back (a stack's stride may still differ: matrices are found by it)
-  r->linear = r->vec && s.cols % kStateBlock == 0 && (s.rows == 1 || r->ld == s.cols);
+  r->linear = (reinterpret_cast<uintptr_t>(v.data) & 15u) == 0 && s.cols % kStateBlock == 0 &&
+              (s.rows == 1 || r->ld == s.cols) && (s.count == 1 || r->bs * es % 16 == 0);
   return MUON_OK;
 }
 
@@ -545,8 +546,8 @@ void fill_state(const muon_state_t& s, const Rows* in, const Rows* out, int mat,
   g->count = static_cast<int>(s.count);
   g->mat_begin = mat;
   g->unit_ctas = static_cast<int>((s.rows * g->blocks + kStateUnits - 1) / kStateUnits);
-  bool vec = (reinterpret_cast<uintptr_t>(s.codes) & 7u) == 0;
-  bool linear = vec && s.cols % kStateBlock == 0;
+  bool vec = (reinterpret_cast<uintptr_t>(s.codes) & 3u) == 0;
+  bool linear = (reinterpret_cast<uintptr_t>(s.codes) & 7u) == 0 && s.cols % kStateBlock == 0;
   if (in != nullptr) {
     g->in = in->data;
     g->in_ld = in->ld;
