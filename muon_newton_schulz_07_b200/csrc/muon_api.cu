@@ -251,7 +251,7 @@ void muon::stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur
     G->tm_out = gp.ts_a;
     G->out = h->ws + gp.off_a;
     G->tiles_per_mat = T * (T + 1) / 2;  // 256 x 256 pair tiles on or above the diagonal
-    G->kblocks = gp.np / kTcBK;
+    G->kblocks = (gp.n + kTcBK - 1) / kTcBK;  // beyond them are zeros
     G->tdim = T;
     G->out_ld = gp.mp;
     G->m_real = gp.m;
@@ -265,7 +265,7 @@ void muon::stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur
     G->tm_aux = gp.ts_a;
     G->tiles_per_mat = T * (T + 1) / 2;
     G->m_real = gp.m;
-    G->kblocks = gp.mp / kTcBK;
+    G->kblocks = (gp.m + kTcBK - 1) / kTcBK;
     G->tdim = T;
     G->out_ld = gp.mp;
   } else {
@@ -276,7 +276,7 @@ void muon::stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur
     G->tm_out = gp.ts_x[nxt];
     G->out = h->ws + gp.off_x[nxt];
     G->tiles_per_mat = (gp.mp / 256) * (gp.np / tw);  // 256 x tw pair tiles
-    G->kblocks = gp.mp / kTcBK;
+    G->kblocks = (gp.m + kTcBK - 1) / kTcBK;
     G->tdim = gp.np / tw;
     G->out_ld = gp.np;
     G->m_real = gp.m;
