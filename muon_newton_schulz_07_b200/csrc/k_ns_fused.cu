@@ -439,6 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     float* st32 = reinterpret_cast<float*>(wblock);
     const int sub_r = lane >> 2, sub_c = (lane & 3) * 8;
     const int swz = (lane >> 1) & 3;  // 64-byte swizzle of this lane's staging row
+    const uint32_t lead = elect_one();  // the lane whose stores and loads a bulk wait covers
     uint32_t uses[2] = {0u, 0u};
     int next_slot = 0;
     bool ok = true;
@@ -466,7 +467,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       const bool wread = fw && p.w_decay != 0.0f && gr0 < G.m_real;
       if (fw) {
         // the fp32 staging overlays this warp's store tiles: no store of its may still read them
-        if (lane == 0) bulk_wait_read<0>();
+        if (lead) bulk_wait_read<0>();
         __syncwarp();
       }
       auto woff = [&](int gc, int rr) -> size_t {
@@ -474,7 +475,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       };
       // column (within the tile) of chunk c of half h for this warp
       auto chunk_col = [&](int h, int c) { return h * TILE + cbase + c * 32; };
-      // lane 0: the four chunks of A under half h, into the tiles their results will leave from
+      // the leading lane: the four chunks of A under half h, into the tiles their results will leave from
       auto aux_issue = [&](int h) {
         bulk_wait_read<0>();  // the tiles' last stores have been read
         ++nissued;
@@ -488,16 +489,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const unsigned int* dep;
         unsigned int target;
         bool dok = true;
-        if (lane == 0) {
+        if (lead) {
           if (dependency(p, f, &dep, &target)) dok = wait_counter_bounded(dep, target, tmo, abort_flag, p.status);
           if (dok) {
             fence_proxy_async_global();
             aux_issue(0);
           }
         }
-        ok = __shfl_sync(0xffffffffu, dok ? 1 : 0, 0) != 0;
+        ok = __all_sync(0xffffffffu, dok);
         if (!ok) break;
       }
+      // Before a half's values are turned: its chunks of A have come, or the tiles' last stores have been read.
+      auto tiles_ready = [&](int h) {
+        if (aux) {
+          if (lead && h > 0) aux_issue(h);
+          if (!mbar_wait_bounded(aux_bar(e), naux & 1u, tmo, abort_flag, p.status)) return false;
+          ++naux;
+        } else if (!fw) {
+          if (lead) bulk_wait_read<0>();
+        }
+        __syncwarp();
+        return true;
+      };
+      if (!tiles_ready(0)) break;  // (while the products are still being computed)
       uint4 pf[4];
       auto pre_load = [&](int colw, uint4 (&dst)[4]) {
         const int gc = f.col0 + colw;
@@ -596,17 +610,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           // This warp's part of the half, 32 rows x 128 columns, in two reads, then the slot handed
           // back and four chunks stored from four tiles.  Chunk by chunk, each waiting for the last one's
           // read and store, took 0.6 k cycles a tile longer, which a stage of few tiles cannot hide.
-          if (aux) {
-            if (lane == 0 && h > 0) aux_issue(h);
-            if (!mbar_wait_bounded(aux_bar(e), naux & 1u, tmo, abort_flag, p.status)) {
-              ok = false;
-              break;
-            }
-            ++naux;
-          } else {
-            if (lane == 0) bulk_wait_read<0>();  // the tiles' last stores have been read
+          if (h > 0 && !tiles_ready(h)) {
+            ok = false;
+            break;
           }
-          __syncwarp();
 #pragma unroll
           for (int cc = 0; cc < 4; cc += 2) {
             float v[64];
@@ -646,12 +653,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           }
           fence_async_smem();
           __syncwarp();
-          if (lane == 0) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              tma_store_3d(out_map, otile_u32 + c * EPI_OUT_BYTES, f.col0 + chunk_col(h, c), gr0, f.mat);
-            bulk_commit();
-          }
+          for (int c = 0; c < 4; ++c)
+            tma_store_3d_lead(lead, out_map, otile_u32 + c * EPI_OUT_BYTES, f.col0 + chunk_col(h, c), gr0, f.mat);
+          if (lead) bulk_commit();
+          __syncwarp();
         }
         if (!ok) break;
       }
@@ -666,7 +672,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       // Publish this warp's part of the tile to the stages that read it (the last round's
       // Update has no reader inside this launch).
       if (!(f.kind == kUpdate && f.last)) {
-        if (lane == 0) {
+        if (lead) {
           bulk_wait_all();             // this warp's TMA stores of the tile are complete
           fence_proxy_async_global();  // ... and ordered before the release below
           red_release_gpu_add(counter(p, 3 * f.it + f.kind, f), 1u);
@@ -675,10 +681,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       }
     }
     // every TMA store of this warp has finished (its shared memory read, its global write)
-    if (lane == 0) bulk_wait_all();
+    if (lead) bulk_wait_all();
     // after an early exit, A chunks may still be on their way into this warp's buffers: wait
     // (bounded) for them before the CTA leaves
-    if (lane == 0 && naux < nissued) (void)mbar_wait_bounded(aux_bar(e), naux & 1u, tmo, nullptr, p.status);
+    if (lead && naux < nissued) (void)mbar_wait_bounded(aux_bar(e), naux & 1u, tmo, nullptr, p.status);
     __syncwarp();
   }
 
