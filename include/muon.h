@@ -178,7 +178,8 @@ typedef struct {
  * The orthogonaliser on views (MUON_MODE_HALF): O_i = NS_k(X_i) for the matrices of the handle, in
  * order; view j covers its `count` next matrices, which must have one shape (X and O have n views of
  * equal counts, adding up to the handle's matrices).  Each view has its own storage type: bf16,
- * fp16 or fp32.  O may be X itself; otherwise an output overlaps no input and no other output.
+ * fp16 or fp32.  O_i may be X_i itself (the same view); otherwise an output overlaps no input and no
+ * other output (of what would race, equal addresses are refused with MUON_ERR_INVALID_ARG).
  * Only hp->eps, a, b, c and ns_steps are used; muon_set_coefficients overrides a, b, c.
  * Returns MUON_ERR_UNSUPPORTED for a handle of another mode and for views that
  * are stored neither by rows nor by columns.

@@ -13,6 +13,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <exception>
+#include <utility>
 #include <vector>
 
 #include "muon_ctx.h"
@@ -97,6 +99,45 @@ muon_status_t cover(const muon_ctx* h, const muon_view_t* v, int n, std::vector<
     at += static_cast<int>(v[j].count);
   }
   return at == h->n ? MUON_OK : MUON_ERR_INVALID_ARG;
+}
+
+// Outputs at one address, or at another matrix's input, would race: the same tensor twice in a list,
+// or a list given back in another order.  (Views that overlap in part are the caller's to avoid.)
+bool distinct(std::vector<const void*>& at) {
+  std::sort(at.begin(), at.end());
+  return std::adjacent_find(at.begin(), at.end()) == at.end();
+}
+bool apart(const std::vector<const void*>& in, const std::vector<const void*>& out) {
+  if (out.size() == 1) return true;
+  std::vector<std::pair<const void*, size_t>> sorted;
+  for (size_t j = 0; j < out.size(); ++j) sorted.emplace_back(out[j], j);
+  std::sort(sorted.begin(), sorted.end());
+  for (size_t j = 1; j < sorted.size(); ++j)
+    if (sorted[j].first == sorted[j - 1].first) return false;
+  for (size_t j = 0; j < in.size(); ++j) {
+    const auto it = std::lower_bound(sorted.begin(), sorted.end(), std::make_pair(in[j], size_t{0}));
+    if (it != sorted.end() && it->first == in[j] && it->second != j) return false;
+  }
+  return true;
+}
+bool states_distinct(const muon_state_t* S, int n) {
+  if (n == 1) return true;
+  std::vector<const void*> at;
+  for (int j = 0; j < n; ++j) {
+    at.push_back(S[j].codes);
+    at.push_back(S[j].scales);
+  }
+  return distinct(at);
+}
+
+// No exception leaves a C entry point: host tables that cannot be allocated are an error code.
+template <typename F>
+muon_status_t no_throw(F f) noexcept {
+  try {
+    return f();
+  } catch (const std::exception&) {
+    return MUON_ERR_INVALID_ARG;
+  }
 }
 
 // (a, b, c) of iteration t.
@@ -585,6 +626,13 @@ muon_status_t convert(const muon_view_t* X, const muon_state_t* S, int n, muon_s
     mats += S[j].count;
     if (mats > 0x7fffffffll) return MUON_ERR_UNSUPPORTED;
   }
+  if (write_state) {
+    if (!states_distinct(S, n)) return MUON_ERR_INVALID_ARG;
+  } else if (n > 1) {
+    std::vector<const void*> at;
+    for (int j = 0; j < n; ++j) at.push_back(X[j].data);
+    if (!distinct(at)) return MUON_ERR_INVALID_ARG;
+  }
   static thread_local StateParams p;  // 4 KB that need no clearing
   int j = 0, mat = 0;
   while (j < n) {
@@ -684,38 +732,45 @@ cudaError_t run_step(muon_ctx* h, std::vector<Item>& items, const std::vector<Mo
 
 muon_status_t muon::half_orthogonalize(muon_ctx* h, const void* const* X, void* const* O, const muon_hparams_t* hp,
                                        cudaStream_t stream) {
-  std::vector<muon_view_t> x, o;
-  for (int i = 0; i < h->n; ++i) {
-    x.push_back(contiguous(X[i], h->shapes[i], h->dtype));
-    o.push_back(contiguous(O[i], h->shapes[i], h->dtype));
-  }
-  return muon_orthogonalize_views(h, x.data(), o.data(), h->n, hp, stream);
+  return no_throw([&]() -> muon_status_t {
+    std::vector<muon_view_t> x, o;
+    for (int i = 0; i < h->n; ++i) {
+      x.push_back(contiguous(X[i], h->shapes[i], h->dtype));
+      o.push_back(contiguous(O[i], h->shapes[i], h->dtype));
+    }
+    return muon_orthogonalize_views(h, x.data(), o.data(), h->n, hp, stream);
+  });
 }
 
 muon_status_t muon::half_step(muon_ctx* h, void* const* W, const void* const* G, void* const* M,
                               const muon_hparams_t* hp, cudaStream_t stream) {
-  if (!steps_ok(h, hp)) return MUON_ERR_INVALID_ARG;
-  std::vector<Item> items(h->n);
-  std::vector<MomentumIn> in(h->n);
-  for (int i = 0; i < h->n; ++i) {
-    const muon_shape_t& sh = h->shapes[i];
-    const muon_view_t w = contiguous(W[i], sh, h->dtype), g = contiguous(G[i], sh, h->dtype);
-    const size_t es = h->dtype == MUON_BF16 ? 2 : 4;
-    if ((reinterpret_cast<uintptr_t>(M[i]) % es) != 0) return MUON_ERR_INVALID_ARG;
-    items[i].first = in[i].first = i;
-    items[i].count = 1;
-    in[i].state = muon_state_t{M[i], nullptr, 1, sh.rows, sh.cols};
-    muon_status_t r = make_side(w, sh.rows, sh.cols, true, &items[i].dst);
-    if (r == MUON_OK) r = make_rows(g, in[i].state, false, &in[i].g);
-    if (r != MUON_OK) return r;
-    stage(h, i, 1, &items[i], &in[i].u);
-  }
-  DeviceGuard guard(h->device);
-  NvtxRange range("muon_step");
-  trace(h, -1, stream);
-  const cudaError_t e = run_step(h, items, in, kStateDense, hp, nullptr, stream);
-  trace_call_end(h);
-  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return no_throw([&]() -> muon_status_t {
+    if (!steps_ok(h, hp)) return MUON_ERR_INVALID_ARG;
+    std::vector<const void*> outs(W, W + h->n);
+    outs.insert(outs.end(), M, M + h->n);
+    if (!distinct(outs)) return MUON_ERR_INVALID_ARG;
+    std::vector<Item> items(h->n);
+    std::vector<MomentumIn> in(h->n);
+    for (int i = 0; i < h->n; ++i) {
+      const muon_shape_t& sh = h->shapes[i];
+      const muon_view_t w = contiguous(W[i], sh, h->dtype), g = contiguous(G[i], sh, h->dtype);
+      const size_t es = h->dtype == MUON_BF16 ? 2 : 4;
+      if ((reinterpret_cast<uintptr_t>(M[i]) % es) != 0) return MUON_ERR_INVALID_ARG;
+      items[i].first = in[i].first = i;
+      items[i].count = 1;
+      in[i].state = muon_state_t{M[i], nullptr, 1, sh.rows, sh.cols};
+      muon_status_t r = make_side(w, sh.rows, sh.cols, true, &items[i].dst);
+      if (r == MUON_OK) r = make_rows(g, in[i].state, false, &in[i].g);
+      if (r != MUON_OK) return r;
+      stage(h, i, 1, &items[i], &in[i].u);
+    }
+    DeviceGuard guard(h->device);
+    NvtxRange range("muon_step");
+    trace(h, -1, stream);
+    const cudaError_t e = run_step(h, items, in, kStateDense, hp, nullptr, stream);
+    trace_call_end(h);
+    return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  });
 }
 
 bool muon::half_fused_possible(const muon_ctx* h) {
@@ -758,8 +813,10 @@ muon_status_t muon_set_coefficients(muon_handle_t h, const float* abc, int steps
   if (h->mode != MUON_MODE_HALF) return MUON_ERR_UNSUPPORTED;
   for (int i = 0; i < 3 * steps; ++i)
     if (!std::isfinite(abc[i])) return MUON_ERR_INVALID_ARG;
-  h->coef.assign(abc, abc + 3 * steps);
-  return MUON_OK;
+  return no_throw([&]() -> muon_status_t {
+    h->coef.assign(abc, abc + 3 * steps);
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_orthogonalize_views(muon_handle_t h, const muon_view_t* X, const muon_view_t* O, int n,
@@ -767,38 +824,47 @@ muon_status_t muon_orthogonalize_views(muon_handle_t h, const muon_view_t* X, co
   if (h == nullptr || X == nullptr || O == nullptr || n < 1 || !hp_ok(hp, false)) return MUON_ERR_INVALID_ARG;
   if (h->mode != MUON_MODE_HALF) return MUON_ERR_UNSUPPORTED;
   if (!steps_ok(h, hp)) return MUON_ERR_INVALID_ARG;
-  std::vector<int> first;
-  muon_status_t r = cover(h, X, n, &first);
-  if (r != MUON_OK) return r;
-  std::vector<Item> items(n);
-  for (int j = 0; j < n; ++j) {
-    if (O[j].count != X[j].count) return MUON_ERR_INVALID_ARG;
-    const muon_shape_t& sh = h->shapes[first[j]];
-    items[j].first = first[j];
-    items[j].count = static_cast<int>(X[j].count);
-    r = make_side(X[j], sh.rows, sh.cols, false, &items[j].src);
-    if (r == MUON_OK) r = make_side(O[j], sh.rows, sh.cols, true, &items[j].dst);
+  return no_throw([&]() -> muon_status_t {
+    std::vector<int> first;
+    muon_status_t r = cover(h, X, n, &first);
     if (r != MUON_OK) return r;
-  }
-  DeviceGuard guard(h->device);
-  NvtxRange range("muon_orthogonalize_views");
-  muon_hparams_t q = *hp;
-  q.lr = 0.0f;
-  q.weight_decay = 0.0f;
-  trace(h, -1, stream);
-  const cudaError_t e = half_run(h, items, &q, true, false, stream);
-  trace_call_end(h);
-  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+    std::vector<Item> items(n);
+    std::vector<const void*> ins, outs;
+    for (int j = 0; j < n; ++j) {
+      if (O[j].count != X[j].count) return MUON_ERR_INVALID_ARG;
+      const muon_shape_t& sh = h->shapes[first[j]];
+      items[j].first = first[j];
+      items[j].count = static_cast<int>(X[j].count);
+      r = make_side(X[j], sh.rows, sh.cols, false, &items[j].src);
+      if (r == MUON_OK) r = make_side(O[j], sh.rows, sh.cols, true, &items[j].dst);
+      if (r != MUON_OK) return r;
+      const Side &a = items[j].src, &b = items[j].dst;  // in place: an element is written where it was read
+      if (a.data == b.data && (a.type != b.type || a.by_cols != b.by_cols || a.ld != b.ld || a.bs != b.bs))
+        return MUON_ERR_INVALID_ARG;
+      ins.push_back(X[j].data);
+      outs.push_back(O[j].data);
+    }
+    if (!apart(ins, outs)) return MUON_ERR_INVALID_ARG;
+    DeviceGuard guard(h->device);
+    NvtxRange range("muon_orthogonalize_views");
+    muon_hparams_t q = *hp;
+    q.lr = 0.0f;
+    q.weight_decay = 0.0f;
+    trace(h, -1, stream);
+    const cudaError_t e = half_run(h, items, &q, true, false, stream);
+    trace_call_end(h);
+    return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  });
 }
 
 muon_status_t muon_state_quantize(const muon_view_t* X, const muon_state_t* S, int n, muon_state_format_t format,
                                   const uint32_t* seed, cudaStream_t stream) {
-  return convert(X, S, n, format, seed, true, stream);
+  return no_throw([&] { return convert(X, S, n, format, seed, true, stream); });
 }
 
 muon_status_t muon_state_dequantize(const muon_state_t* S, const muon_view_t* X, int n, muon_state_format_t format,
                                     cudaStream_t stream) {
-  return convert(X, S, n, format, nullptr, false, stream);
+  return no_throw([&] { return convert(X, S, n, format, nullptr, false, stream); });
 }
 
 muon_status_t muon_momentum_state(muon_handle_t h, const muon_view_t* G, const muon_state_t* S, const muon_view_t* U,
@@ -807,26 +873,33 @@ muon_status_t muon_momentum_state(muon_handle_t h, const muon_view_t* G, const m
   if (h == nullptr || G == nullptr || S == nullptr || U == nullptr || n < 1 || !format_ok(format) || hp == nullptr ||
       !std::isfinite(hp->beta) || hp->beta < 0.0f || hp->beta > 1.0f)
     return MUON_ERR_INVALID_ARG;
-  std::vector<int> first;
-  muon_status_t r = cover(h, G, n, &first);
-  if (r != MUON_OK) return r;
-  std::vector<MomentumIn> in(n);
-  for (int j = 0; j < n; ++j) {
-    const muon_shape_t& sh = h->shapes[first[j]];
-    if (S[j].rows != sh.rows || S[j].cols != sh.cols || G[j].dtype != h->dtype || U[j].dtype != h->dtype)
-      return MUON_ERR_INVALID_ARG;
-    r = check_state(S[j]);
-    if (r == MUON_OK) r = make_rows(G[j], S[j], false, &in[j].g);
-    if (r == MUON_OK) r = make_rows(U[j], S[j], true, &in[j].u);
+  return no_throw([&]() -> muon_status_t {
+    std::vector<int> first;
+    muon_status_t r = cover(h, G, n, &first);
     if (r != MUON_OK) return r;
-    in[j].state = S[j];
-    in[j].first = first[j];
-  }
-  DeviceGuard guard(h->device);
-  trace(h, -1, stream);
-  const cudaError_t e = momentum_pass(h, in, format_of(format), kPassMomentum, hp, seed, stream);
-  trace_call_end(h);
-  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+    std::vector<MomentumIn> in(n);
+    std::vector<const void*> ins, outs;
+    for (int j = 0; j < n; ++j) {
+      const muon_shape_t& sh = h->shapes[first[j]];
+      if (S[j].rows != sh.rows || S[j].cols != sh.cols || G[j].dtype != h->dtype || U[j].dtype != h->dtype)
+        return MUON_ERR_INVALID_ARG;
+      r = check_state(S[j]);
+      if (r == MUON_OK) r = make_rows(G[j], S[j], false, &in[j].g);
+      if (r == MUON_OK) r = make_rows(U[j], S[j], true, &in[j].u);
+      if (r != MUON_OK) return r;
+      if (U[j].data == G[j].data && (in[j].u.ld != in[j].g.ld || in[j].u.bs != in[j].g.bs)) return MUON_ERR_INVALID_ARG;
+      ins.push_back(G[j].data);
+      outs.push_back(U[j].data);
+      in[j].state = S[j];
+      in[j].first = first[j];
+    }
+    if (!apart(ins, outs) || !states_distinct(S, n)) return MUON_ERR_INVALID_ARG;
+    DeviceGuard guard(h->device);
+    trace(h, -1, stream);
+    const cudaError_t e = momentum_pass(h, in, format_of(format), kPassMomentum, hp, seed, stream);
+    trace_call_end(h);
+    return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  });
 }
 
 muon_status_t muon_step_state(muon_handle_t h, const muon_view_t* W, const muon_view_t* G, const muon_state_t* S,
@@ -837,31 +910,36 @@ muon_status_t muon_step_state(muon_handle_t h, const muon_view_t* W, const muon_
     return MUON_ERR_INVALID_ARG;
   if (h->mode != MUON_MODE_HALF) return MUON_ERR_UNSUPPORTED;
   if (!steps_ok(h, hp)) return MUON_ERR_INVALID_ARG;
-  std::vector<int> first;
-  muon_status_t r = cover(h, W, n, &first);
-  if (r != MUON_OK) return r;
-  std::vector<Item> items(n);
-  std::vector<MomentumIn> in(n);
-  for (int j = 0; j < n; ++j) {
-    const muon_shape_t& sh = h->shapes[first[j]];
-    if (S[j].rows != sh.rows || S[j].cols != sh.cols || S[j].count != W[j].count || G[j].dtype != h->dtype ||
-        W[j].dtype != h->dtype)
-      return MUON_ERR_INVALID_ARG;
-    items[j].first = in[j].first = first[j];
-    items[j].count = static_cast<int>(W[j].count);
-    r = check_state(S[j]);
-    if (r == MUON_OK) r = make_rows(G[j], S[j], false, &in[j].g);
-    if (r == MUON_OK) r = make_side(W[j], sh.rows, sh.cols, true, &items[j].dst);
+  return no_throw([&]() -> muon_status_t {
+    std::vector<int> first;
+    muon_status_t r = cover(h, W, n, &first);
     if (r != MUON_OK) return r;
-    in[j].state = S[j];
-    stage(h, first[j], items[j].count, &items[j], &in[j].u);
-  }
-  DeviceGuard guard(h->device);
-  NvtxRange range("muon_step_state");
-  trace(h, -1, stream);
-  const cudaError_t e = run_step(h, items, in, format_of(format), hp, seed, stream);
-  trace_call_end(h);
-  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+    std::vector<Item> items(n);
+    std::vector<MomentumIn> in(n);
+    for (int j = 0; j < n; ++j) {
+      const muon_shape_t& sh = h->shapes[first[j]];
+      if (S[j].rows != sh.rows || S[j].cols != sh.cols || S[j].count != W[j].count || G[j].dtype != h->dtype ||
+          W[j].dtype != h->dtype)
+        return MUON_ERR_INVALID_ARG;
+      items[j].first = in[j].first = first[j];
+      items[j].count = static_cast<int>(W[j].count);
+      r = check_state(S[j]);
+      if (r == MUON_OK) r = make_rows(G[j], S[j], false, &in[j].g);
+      if (r == MUON_OK) r = make_side(W[j], sh.rows, sh.cols, true, &items[j].dst);
+      if (r != MUON_OK) return r;
+      in[j].state = S[j];
+      stage(h, first[j], items[j].count, &items[j], &in[j].u);
+    }
+    std::vector<const void*> outs;
+    for (int j = 0; j < n; ++j) outs.push_back(W[j].data);
+    if (!distinct(outs) || !states_distinct(S, n)) return MUON_ERR_INVALID_ARG;
+    DeviceGuard guard(h->device);
+    NvtxRange range("muon_step_state");
+    trace(h, -1, stream);
+    const cudaError_t e = run_step(h, items, in, format_of(format), hp, seed, stream);
+    trace_call_end(h);
+    return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  });
 }
 
 }  // extern "C"

@@ -148,3 +148,16 @@ def test_half_workspace():
             B.muon_workspace_size([(512, 768)], dtype, B.MUON_MODE_FAST)
     with pytest.raises(B.MuonError):
         B.muon_workspace_size([(512, 768)], B.MUON_FP16, B.MUON_MODE_HALF)
+
+
+def test_one_place_written_twice_is_refused():
+    two = lambda make, a, b: make([tuple(a.values()), tuple(b.values())])  # noqa: E731
+    for codes, scales in ((4096, 8192), (8192, 4096)):   # codes, or scales, shared by two states
+        other = {**STATE, "codes": codes, "scales": scales}
+        with pytest.raises(B.MuonError) as e:
+            B.muon_state_quantize(two(B.views, VIEW, VIEW), two(B.states, {**STATE, "scales": 12288 if codes == 4096 else 4096}, other), 2,
+                                  B.MUON_STATE_INT8, None, 0)
+        assert e.value.code == B.MUON_ERR_INVALID_ARG
+    with pytest.raises(B.MuonError) as e:                # read back into one tensor twice
+        B.muon_state_dequantize(two(B.states, STATE, {**STATE, "codes": 1 << 20}), two(B.views, VIEW, VIEW), 2, B.MUON_STATE_INT8, 0)
+    assert e.value.code == B.MUON_ERR_INVALID_ARG
