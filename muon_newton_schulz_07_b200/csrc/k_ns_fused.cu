@@ -139,6 +139,8 @@ __host__ __device__ __forceinline__ FTile decode(const NsParams& p, int t) {
   return f;
 }
 
+__device__ __forceinline__ bool on_diagonal(const FTile& f) { return f.kind != kUpdate && f.row0 == f.col0; }
+
 // Index of the completion counter of (stage s, matrix of f).
 __host__ __device__ __forceinline__ size_t counter_index(const NsParams& p, int s, const FTile& f) {
   return static_cast<size_t>(s) * p.nslots + p.g[f.g].scal_base + f.mat;
@@ -285,7 +287,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           *abort_flag = 1;
           break;
         }
-        const uint32_t bytes = 2 * (A_STAGE + nsub * B_STAGE);
+        // On the diagonal of A and B' a CTA's half of the second operand is its first operand: it is loaded
+        // once (a large set is bound by what its tiles read from L2).
+        const int first_sub = on_diagonal(f) ? 1 : 0;
+        const uint32_t bytes = 2 * (A_STAGE + (nsub - first_sub) * B_STAGE);
         const int kblocks = k_slices(G, f.kind);
         const int arow = f.row0 + static_cast<int>(rank) * BM;
         const int ia = f.row0 / TILE, jb = f.col0 / TILE;
@@ -305,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             tma_load_3d_pair(sa, ma_row, fb, k0, arow, f.mat);
           else
             tma_load_4d_pair(sa, ma_chk, fb, 0, k0, arow / 64, f.mat);
-          for (int u = 0; u < nsub; ++u) {
+          for (int u = first_sub; u < nsub; ++u) {
             const int bcol = f.col0 + u * TILE + half;
             const bool tbu = tb || (sym_b && k0 / TILE < jb + u);
             if (!(upd || tbu))
@@ -343,6 +348,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const int kblocks = k_slices(G, f.kind);
         const bool sym_a = f.kind != kGram, sym_b = f.kind == kPoly, upd = f.kind == kUpdate;
         const int ia = f.row0 / TILE, jb = f.col0 / TILE;
+        const uint32_t b_at = on_diagonal(f) ? 0u : A_STAGE;  // the (first) second operand within a stage
         auto major_a = [&](int kb) { return sym_a && (kb * BK) / TILE < ia; };
         // the B operand of half u covers block column jb + u
         auto major_b = [&](int kb, int u) { return upd || (sym_b && (kb * BK) / TILE < jb + u); };
@@ -359,7 +365,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
             tc_fence_after();
             const uint32_t sa = smem_base + stage * SB;
-            mma_slice<HALF>(d, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), kb == 0);
+            mma_slice<HALF>(d, sa, sa + b_at, major_a(kb), major_b(kb, 0), kb == 0);
             tc_commit_pair_mc(empty_bar(stage), 0x3);  // frees the stage in both CTAs
             if (++stage == NST) {
               stage = 0;
@@ -384,7 +390,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
             tc_fence_after();
             const uint32_t sa = smem_base + stage * SB;
-            mma_slice<HALF>(tmem_base, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), kb == 0);
+            mma_slice<HALF>(tmem_base, sa, sa + b_at, major_a(kb), major_b(kb, 0), kb == 0);
             held[kb] = stage;
             if (++stage == NST) {
               stage = 0;
@@ -406,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
             tc_fence_after();
             const uint32_t sa = smem_base + stage * SB;
-            mma_slice<HALF>(tmem_base, sa, sa + A_STAGE, major_a(kb), major_b(kb, 0), false);
+            mma_slice<HALF>(tmem_base, sa, sa + b_at, major_a(kb), major_b(kb, 0), false);
             mma_slice<HALF>(tmem_base + TILE, sa, sa + A_STAGE + B_STAGE, major_a(kb), major_b(kb, 1), false);
             tc_commit_pair_mc(empty_bar(stage), 0x3);
             if (++stage == NST) {

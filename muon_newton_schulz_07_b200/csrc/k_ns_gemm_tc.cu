@@ -228,13 +228,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
         const TcGroup& G = p.g[ti.g];
         const int arow = ti.row0 + static_cast<int>(rank) * BM;
         const int ia = ti.row0 / TILE, jb = ti.col0 / TILE;
+        // On the diagonal of A and B' a CTA's half of the second operand is its first operand: loaded once.
+        const bool diagonal = KIND != kUpdate && ti.row0 == ti.col0;
         bool ok = true;
         for (int kb = 0; kb < G.kblocks; ++kb) {
           if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, tmo, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), 2 * SB);
+          if (rank == 0) mbar_arrive_expect_tx(full_bar(stage), diagonal ? 2 * A_STAGE : 2 * SB);
           const uint32_t fb = map_to_rank(full_bar(stage), 0);
           const uint32_t sa = smem_base + stage * SB, sb = sa + A_STAGE;
           const int k0 = kb * BK;
@@ -251,7 +253,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
           else
             tma_load_4d_pair(sa, &G.tm_at, fb, 0, k0, arow / 64, ti.mat);
 #pragma unroll
-          for (int u = 0; u < NSUB; ++u) {
+          for (int u = 0; u < (diagonal ? 0 : NSUB); ++u) {
             const int bcol = ti.col0 + u * TILE + half;
             if (!mnb)
               tma_load_3d_pair(sb + u * B_STAGE, &G.tm_b, fb, k0, bcol, ti.mat);
@@ -293,13 +295,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Layout<KIND, WIDE>::
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TW);
         const int ia = ti.row0 / TILE, jb = ti.col0 / TILE;
+        const uint32_t b_at = KIND != kUpdate && ti.row0 == ti.col0 ? 0u : A_STAGE;
         for (int kb = 0; kb < G.kblocks; ++kb) {
           if (!mbar_wait_bounded(full_bar(stage), phase, tmo, abort_flag, p.status)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t sa = smem_base + stage * SB, sb = sa + A_STAGE;
+          const uint32_t sa = smem_base + stage * SB, sb = sa + b_at;
           const int kk = kb * BK / TILE;
           const bool mna = sym_a && kk < ia;                        // transposed block of A / B'
           const bool mnb = (KIND == kUpdate) || (sym_b && kk < jb);
