@@ -26,8 +26,8 @@
 // The per-tile machinery is that of the staged kernel (CTA pairs with tcgen05.mma.cta_group::2,
 // TMA operand ring without multicast, upper blocks only for the symmetric A and B', MN-major
 // reads of the transposed blocks, eight epilogue warps, fused parameter write in the last
-// Update), with the stage a run-time property of the tile.  Update tiles may be 256 x 512
-// (when every group's padded width allows it); TMEM holds two 256-column accumulator slots:
+// Update), with the stage a run-time property of the tile.  Stages of few tiles take 256 x 128 ones
+// (see fused_tables); Update tiles may be 256 x 512 (when every group's padded width allows it).  TMEM holds two 256-column accumulator slots:
 // a 256-wide tile takes one slot (alternating), a 512-wide tile takes both, and its epilogue
 // drains the first half, hands that slot back, then drains the second, while the MMA issuer
 // already accumulates the next tile's first k slices into the freed half.
@@ -45,6 +45,7 @@ namespace {
 
 constexpr int BM = kTcBM, BN = kTcBN, BK = kTcBK;
 constexpr int TILE = 256;
+constexpr int NARROW = 128;                          // columns of a narrow tile
 constexpr uint32_t A_STAGE = BM * BK * 2;           // 16 KB: this CTA's 128 rows of A
 constexpr uint32_t B_STAGE = (BN / 2) * BK * 2;     // 16 KB: this CTA's half of one 256-column B tile
 constexpr uint32_t TMEM_COLS = 512;                 // two 256-column accumulator slots
@@ -109,37 +110,27 @@ __host__ __device__ __forceinline__ FTile decode(const NsParams& p, int t) {
     const int tm = q / tc;
     f.row0 = tm * TILE;
     f.col0 = (q - tm * tc) * f.tw;
-  } else if (p.sym_wide) {
-    // block row I of the upper triangle holds blocks J = I .. T-1, taken two at a time
-    // (256 x 512 tiles) with a 256-wide tile for an odd one out at the end of the row
-    const int tpm = sym_tiles(T, true);
-    f.mat = local / tpm;
-    int q = local - f.mat * tpm, I = 0;
-    while (q >= (T - I + 1) / 2) {
-      q -= (T - I + 1) / 2;
-      ++I;
-    }
-    const int J = I + 2 * q;
-    f.row0 = I * TILE;
-    f.col0 = J * TILE;
-    f.tw = (J + 1 < T) ? 2 * TILE : TILE;
   } else {
-    // upper-triangle block (I, J), I <= J, row-major over the triangle
-    const int tpm = sym_tiles(T, false);
+    // upper-triangle block (I, J), I <= J, row-major over the triangle, its halves in turn where tiles are narrow
+    const int tpm = sym_tiles(T, p.sym_tw);
     f.mat = local / tpm;
     int q = local - f.mat * tpm, I = 0;
+    const int part = p.sym_tw < TILE ? q & 1 : 0;
+    if (p.sym_tw < TILE) q >>= 1;
     while (q >= T - I) {
       q -= T - I;
       ++I;
     }
     f.row0 = I * TILE;
-    f.col0 = (I + q) * TILE;
-    f.tw = TILE;
+    f.col0 = (I + q) * TILE + part * p.sym_tw;
+    f.tw = p.sym_tw;
   }
   return f;
 }
 
-__device__ __forceinline__ bool on_diagonal(const FTile& f) { return f.kind != kUpdate && f.row0 == f.col0; }
+__device__ __forceinline__ bool on_diagonal(const FTile& f) {
+  return f.kind != kUpdate && f.row0 == f.col0 && f.tw >= TILE;  // (the halves of narrow tiles differ)
+}
 
 // Index of the completion counter of (stage s, matrix of f).
 __host__ __device__ __forceinline__ size_t counter_index(const NsParams& p, int s, const FTile& f) {
@@ -167,7 +158,7 @@ __host__ __device__ __forceinline__ bool dependency_stage(const NsParams& p, con
     *tiles = static_cast<unsigned int>(T * (G.np / p.upd_tw[0]));  // that iteration is not the last
   } else {
     *stage = 3 * f.it + f.kind - 1;
-    *tiles = static_cast<unsigned int>(sym_tiles(T, p.sym_wide != 0));
+    *tiles = static_cast<unsigned int>(sym_tiles(T, p.sym_tw));
   }
   return true;
 }
@@ -181,11 +172,11 @@ __device__ __forceinline__ bool dependency(const NsParams& p, const FTile& f, co
   return true;
 }
 
-// Issue the four K = 16 MMAs of one 64-deep k slice into the 256 columns at d_tmem.
+// Issue the four K = 16 MMAs of one 64-deep k slice into the n columns at d_tmem.
 template <bool HALF>
 __device__ __forceinline__ void mma_slice(uint32_t d_tmem, uint32_t sa, uint32_t sb, bool mna, bool mnb,
-                                          bool first) {
-  const uint32_t idesc = idesc_f16_f32(HALF, 2 * BM, BN, mna ? 1 : 0, mnb ? 1 : 0);
+                                          bool first, int n = BN) {
+  const uint32_t idesc = idesc_f16_f32(HALF, 2 * BM, n, mna ? 1 : 0, mnb ? 1 : 0);
   // K-major: 16 k per step = 32 bytes along the swizzled row; MN-major: 16 k rows = 2 KB, the
   // two 64-wide M/N chunks 8 KB apart.
   const uint64_t adesc0 = mna ? smem_desc_sw128(sa, 8192, 1024) : smem_desc_sw128(sa, 16, 1024);
@@ -264,7 +255,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       // ---------------------------------------------------------- TMA producer (both CTAs)
       int stage = 0;
       uint32_t phase = 0;
-      const int half = static_cast<int>(rank) * (BN / 2);
       bool ok = true;
       for (int t = p.t_begin + cl; t < p.t_end && ok; t += ncl) {
         const FTile f = decode(p, t);
@@ -281,7 +271,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const CUtensorMap* mb_row = f.kind == kGram ? &G.x_row[cur] : f.kind == kPoly ? &G.a_row : &G.x_row[cur];
         const CUtensorMap* mb_chk = f.kind == kGram ? &G.x_chk[cur] : f.kind == kPoly ? &G.a_chk : &G.x_chk[cur];
         const bool sym_a = f.kind != kGram, sym_b = f.kind == kPoly, upd = f.kind == kUpdate;
-        const int nsub = f.tw / TILE;
+        const int nsub = f.tw > TILE ? 2 : 1;
+        // A narrow tile's halves of the second operand are 64 columns; the box of 128 is loaded all the same
+        // (beyond the matrix: zeros), since few tiles are not bound by what they load.
+        const int half = static_cast<int>(rank) * (f.tw < TILE ? f.tw / 2 : BN / 2);
         if (!WR && nsub > 1) {  // a 512-wide tile does not fit this ring's stages (host plan error)
           record_status(p.status, kDevFault);
           *abort_flag = 1;
@@ -352,7 +345,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         auto major_a = [&](int kb) { return sym_a && (kb * BK) / TILE < ia; };
         // the B operand of half u covers block column jb + u
         auto major_b = [&](int kb, int u) { return upd || (sym_b && (kb * BK) / TILE < jb + u); };
-        if (f.tw == TILE) {
+        if (f.tw <= TILE) {
           const int sl = next_slot;
           next_slot ^= 1;
           if (!mbar_wait_bounded(acce_bar(sl), (uses[sl] & 1u) ^ 1u, tmo, abort_flag, p.status)) break;
@@ -365,7 +358,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
             tc_fence_after();
             const uint32_t sa = smem_base + stage * SB;
-            mma_slice<HALF>(d, sa, sa + b_at, major_a(kb), major_b(kb, 0), kb == 0);
+            mma_slice<HALF>(d, sa, sa + b_at, major_a(kb), major_b(kb, 0), kb == 0, f.tw);
             tc_commit_pair_mc(empty_bar(stage), 0x3);  // frees the stage in both CTAs
             if (++stage == NST) {
               stage = 0;
@@ -437,7 +430,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     // plain stores into the caller's W.
     const int e = warp - 2;                 // epilogue warp 0..7
     const int quad = warp & 3;              // TMEM lanes 32*quad .. 32*quad+31
-    const int cbase = (e >> 2) * 128;       // this warp's first column within each half
     uint8_t* wblock = smem + EPI_OFFSET + e * EPI_WARP_BYTES;  // this warp's own epilogue block
     uint8_t* otile = wblock;
     const uint32_t otile_u32 = smem_u32(otile);
@@ -452,7 +444,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     for (int t = p.t_begin + cl; t < p.t_end && ok; t += ncl) {
       const FTile f = decode(p, t);
       const NsGroup& G = p.g[f.g];
-      const int nsub = f.tw / TILE;
+      const int nsub = f.tw > TILE ? 2 : 1;
+      const int nch = f.tw < TILE ? 2 : 4;     // chunks of a warp in each half ...
+      const int cbase = (e >> 2) * 32 * nch;   // ... and the first one's column
       const bool fw = p.fuse_write != 0 && f.kind == kUpdate && f.last;
       const bool aux = f.kind == kPoly;   // the polynomial's b A + a I reads A
       const CUtensorMap* out_map =
@@ -485,8 +479,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       auto aux_issue = [&](int h) {
         bulk_wait_read<0>();  // the tiles' last stores have been read
         ++nissued;
-        mbar_arrive_expect_tx(aux_bar(e), 4 * EPI_AUX_BYTES);
-        for (int c = 0; c < 4; ++c)
+        mbar_arrive_expect_tx(aux_bar(e), nch * EPI_AUX_BYTES);
+        for (int c = 0; c < nch; ++c)
           tma_load_3d(otile_u32 + c * EPI_OUT_BYTES, &G.a_st, aux_bar(e), f.col0 + chunk_col(h, c), gr0, f.mat);
       };
       if (aux) {
@@ -554,13 +548,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
         const uint32_t acce_leader = map_to_rank(acce_bar(slot), 0);
         if (fw) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
+          for (int c = 0; c < nch; ++c) {
             const int colw = chunk_col(h, c);
             const int gc0 = f.col0 + colw;
             float v[32];
             __syncwarp();
             tmem_ld_32cols(tmem_base + tlane + tcol0 + static_cast<uint32_t>(colw), v);
-            if (c == 3) {
+            if (c == nch - 1) {
               // this warp's part of the slot has been read: hand it back to the MMA issuer
               tc_fence_before();
               __syncwarp();
@@ -568,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
             }
             uint4 nx[4];
             if (has_pre) {
-              if (c + 1 < 4)
+              if (c + 1 < nch)
                 pre_load(chunk_col(h, c + 1), nx);
               else if (h + 1 < nsub)
                 pre_load(chunk_col(h + 1, 0), nx);
@@ -622,9 +616,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           }
 #pragma unroll
           for (int cc = 0; cc < 4; cc += 2) {
+            if (cc >= nch) break;
             float v[64];
             tmem_ld_64cols(tmem_base + tlane + tcol0 + static_cast<uint32_t>(chunk_col(h, cc)), v);
-            if (cc == 2) {
+            if (cc == nch - 2) {
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive_remote(acce_leader);
@@ -661,7 +656,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
           __syncwarp();
 #pragma unroll
           for (int c = 0; c < 4; ++c)
-            tma_store_3d_lead(lead, out_map, otile_u32 + c * EPI_OUT_BYTES, f.col0 + chunk_col(h, c), gr0, f.mat);
+            tma_store_3d_lead(c < nch ? lead : 0u, out_map, otile_u32 + c * EPI_OUT_BYTES, f.col0 + chunk_col(h, c), gr0, f.mat);
           if (lead) bulk_commit();
           __syncwarp();
         }
@@ -731,8 +726,8 @@ long long check_fused_tiles(const NsParams& p) {
     }
     const NsGroup& G = p.g[f.g];
     const int T = G.tdim;
-    if (f.mat < 0 || f.mat >= G.cnt || f.row0 % TILE != 0 || f.col0 % TILE != 0 || f.row0 < 0 ||
-        f.row0 + TILE > G.mp || (f.tw != TILE && f.tw != 2 * TILE)) {
+    if (f.mat < 0 || f.mat >= G.cnt || f.row0 % TILE != 0 || f.col0 % NARROW != 0 || f.row0 < 0 ||
+        f.row0 + TILE > G.mp || (f.tw != NARROW && f.tw != TILE && f.tw != 2 * TILE)) {
       ++bad;
       continue;
     }
@@ -741,7 +736,7 @@ long long check_fused_tiles(const NsParams& p) {
       ++bad;
       continue;
     }
-    if (f.kind == kUpdate && f.last && p.fuse_write && f.tw != TILE) ++bad;
+    if (f.kind == kUpdate && f.last && p.fuse_write && f.tw > TILE) ++bad;
     const size_t ci = counter_index(p, 3 * f.it + f.kind, f);
     if (ci >= count.size()) {
       ++bad;
@@ -750,9 +745,9 @@ long long check_fused_tiles(const NsParams& p) {
     ++count[ci];
     last[ci] = t;
     std::vector<unsigned char>& cv = cover[ci];
-    const int nb = (width / TILE) * T;
+    const int nb = (width / NARROW) * T;
     if (cv.empty()) cv.assign(nb, 0);
-    for (int c = f.col0; c < f.col0 + f.tw; c += TILE) ++cv[(f.row0 / TILE) * (width / TILE) + c / TILE];
+    for (int c = f.col0; c < f.col0 + f.tw; c += NARROW) ++cv[(f.row0 / TILE) * (width / NARROW) + c / NARROW];
     int s;
     unsigned int tiles;
     if (dependency_stage(p, f, &s, &tiles)) {
@@ -772,10 +767,10 @@ long long check_fused_tiles(const NsParams& p) {
             ++bad;
             continue;
           }
-          const int cols = (kind == kUpdate ? G.np : G.mp) / TILE;
+          const int cols = (kind == kUpdate ? G.np : G.mp) / NARROW;
           for (int I = 0; I < T; ++I)
             for (int J = 0; J < cols; ++J) {
-              const int want = (kind == kUpdate || J >= I) ? 1 : 0;  // upper blocks only for A, B'
+              const int want = (kind == kUpdate || J >= I * (TILE / NARROW)) ? 1 : 0;  // upper blocks only for A, B'
               if (cover[ci][I * cols + J] != want) ++bad;
             }
         }
@@ -827,7 +822,7 @@ cudaError_t launch_fused_kind(const NsParams& p, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_ns_fused(const NsParams& p, int num_sms, cudaStream_t s) {
   if (p.t_end <= p.t_begin) return cudaSuccess;
-  const bool wide = p.upd_tw[0] > TILE || p.upd_tw[1] > TILE || p.sym_wide != 0;
+  const bool wide = p.upd_tw[0] > TILE || p.upd_tw[1] > TILE;
   if (p.half) return wide ? launch_fused_kind<true, true>(p, num_sms, s) : launch_fused_kind<false, true>(p, num_sms, s);
   return wide ? launch_fused_kind<true, false>(p, num_sms, s) : launch_fused_kind<false, false>(p, num_sms, s);
 }

@@ -396,8 +396,12 @@ cudaError_t enqueue_front(muon_ctx* h, const void* const* src, void* const* mom,
 // Tile tables of the single-launch schedule (everything but the tensor maps, pointers and
 // hyper-parameters): Update tiles 256 x 512 when every group's padded width allows it (except in
 // the iteration that writes W), Gram and Poly two upper blocks per tile, and the first tile of
-// each (stage, group) within an iteration.
-void muon::fused_tables(const std::vector<const GroupPlan*>& groups, int nslots, int k, bool fuse_write, bool wide, NsParams* q) {
+// each (stage, group) within an iteration.  Tiles of a stage that leaves half of the `pairs` idle are 256 x 128
+// instead: twice as many, whose products and epilogue take half as long.  Measured, five iterations, 256 x 256
+// tiles and this rule: 2 x 512 x 512 140 and 122 us, 4 x 768 x 768 166 and 153 (narrow in all stages);
+// 7 x 331 x 1003 167 and 159, 4 x 512 x 2048 188 and 178 (in Gram and Poly).  pairs = 0: never.
+void muon::fused_tables(const std::vector<const GroupPlan*>& groups, int nslots, int k, bool fuse_write, bool wide,
+                        int pairs, NsParams* q) {
   std::memset(q, 0, sizeof(*q));
   const int ng = static_cast<int>(groups.size());
   for (const GroupPlan* gp : groups) wide = wide && gp->np % 512 == 0;
@@ -405,7 +409,14 @@ void muon::fused_tables(const std::vector<const GroupPlan*>& groups, int nslots,
   q->upd_tw[1] = (wide && !fuse_write) ? 512 : 256;  // the Update that writes W keeps 256-wide tiles
   // Gram and Poly keep one 256 x 256 block per tile: two blocks per tile (256 x 512, one
   // accumulator, half of the epilogue exposed) measured 13 % (Gram) and 20 % (Poly) slower on d24
-  q->sym_wide = 0;
+  q->sym_tw = 256;
+  long long sym = 0, update = 0;
+  for (const GroupPlan* gp : groups) {
+    sym += static_cast<long long>(gp->cnt) * sym_tiles(gp->mp / 256, 256);
+    update += static_cast<long long>(gp->cnt) * (gp->mp / 256) * (gp->np / 256);
+  }
+  if (2 * sym <= pairs) q->sym_tw = 128;
+  if (2 * update <= pairs) q->upd_tw[0] = q->upd_tw[1] = 128;
   for (int g = 0; g < ng; ++g) {
     const GroupPlan& gp = *groups[g];
     NsGroup& G = q->g[g];
@@ -424,7 +435,7 @@ void muon::fused_tables(const std::vector<const GroupPlan*>& groups, int nslots,
       for (int g = 0; g < ng; ++g) {
         const GroupPlan& gp = *groups[g];
         const int T = gp.mp / 256;
-        const int tpm = kind == kUpdate ? T * (gp.np / q->upd_tw[L]) : sym_tiles(T, q->sym_wide != 0);
+        const int tpm = kind == kUpdate ? T * (gp.np / q->upd_tw[L]) : sym_tiles(T, q->sym_tw);
         q->begin[L][kind][g] = off;
         off += tpm * gp.cnt;
       }
@@ -540,7 +551,7 @@ cudaError_t enqueue_ns(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st, i
     NvtxRange range("muon: Newton-Schulz, every iteration in one launch");
     NsParams& q = h->ns;
     const std::vector<const GroupPlan*> groups = all_groups(P);
-    fused_tables(groups, h->n, k, fuse, true, &q);
+    fused_tables(groups, h->n, k, fuse, true, 0, &q);
     fused_maps(groups, &q);
     q.gram = 1.0f;
     for (int t = 0; t < k; ++t) {
@@ -957,8 +968,10 @@ muon_status_t muon_check_plan(const muon_shape_t* shapes, int n, int ns_steps, i
   }
   if (ns_steps >= 1 && P.groups.size() <= static_cast<size_t>(kTcMaxGroups)) {
     for (int fw = 0; fw < 2; ++fw) {
-      fused_tables(all_groups(P), n, ns_steps, fw != 0, true, ns);
-      bad += check_fused_tiles(*ns);
+      for (int pairs : {0, num_sms / 2, 0x7fffffff}) {  // never narrow, as the rule has it, always
+        fused_tables(all_groups(P), n, ns_steps, fw != 0, true, pairs, ns);
+        bad += check_fused_tiles(*ns);
+      }
     }
   }
   delete ew;

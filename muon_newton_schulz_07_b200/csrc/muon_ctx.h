@@ -106,7 +106,7 @@ void stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur, int 
 
 // The single-launch schedule over these groups: tile tables (`wide`: with 256 x 512 Update tiles where
 // every padded width allows them), and tensor maps.
-void fused_tables(const std::vector<const GroupPlan*>& groups, int nslots, int k, bool fuse_write, bool wide,
+void fused_tables(const std::vector<const GroupPlan*>& groups, int nslots, int k, bool fuse_write, bool wide, int pairs,
                   NsParams* q);
 void fused_maps(const std::vector<const GroupPlan*>& groups, NsParams* q);
 // The small-matrix kernel's groups, X_k into buffer `fin`.

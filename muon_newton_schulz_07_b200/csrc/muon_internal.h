@@ -171,8 +171,8 @@ struct NsParams {
   int tiles_iter;        // tiles of an iteration other than the last
   int total_tiles;
   int t_begin, t_end;    // the tiles this launch runs: [0, total_tiles), or one stage of them
-  int upd_tw[2];         // Update tile width (256 or 512) of [other, last] iterations
-  int sym_wide;          // Gram and Poly take two neighbouring upper blocks per tile (256 x 512)
+  int upd_tw[2];         // Update tile width (128, 256 or 512) of [other, last] iterations
+  int sym_tw;            // Gram and Poly tile width (128 or 256)
   int fuse_write;        // the last Update writes the parameters (see TcParams)
   // first tile of (stage, group) within an iteration, [other, last][stage][group];
   // [..][stage][ngroups] is the end of the stage
@@ -191,15 +191,9 @@ struct NsParams {
   unsigned char wtrans[kTcMaxFused];
 };
 
-// Tiles per matrix of a symmetric stage (Gram, Poly) over the T x T blocks of the upper
-// triangle: one per block, or (wide) one per pair of neighbouring blocks of a block row, with a
-// 256-wide tile for the odd block at the end of a row.
-__host__ __device__ inline int sym_tiles(int T, bool wide) {
-  if (!wide) return T * (T + 1) / 2;
-  int n = 0;
-  for (int I = 0; I < T; ++I) n += (T - I + 1) / 2;
-  return n;
-}
+// Tiles per matrix of a symmetric stage (Gram, Poly) over the T x T blocks of the upper triangle: one
+// per block of 256 x 256, or two of 256 x 128.
+__host__ __device__ inline int sym_tiles(int T, int tw) { return T * (T + 1) / 2 * (256 / tw); }
 
 size_t fused_smem_bytes();
 cudaError_t launch_ns_fused(const NsParams& p, int num_sms, cudaStream_t s);

@@ -344,7 +344,7 @@ cudaError_t enqueue_single(muon_ctx* h, const std::vector<Item>& items, const mu
   cudaError_t e = cudaMemsetAsync(deps, 0, sizeof(unsigned int) * 3 * k * static_cast<size_t>(h->n), st);
   if (e != cudaSuccess) return e;
   NsParams& q = h->ns;
-  fused_tables(groups, h->n, k, fuse, wide_pays(h, groups), &q);
+  fused_tables(groups, h->n, k, fuse, wide_pays(h, groups), h->num_sms / 2, &q);
   fused_maps(groups, &q);
   q.half = 1;
   fill_iterations(h, hp, &q);
