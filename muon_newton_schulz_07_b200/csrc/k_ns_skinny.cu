@@ -178,8 +178,9 @@ __device__ __noinline__ void write_eight(void* dst, int type, long long at, uint
   store_eight(dst, type, at, 8, true, v);
 }
 
-// CLUSTER: 1, 2, or 4 for any larger cluster.
-template <int CLUSTER>
+// CLUSTER: 1, 2, or 4 for any larger cluster.  FOLDED: matrices are cut into column ranges (their sums in code
+// that every tile carried took 288 of 1536 x 128 from 320 to 328 us).
+template <int CLUSTER, bool FOLDED>
 __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_constant__ SkinnyParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -203,7 +204,8 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   const int rank = C > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int tile = static_cast<int>(blockIdx.x) / C;
   const int lh = __ffs(p.slot_rows) - 1;         // log2 of the rows of a matrix in the tile
-  const int lf = __ffs(p.folds) - 1;             // log2 of the column ranges a matrix is cut into
+  const int folds = FOLDED ? p.folds : 1;        // column ranges a matrix is cut into
+  const int lf = __ffs(folds) - 1;
   const int ls = lh + lf;                        // log2 of the tile's rows that hold a matrix
   const int used = p.slots << ls;                // rows of the tile in use
   const int used16 = (used + 15) & ~15;
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   const int ig = (tid >> 3) & 15;                // rows 8 ig .. 8 ig + 7
   const int i0 = (ig * 8) & (p.slot_rows - 1);   // the first of them, within the matrix
   const int slot_l = (ig * 8) >> ls;             // the matrix of the tile
-  const int col0 = ((((ig * 8) >> lh) & (p.folds - 1)) * C + rank) * p.width;  // first column of those rows
+  const int col0 = ((((ig * 8) >> lh) & (folds - 1)) * C + rank) * p.width;  // first column of those rows
   int seg = 0, e = -1;                           // view of those rows, and matrix within it (-1: none)
   if (ig * 8 < used && first_mat + slot_l < p.total && i0 < p.m) {
     while (seg + 1 < p.nseg && p.seg[seg + 1].mat_begin <= first_mat + slot_l) ++seg;
@@ -550,7 +552,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
       {
         float v[32];
         if (ok && (active || C > 1)) tmem_ld_32cols(t_row + T_A + ca0, v);
-        if (p.folds > 1) {
+        if (FOLDED) {
           // The matrix's A is the sum of its column ranges' blocks: through the place of A, fp32, each row
           // its h columns in groups of four.  Of h >= 32 a warp's 32 columns are all its rows' own or none.
           const int lq = lh - 2, q0 = (ca0 & (p.slot_rows - 1)) >> 2, swz = r & min(7, (1 << lq) - 1);
@@ -571,7 +573,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[i] = 0.0f;
 #pragma unroll 1
-            for (int f = 0; f < p.folds; ++f) {
+            for (int f = 0; f < folds; ++f) {
               const uint32_t from = first + f * step;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -593,7 +595,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
             mbar_arrive_expect_tx(rows_full, (C - 1) * rows_c * 256);
           }
           __syncwarp();
-          if (C == 2 && p.folds > 1) wait_on(peer_free, par);
+          if (C == 2 && FOLDED) wait_on(peer_free, par);
           else if (C == 2 && it > 0) wait_on(peer_free, par ^ 1);
           if (ok && owner != rank) {
             const uint32_t bar = map_to_rank(share_full, owner);
@@ -664,7 +666,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
       wait_on(aa_full, par);
       if (C > 1) wait_on(peer_got, par);  // the rows of A that this CTA copied have been read
       epi_sync();
-      if (C == 2 && p.folds == 1 && tid == 0 && ok)
+      if (C == 2 && !FOLDED && tid == 0 && ok)
         mbar_arrive_remote(map_to_rank(peer_free, rank ^ 1));  // A has been read
       if (ok && active) {
         const bool out = slot >= 0 && poison[slot] != 0;
@@ -808,7 +810,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
 }  // namespace
 
 namespace {
-template <int CLUSTER>
+template <int CLUSTER, bool FOLDED>
 cudaError_t launch(const SkinnyParams& p, cudaStream_t s) {
   // The shared-memory limit is a property of the function on each device: set it once per device.
   static std::atomic<unsigned long long> attr_set{0};
@@ -817,7 +819,7 @@ cudaError_t launch(const SkinnyParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   const unsigned long long bit = 1ull << (dev & 63);
   if ((attr_set.load() & bit) == 0) {
-    e = cudaFuncSetAttribute(ns_skinny_kernel<CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(ns_skinny_kernel<CLUSTER, FOLDED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(SMEM_LIMIT));
     if (e != cudaSuccess) return e;
     attr_set.fetch_or(bit);
@@ -835,15 +837,15 @@ cudaError_t launch(const SkinnyParams& p, cudaStream_t s) {
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, ns_skinny_kernel<CLUSTER>, p);
+  return cudaLaunchKernelEx(&cfg, ns_skinny_kernel<CLUSTER, FOLDED>, p);
 }
 }  // namespace
 
 cudaError_t launch_ns_skinny(const SkinnyParams& p, cudaStream_t s) {
   if (p.total <= 0) return cudaSuccess;
-  if (p.cluster == 1) return launch<1>(p, s);
-  if (p.cluster == 2) return launch<2>(p, s);
-  return launch<4>(p, s);
+  if (p.cluster == 1) return p.folds > 1 ? launch<1, true>(p, s) : launch<1, false>(p, s);
+  if (p.cluster == 2) return p.folds > 1 ? launch<2, true>(p, s) : launch<2, false>(p, s);
+  return p.folds > 1 ? launch<4, true>(p, s) : launch<4, false>(p, s);
 }
 
 }  // namespace muon
