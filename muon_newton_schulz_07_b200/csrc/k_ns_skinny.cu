@@ -37,6 +37,11 @@
 // the row by the exact diagonal entry over the rounded one, which takes a third off the error
 // of the result (64 x 768, five quintic iterations: 1.9e-3 -> 1.2e-3).
 //
+// Measured, five iterations: 12 of 64 x 768 43 us, 288 of 1536 x 128 (clusters of two) 320 us.  An iteration of 128 x 768
+// a CTA takes 13 k cycles, 7 k of them the six blocks (their MMAs at the rate of the tensor core), 5 k the chain from A to the first
+// block, 1 k the last block's Gram product; a cluster of two adds 6 k for the exchange of A.  Loading, converting
+// and storing a tile is 30 to 45 k once, which one CTA an SM has nothing to hide behind.
+//
 // All waits are bounded; a CTA whose wait runs out records the timeout, stops its work, and still
 // takes every barrier of the schedule.
 #include <algorithm>
