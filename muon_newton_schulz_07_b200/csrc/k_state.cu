@@ -167,12 +167,14 @@ __device__ __forceinline__ int unit_lane() { return threadIdx.x % LANES; }
 constexpr uint32_t UNITS = THREADS / LANES;  // of a pass
 
 // Where the units of this thread's 16 lanes are, one a pass.  LINEAR: rows are whole blocks and every
-// side is contiguous, so unit i of a matrix is its values 128 i .. everywhere; a pass is a constant
-// further on, and passes beyond the matrix work on its last unit again without storing.  Otherwise
-// the row and column of a unit: one division, then steps.
+// side is contiguous, so unit i of a matrix is its values 128 i .. everywhere, and a pass is a constant further
+// on: one address a side, computed once (computed for each pass they were a sixth of the instructions,
+// which bound the kernels that round stochastically).  Otherwise the row and column of a unit: one division, then
+// steps.
 template <bool LINEAR>
 struct Sites {
   uint32_t unit0, total;                        // LINEAR
+  long long code0, scale0;                      // LINEAR, of pass 0
   int row[LINEAR ? 1 : PASSES], col[LINEAR ? 1 : PASSES], vals[LINEAR ? 1 : PASSES];
   const StateSeg& s;
   const Cta& c;
@@ -180,6 +182,8 @@ struct Sites {
     unit0 = cta.first + threadIdx.x / LANES;  // below 2^31 + 64
     if (LINEAR) {
       total = static_cast<uint32_t>(s.rows) * s.blocks;
+      scale0 = static_cast<long long>(c.e) * total + unit0;
+      code0 = scale0 * kStateBlock;  // (rows are whole blocks)
       return;
     }
     uint32_t r = unit0 / static_cast<uint32_t>(s.blocks), block = unit0 - r * s.blocks;
@@ -197,25 +201,26 @@ struct Sites {
       }
     }
   }
-  __device__ __forceinline__ uint32_t unit(int q) const { return min(unit0 + q * UNITS, total - 1); }
+  static constexpr int kPass = UNITS * kStateBlock;  // LINEAR: values from one pass to the next
   // values of the unit that exist (0: beyond the matrix)
   __device__ __forceinline__ int have(int q) const {
     return LINEAR ? (unit0 + q * UNITS < total ? kStateBlock : 0) : vals[LINEAR ? 0 : q];
   }
   // of the unit's first value: within the matrix, in the codes of the stack, and its scale
   __device__ __forceinline__ unsigned long long place_of(int q) const {
-    return LINEAR ? static_cast<unsigned long long>(unit(q)) * kStateBlock
+    return LINEAR ? static_cast<unsigned long long>(unit0) * kStateBlock + q * kPass
                   : static_cast<unsigned long long>(row[LINEAR ? 0 : q]) * s.cols + col[LINEAR ? 0 : q];
   }
   __device__ __forceinline__ long long code_at(int q) const {
-    return static_cast<long long>(c.e) * s.rows * s.cols + place_of(q);
+    return LINEAR ? code0 + q * kPass : static_cast<long long>(c.e) * s.rows * s.cols + place_of(q);
   }
   __device__ __forceinline__ long long scale_at(int q) const {
-    return static_cast<long long>(c.e) * s.rows * s.blocks +
-           (LINEAR ? unit(q) : static_cast<long long>(row[LINEAR ? 0 : q]) * s.blocks + col[LINEAR ? 0 : q] / kStateBlock);
+    return LINEAR ? scale0 + q * static_cast<int>(UNITS)
+                  : static_cast<long long>(c.e) * s.rows * s.blocks +
+                        (static_cast<long long>(row[LINEAR ? 0 : q]) * s.blocks + col[LINEAR ? 0 : q] / kStateBlock);
   }
   __device__ __forceinline__ long long value_at(int q, long long ld, long long bs) const {
-    return LINEAR ? c.e * bs + static_cast<long long>(unit(q)) * kStateBlock
+    return LINEAR ? c.e * bs + static_cast<long long>(unit0) * kStateBlock + q * kPass
                   : c.e * bs + row[LINEAR ? 0 : q] * ld + col[LINEAR ? 0 : q];
   }
   template <typename T>
@@ -294,12 +299,12 @@ struct TypeOf<__half> { static constexpr int id = kViewF16; };
 template <bool LINEAR, typename T>
 __device__ __forceinline__ void load_values(const T* base, bool vec, int have, Eight<T>& x) {
   const int lane = unit_lane();
-  if (LINEAR) {
-    x.load(base + lane * 8);
-    return;
-  }
 #pragma unroll
   for (int i = 0; i < static_cast<int>(sizeof(x) / 4); ++i) reinterpret_cast<uint32_t*>(&x)[i] = 0;
+  if (LINEAR) {
+    if (have > 0) x.load(base + lane * 8);
+    return;
+  }
   if (vec) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -382,7 +387,8 @@ __device__ __forceinline__ void write_units(const Sites<LINEAR>& at, bool vec, u
     if (STOCHASTIC) {
       const unsigned long long first = at.place_of(q);
       if (LINEAR) {  // eight neighbours from an even place: four pairs
-        const uint32_t counter = pair_counter(key, (first + lane * 8) / 2);  // (a multiple of 4: no carry below)
+        // (A CTA's pairs are 4096 neighbours from a multiple of that: their upper 32 bits are the same.)
+        const uint32_t counter = pair_counter(key, (at.place_of(0) + lane * 8) / 2) + q * (Sites<LINEAR>::kPass / 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] = mixed(counter + i);
       } else if (vec) {
@@ -428,11 +434,13 @@ __device__ __forceinline__ void load_codes(const Sites<LINEAR>& at, int q, bool 
   const int lane = unit_lane(), have = at.have(q);
   const uint8_t* p = static_cast<const uint8_t*>(at.s.codes) + at.code_at(q);
   c.w[0] = c.w[1] = 0;
-  c.scale = LINEAR || have > 0 ? at.s.scales[at.scale_at(q)] : 0.0f;
+  c.scale = have > 0 ? at.s.scales[at.scale_at(q)] : 0.0f;
   if (LINEAR) {
-    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p + lane * 8));
-    c.w[0] = v.x;
-    c.w[1] = v.y;
+    if (have > 0) {
+      const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p + lane * 8));
+      c.w[0] = v.x;
+      c.w[1] = v.y;
+    }
   } else if (vec) {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
