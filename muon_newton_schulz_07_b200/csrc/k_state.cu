@@ -17,8 +17,8 @@
 //
 // All three are bound by memory traffic (bf16: 3.03 bytes a value to write, 3.03 to read back, 6.06
 // for the momentum) or, with stochastic rounding, by the integer and logic pipe.  Measured with 226 M bf16
-// values: read back 101 us (6.8 TB/s, the rate of a copy), written as e4m3 with stochastic rounding 233 us,
-// momentum on int8 with it 364 us (3.8 TB/s); to nearest, 57 M values as int8 38 us (4.5 TB/s).  A unit is one block of one row, 16 lanes of 8 values; consecutive units are
+// values: read back 101 us (6.8 TB/s, the rate of a copy), written as e4m3 with stochastic rounding 193 us,
+// momentum on int8 with it 312 us (4.4 TB/s); to nearest, 57 M values as int8 38 us (4.5 TB/s).  A unit is one block of one row, 16 lanes of 8 values; consecutive units are
 // consecutive in memory, so a CTA of 64 units streams up to 8192 contiguous values whatever the
 // row length, and a thread has the loads of all four of its units in flight before it computes.
 // Rows that are not whole blocks back to back interleave the 16 lanes instead, four values each where
