@@ -62,6 +62,7 @@ class HParams(ctypes.Structure):
 # Packed rather than ctypes structures: a call on a small matrix is bounded by what the host does for it.
 _View = struct.Struct("Pqqqqi4x")   # muon_view_t: data, count, batch_stride, row_stride, col_stride, dtype
 _State = struct.Struct("PPqqq")     # muon_state_t: codes, scales, count, rows, cols
+pack_view, pack_state = _View.pack, _State.pack
 
 
 _lib = None

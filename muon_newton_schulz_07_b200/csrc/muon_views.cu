@@ -436,8 +436,8 @@ cudaError_t enqueue_tiles(muon_ctx* h, const std::vector<Item>& items, const muo
 // ranges of at least 64 each is cut, and the fewest CTAs that hold them, by what the waves of tiles would take.
 // Measured, an iteration of a tile takes about 7 k cycles for the A -> B' chain, 6 k more to add up
 // the A of a cluster, 2.7 k more to add up column ranges, and 1.6 k for each 128 columns (1.15 k in the
-// update, the rest its share of loading and storing the tile): 12 of 64 x 768 take 45 us in two ranges and
-// 47 in one, 9 of 25 x 626 51 us in four and 83 in one.
+// update, the rest its share of loading and storing the tile): 12 of 64 x 768 take 43 us in two ranges and
+// 51 in one, 9 of 25 x 626 51 us in four and 83 in one.
 void skinny_layout(const GroupPlan& gp, int cnt, int num_sms, SkinnyParams* p) {
   p->m = gp.m;
   p->n = gp.n;

@@ -43,8 +43,8 @@ def _views(tensors, entries, device, name, dtype=None, by_rows=False):
         if cs != 1 and cols != 1 and (by_rows or not (rs == 1 or rows == 1)):
             raise ValueError(f"{name}: a tensor of strides {st} is not stored by rows"
                              + ("" if by_rows else " or by columns"))
-        out.append((t.data_ptr(), count, bs, rs, cs, _VIEW_TYPES[dt]))
-    return B.views(out)
+        out.append(B.pack_view(t.data_ptr(), count, bs, rs, cs, _VIEW_TYPES[dt]))
+    return b"".join(out)
 
 
 def _device(device):
@@ -82,17 +82,17 @@ class QuantizedState:
         if fmt not in self.FORMATS:
             raise ValueError(f"fmt must be one of {sorted(self.FORMATS)}")
         self.fmt = fmt
-        self._fmt, code = self.FORMATS[fmt]
+        self._fmt, self._type = self.FORMATS[fmt]
         self._entries = _entries(shapes)
         self.shapes = [e[3] for e in self._entries]
         self._scale_shapes = [s[:-1] + (-(-s[-1] // self.BLOCK),) for s in self.shapes]
         self.device = dev = _device(device)
-        self.codes = [torch.zeros(s, dtype=torch.uint8, device=dev).view(code) for s in self.shapes]
+        self.codes = [torch.zeros(s, dtype=torch.uint8, device=dev).view(self._type) for s in self.shapes]
         self.scales = [torch.zeros(s, dtype=torch.float32, device=dev) for s in self._scale_shapes]
 
     def _states(self):
         out = []
-        code, device = self.FORMATS[self.fmt][1], self.device
+        code, device = self._type, self.device
         for q, s, (count, rows, cols, shape), scales in zip(self.codes, self.scales, self._entries, self._scale_shapes,
                                                              strict=True):
             if q.shape != shape or q.dtype is not code or q.device != device or not q.is_contiguous():
@@ -101,8 +101,8 @@ class QuantizedState:
             if s.shape != scales or s.dtype is not torch.float32 or s.device != device or not s.is_contiguous():
                 raise ValueError(f"scales: tensor {tuple(s.shape)} {s.dtype} {s.device} does not match {shape}, a scale "
                                  f"for {self.BLOCK} columns, torch.float32 {self.device} (contiguous)")
-            out.append((q.data_ptr(), s.data_ptr(), count, rows, cols))
-        return B.states(out)
+            out.append(B.pack_state(q.data_ptr(), s.data_ptr(), count, rows, cols))
+        return b"".join(out)
 
     def _side(self, tensors, name):
         if len(tensors) > 1 and any(t.dtype is not tensors[0].dtype for t in tensors):
@@ -120,7 +120,7 @@ class QuantizedState:
                    _stream(self.device, stream))
 
     def _call(self, f, *args):
-        if torch.cuda.current_device() == self.device.index:
+        if torch._C._cuda_getDevice() == self.device.index:
             f(*args)
         else:  # the library launches on the current device
             with torch.cuda.device(self.device):
