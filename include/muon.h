@@ -131,8 +131,10 @@ MUON_API muon_status_t muon_workspace_size(const muon_shape_t* shapes, int n, mu
  * Build a handle for a fixed parameter set.
  *   shapes:    host array of n shapes (copied).
  *   workspace: device pointer, 1024-byte aligned, ws_bytes >= muon_workspace_size().
- *              It is zero-filled here (synchronously, on the legacy default stream
- *              semantics of cudaMemset) and must outlive the handle.
+ *              It is zero-filled here, on the legacy default stream, and the call
+ *              returns once that is done: the handle may be used on any stream at
+ *              once.  No earlier work on any stream may still use that memory.  It
+ *              must outlive the handle.
  * Uses the current CUDA device, which must be sm_100 (B200).  The handle is
  * bound to that device.
  */

@@ -841,7 +841,9 @@ muon_status_t muon_create(muon_handle_t* handle, const muon_shape_t* shapes, int
   h->d_scal = reinterpret_cast<float*>(h->ws + h->plan.off_scal);
   h->d_partials = reinterpret_cast<float*>(h->ws + h->plan.off_partials);
   h->d_norms = reinterpret_cast<float*>(h->ws + h->plan.off_norms);
-  if (cudaMemset(workspace, 0, h->plan.total) != cudaSuccess) {
+  // cudaMemset of device memory does not wait for the fill, and a stream created non-blocking does not wait for
+  // the default stream: without the second call the handle's first work there could meet the fill.
+  if (cudaMemset(workspace, 0, h->plan.total) != cudaSuccess || cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
     cudaGetLastError();
     delete h;
     return MUON_ERR_CUDA;

@@ -158,6 +158,8 @@ class MuonStep:
             self._ws = torch.empty(nbytes + 1024, dtype=torch.uint8, device=self.device)
             base = self._ws.data_ptr()
             self._ws_ptr = (base + 1023) // 1024 * 1024
+            # the block may be one that this stream's earlier work still uses; muon_create fills it on another stream
+            torch.cuda.current_stream(self.device).synchronize()
             self.handle = B.muon_create(matrices, self._dt, self._mode, self._ws_ptr, nbytes)
         self.n_groups, _ = B.muon_get_plan(self.handle, 5)
         if schedule != "auto":

@@ -1,0 +1,91 @@
+"""What a handle keeps in its workspace between calls: the fill at its creation against work on other streams.
+
+The results are compared bit for bit with those of a handle that nothing ran beside.
+"""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from muon_newton_schulz_07_b200 import binding as B
+from muon_newton_schulz_07_b200.optimizer import MuonStep, QuantizedState
+
+pytestmark = pytest.mark.gpu
+
+SHAPES = [(3, 64, 96), (300, 256), (2, 512, 768)]
+
+
+def values(shape, seed, dtype=torch.bfloat16):
+    gen = torch.Generator().manual_seed(seed)
+    return (1e-2 * torch.randn(shape, generator=gen)).to("cuda", dtype)
+
+
+def tensors():
+    """W, G, U and a state of one set of values."""
+    G = [values(s, 10 + i) for i, s in enumerate(SHAPES)]
+    state = QuantizedState(SHAPES)
+    state.write([values(s, 20 + i) for i, s in enumerate(SHAPES)])
+    return [values(s, 30 + i) for i, s in enumerate(SHAPES)], G, [torch.empty_like(g) for g in G], state
+
+
+def calls(op, W, G, U, state):
+    """Momentum, a step and the orthogonaliser, twice: everything that they write, the norms with it."""
+    out = []
+    for t in range(2):
+        out.append(op.momentum(G, state, U, seed=2 * t))
+        out += [u.clone() for u in U]
+        op(W, G, state, seed=2 * t + 1)
+        out += [op.norms()] + [w.clone() for w in W]
+        op.orthogonalize(G, U)
+        out += [op.norms()] + [u.clone() for u in U]
+    return out + [q.clone() for q in state.codes] + [s.clone() for s in state.scales]
+
+
+def same(a, b):
+    return all(torch.equal(x, y) for x, y in zip(a, b, strict=True))
+
+
+def alone():
+    op = MuonStep(SHAPES, mode="half")
+    got = calls(op, *tensors())
+    torch.cuda.synchronize()
+    assert op.status() == B.MUON_OK
+    op.close()
+    return got
+
+
+def test_a_handle_made_while_the_default_stream_is_busy():
+    """The workspace is filled before muon_create returns, whatever else the device has to do."""
+    want = alone()
+    made = tensors()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)                      # a tenth of a second on the default stream
+    with torch.cuda.stream(side):
+        op = MuonStep(SHAPES, mode="half")
+        got = calls(op, *made)
+    torch.cuda.synchronize()
+    assert op.status() == B.MUON_OK
+    assert same(got, want)
+    op.close()
+
+
+def test_a_workspace_whose_block_is_still_in_use():
+    """A block that the allocator hands over may still be written by the stream it comes from."""
+    want = alone()
+    nbytes = B.muon_workspace_size([(s[-2], s[-1]) for s in SHAPES for _ in range(s[0] if len(s) == 3 else 1)],
+                                   B.MUON_BF16, B.MUON_MODE_HALF) + 1024
+    made = tensors()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        before = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+        torch.cuda._sleep(200_000_000)
+        before.fill_(1)
+        del before
+        op = MuonStep(SHAPES, mode="half")
+        got = calls(op, *made)
+    torch.cuda.synchronize()
+    assert op.status() == B.MUON_OK
+    assert same(got, want)
+    op.close()
