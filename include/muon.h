@@ -287,7 +287,7 @@ MUON_API muon_status_t muon_adamw_step(void* const* P, const void* const* G, flo
 MUON_API muon_status_t muon_get_norms(muon_handle_t handle, float* dst, cudaStream_t stream);
 
 /*
- * Synchronise `stream`, read the device status word of the handle and clear it.
+ * Synchronise `stream`, read the device status word of the handle and clear it (on `stream` too).
  * Returns MUON_OK, MUON_ERR_TIMEOUT or MUON_ERR_DEVICE_STATUS (device fault
  * recorded since the last call), or MUON_ERR_CUDA if the stream reported an error.
  */

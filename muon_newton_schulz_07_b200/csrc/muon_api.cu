@@ -928,11 +928,15 @@ muon_status_t muon_get_norms(muon_handle_t h, float* dst, cudaStream_t stream) {
 muon_status_t muon_get_status(muon_handle_t h, cudaStream_t stream) {
   if (h == nullptr) return MUON_ERR_INVALID_ARG;
   DeviceGuard guard(h->device);
-  if (cudaStreamSynchronize(stream) != cudaSuccess) return MUON_ERR_CUDA;
+  // All on `stream`, and done on return: a clear on the default stream could come after the handle's next call.
   unsigned int code = 0;
-  if (cudaMemcpy(&code, h->d_status, sizeof(code), cudaMemcpyDeviceToHost) != cudaSuccess) return MUON_ERR_CUDA;
+  if (cudaMemcpyAsync(&code, h->d_status, sizeof(code), cudaMemcpyDeviceToHost, stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return MUON_ERR_CUDA;
   if (code == 0) return MUON_OK;
-  if (cudaMemset(h->d_status, 0, sizeof(code)) != cudaSuccess) return MUON_ERR_CUDA;
+  if (cudaMemsetAsync(h->d_status, 0, sizeof(code), stream) != cudaSuccess ||
+      cudaStreamSynchronize(stream) != cudaSuccess)
+    return MUON_ERR_CUDA;
   return code == kDevTimeout ? MUON_ERR_TIMEOUT : MUON_ERR_DEVICE_STATUS;
 }
 

@@ -89,3 +89,22 @@ def test_a_workspace_whose_block_is_still_in_use():
     assert op.status() == B.MUON_OK
     assert same(got, want)
     op.close()
+
+
+def test_status_is_read_and_cleared_on_its_own_stream():
+    op = MuonStep(SHAPES, mode="half")
+    side = torch.cuda.Stream()
+    B.muon_selftest_timeout(op.handle, 10_000, side.cuda_stream)    # a kernel's first launch loads it, which waits for the device
+    assert op.status(side) == B.MUON_ERR_TIMEOUT
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)
+    busy = torch.cuda.Event()
+    busy.record()
+    assert op.status(side) == B.MUON_OK
+    for _ in range(3):                                  # recorded, read, cleared: and recorded again right after
+        B.muon_selftest_timeout(op.handle, 10_000, side.cuda_stream)
+        assert op.status(side) == B.MUON_ERR_TIMEOUT
+    assert op.status(side) == B.MUON_OK
+    assert not busy.query()                             # without a wait for the default stream
+    torch.cuda.synchronize()
+    op.close()
