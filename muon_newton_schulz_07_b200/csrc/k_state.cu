@@ -574,11 +574,10 @@ __global__ void __launch_bounds__(THREADS, !LINEAR || sizeof(T) == 2 ? 3 : 1)
   if (PASS == kPassStep) return;
   ss = block_sum(ss, red);
   if (threadIdx.x == 0) p.partials[blockIdx.x] = ss;
-  // The last CTA of a matrix adds its parts, in a fixed order.  The count wraps to 0 for the next call.
+  // The last CTA of a matrix adds its parts, in a fixed order.
   if (threadIdx.x == 0) {
     __threadfence();
-    last = atomicInc(p.arrivals + s.caller_idx + c.e, static_cast<unsigned>(s.unit_ctas) - 1u) ==
-           static_cast<unsigned>(s.unit_ctas) - 1u;
+    last = atomicAdd(p.arrivals + s.caller_idx + c.e, 1u) == static_cast<unsigned>(s.unit_ctas) - 1u;
   }
   __syncthreads();
   if (!last) return;

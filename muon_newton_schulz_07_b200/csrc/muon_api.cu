@@ -109,10 +109,10 @@ void make_plan(const muon_shape_t* shapes, int n, muon_mode_t mode, Plan* P) {
   size_t off = 0;
   P->off_status = off;
   off = align_up(off + 64, 1024);
-  P->off_arrivals = off;  // CTAs of each matrix that have finished (the 8-bit momentum's norms); zero between calls
-  off = align_up(off + sizeof(unsigned int) * static_cast<size_t>(n), 1024);
-  // the single-launch schedule's completion counters, [3 k][n] for k up to 64
-  P->off_deps = off;
+  // Counters, cleared on the stream of each call that uses them (clear_counters): CTAs of each matrix that have
+  // added to its norm, then the single-launch schedule's completion counters, [3 k][n] for k up to 64
+  P->off_arrivals = off;
+  P->off_deps = off + sizeof(unsigned int) * static_cast<size_t>(n);
   off = align_up(P->off_deps + sizeof(unsigned int) * 3 * 64 * static_cast<size_t>(n), 1024);
   P->off_scal = off;
   off = align_up(off + sizeof(float) * 2 * n, 1024);
@@ -236,6 +236,10 @@ void muon::trace_call_end(muon_ctx* h) {
   if (h->prof_steps_left > 0) --h->prof_steps_left;
 }
 
+cudaError_t muon::clear_counters(const muon_ctx* h, int k, cudaStream_t st) {
+  return cudaMemsetAsync(h->ws + h->plan.off_arrivals, 0, sizeof(unsigned int) * (1 + 3 * k) * static_cast<size_t>(h->n), st);
+}
+
 // One group's part of a staged launch.
 void muon::stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur, int nxt, int tw, TcGroup* G) {
   G->cnt = gp.cnt;
@@ -351,7 +355,7 @@ cudaError_t enqueue_front(muon_ctx* h, const void* const* src, void* const* mom,
   cudaError_t e = cudaSuccess;
   if (fused_schedule(h, hp->ns_steps)) {
     // the single-launch schedule's stage completion counters start at zero
-    e = cudaMemsetAsync(h->ws + P.off_deps, 0, sizeof(unsigned int) * 3 * hp->ns_steps * static_cast<size_t>(h->n), st);
+    e = clear_counters(h, hp->ns_steps, st);
     if (e != cudaSuccess) return e;
   }
   trace(h, -1, st);  // start of the traced kernel sequence of this call

@@ -100,6 +100,10 @@ namespace muon {
 bool hp_ok(const muon_hparams_t* hp, bool need_momentum);
 void trace(muon_ctx* h, int kind, cudaStream_t st);
 void trace_call_end(muon_ctx* h);
+// Zero the counters that a call uses, in stream order before its kernels: the arrivals, and the completion
+// counters of a single launch of k iterations (0: none).  What an earlier call left behind, one that overlapped another
+// on the handle for instance, does not reach this one.
+cudaError_t clear_counters(const muon_ctx* h, int k, cudaStream_t st);
 // One group's part of a staged Newton-Schulz launch (operands, output, tile counts; tile_begin is
 // the caller's), from X buffer `cur` to `nxt`, Update tiles `tw` wide.
 void stage_group(const muon_ctx* h, const GroupPlan& gp, int kind, int cur, int nxt, int tw, TcGroup* G);

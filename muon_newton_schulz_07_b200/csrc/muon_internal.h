@@ -362,7 +362,7 @@ struct StateParams {
   float* partials;       // momentum: one sum of squares per CTA
   float eps;             // momentum, kPassStep
   float* norms;          // momentum: each matrix's last CTA puts its norm there
-  unsigned int* arrivals;  // CTAs of each matrix that have, zero between calls
+  unsigned int* arrivals;  // CTAs of each matrix that have left their part, zero before the call's first launch
 };
 cudaError_t launch_state_quantize(const StateParams& p, StateFormat f, cudaStream_t s);
 cudaError_t launch_state_dequantize(const StateParams& p, StateFormat f, cudaStream_t s);

@@ -340,9 +340,7 @@ cudaError_t enqueue_single(muon_ctx* h, const std::vector<Item>& items, const mu
   NvtxRange range("muon: Newton-Schulz, every iteration in one launch");
   const std::vector<const GroupPlan*> groups = tiled_groups(h);
   const int k = hp->ns_steps;
-  char* deps = h->ws + h->plan.off_deps;  // completion counters, zero before the launch
-  cudaError_t e = cudaMemsetAsync(deps, 0, sizeof(unsigned int) * 3 * k * static_cast<size_t>(h->n), st);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
   NsParams& q = h->ns;
   fused_tables(groups, h->n, k, fuse, wide_pays(h, groups), h->num_sms / 2, &q);
   fused_maps(groups, &q);
@@ -350,7 +348,7 @@ cudaError_t enqueue_single(muon_ctx* h, const std::vector<Item>& items, const mu
   fill_iterations(h, hp, &q);
   q.scal = h->d_scal;
   q.status = h->d_status;
-  q.deps = reinterpret_cast<unsigned int*>(deps);
+  q.deps = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_deps);  // zero: clear_counters
   q.timeout_ns = kTimeoutNs;
   if (fuse) fill_results(h, items, hp, store, &q);
   if (h->schedule != MUON_SCHEDULE_SPLIT) {
@@ -506,12 +504,19 @@ cudaError_t enqueue_skinny(muon_ctx* h, const std::vector<Item>& items, const mu
   return cudaSuccess;
 }
 
+// Whether the workspace groups' iterations count completed tiles (enqueue_single), and of how many iterations.
+int counted_iterations(const muon_ctx* h, int k) {
+  return !tiled_groups(h).empty() && !small_tiles(h, k) && single_launch(h, k) ? k : 0;
+}
+
 // From sources in the caller's layout to the results.  `normalised`: the sources are 2^12 X already.
 cudaError_t half_run(muon_ctx* h, std::vector<Item>& items, const muon_hparams_t* hp, bool store, bool normalised,
                      cudaStream_t st) {
   const int k = hp->ns_steps;
   cudaError_t e = cudaSuccess;
   if (!normalised) {
+    const int counted = counted_iterations(h, k);
+    if (counted > 0) e = clear_counters(h, counted, st);
     // view_sumsq_kernel writes partial sums, one a tile, where view_orient_kernel looks for them
     int at = 0;
     for (Item& it : items) {
@@ -520,7 +525,7 @@ cudaError_t half_run(muon_ctx* h, std::vector<Item>& items, const muon_hparams_t
       it.part_begin = at;
       at += it.parts * it.count;
     }
-    e = view_pass(h, items, kSumsq, hp, store, normalised, 0, st);
+    if (e == cudaSuccess) e = view_pass(h, items, kSumsq, hp, store, normalised, 0, st);
   }
   if (e == cudaSuccess) e = view_pass(h, items, kOrient, hp, store, normalised, 0, st);
   const bool fuse = result_fusable(h, items, k);
@@ -722,7 +727,8 @@ void stage(muon_ctx* h, int mat, int count, Item* item, Rows* rows) {
 
 cudaError_t run_step(muon_ctx* h, std::vector<Item>& items, const std::vector<MomentumIn>& in, StateFormat f,
                      const muon_hparams_t* hp, const uint32_t* seed, cudaStream_t st) {
-  cudaError_t e = momentum_pass(h, in, f, kPassNorm, hp, nullptr, st);
+  cudaError_t e = clear_counters(h, counted_iterations(h, hp->ns_steps), st);
+  if (e == cudaSuccess) e = momentum_pass(h, in, f, kPassNorm, hp, nullptr, st);
   if (e == cudaSuccess) e = momentum_pass(h, in, f, kPassStep, hp, seed, st);
   if (e == cudaSuccess) e = half_run(h, items, hp, false, true, st);
   return e;
@@ -896,7 +902,8 @@ muon_status_t muon_momentum_state(muon_handle_t h, const muon_view_t* G, const m
     if (!apart(ins, outs) || !states_distinct(S, n)) return MUON_ERR_INVALID_ARG;
     DeviceGuard guard(h->device);
     trace(h, -1, stream);
-    const cudaError_t e = momentum_pass(h, in, format_of(format), kPassMomentum, hp, seed, stream);
+    cudaError_t e = clear_counters(h, 0, stream);
+    if (e == cudaSuccess) e = momentum_pass(h, in, format_of(format), kPassMomentum, hp, seed, stream);
     trace_call_end(h);
     return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
   });

@@ -1,4 +1,5 @@
-"""What a handle keeps in its workspace between calls: the fill at its creation against work on other streams.
+"""What a handle keeps in its workspace between calls: the fill at its creation against work on other streams, counters that an
+earlier call left behind, the status word.
 
 The results are compared bit for bit with those of a handle that nothing ran beside.
 """
@@ -107,4 +108,49 @@ def test_status_is_read_and_cleared_on_its_own_stream():
     assert op.status(side) == B.MUON_OK
     assert not busy.query()                             # without a wait for the default stream
     torch.cuda.synchronize()
+    op.close()
+
+
+def spoil(op):
+    """Everything in a handle's workspace but the status word, as a call that overlapped another might leave the counters."""
+    at = op._ws_ptr - op._ws.data_ptr()
+    op._ws[at + 1024:at + op.workspace_bytes].fill_(0x11)
+
+
+@pytest.mark.parametrize("schedule", ["auto", "staged", "fused"])
+def test_what_a_call_leaves_behind_does_not_reach_the_next(schedule):
+    want = alone()
+    op = MuonStep(SHAPES, mode="half", schedule=schedule)
+    spoil(op)
+    assert same(calls(op, *tensors()), want)
+    W, G, U, state = tensors()
+    V = [torch.empty_like(u) for u in U]
+    op.orthogonalize(G, V)
+    for call in (lambda: op.momentum(G, state, U, seed=1), lambda: op(W, G, state, seed=2), lambda: op.orthogonalize(G, U)):
+        spoil(op)
+        call()
+    assert same(U, V)
+    assert op.status() == B.MUON_OK
+    op.close()
+
+
+def test_a_captured_call_clears_its_counters():
+    op = MuonStep(SHAPES, mode="half")
+    want = alone()
+    made, back = tensors(), tensors()
+    W, G, U, state = made
+    for _ in range(2):
+        calls(op, *made)                                # (what a capture may not load)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls(op, *made)
+    for _ in range(2):
+        for a, b in zip(W + state.codes + state.scales, back[0] + back[3].codes + back[3].scales):
+            a.copy_(b)
+        spoil(op)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert same(got, want)
+    assert op.status() == B.MUON_OK
+    del graph
     op.close()
