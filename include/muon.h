@@ -316,31 +316,6 @@ MUON_API const char* muon_status_string(muon_status_t status);
 MUON_API muon_status_t muon_get_plan(muon_handle_t handle, int ns_steps, int* n_groups, int* launches_per_step);
 
 /*
- * How the k Newton-Schulz iterations of a MUON_MODE_FAST handle are launched.
- *   MUON_SCHEDULE_STAGED  one tensor-core launch per stage and iteration (3 k
- *                         launches: Gram, polynomial, update), each over every
- *                         matrix of the handle.
- *   MUON_SCHEDULE_FUSED   all 3 k stages in one persistent launch: the tiles of
- *                         every stage form one list, and a tile waits (on the
- *                         device, bounded) only until the stage it reads is
- *                         complete for its own matrix, so the stages of different
- *                         matrices overlap and no launch boundary drains the GPU.
- *                         Same arithmetic and rounding as STAGED (results are
- *                         bitwise equal).  Needs at most 6 distinct shape groups.
- *   MUON_SCHEDULE_SPLIT   the tiles of FUSED, one launch per stage (3 k launches):
- *                         separates the single-launch kernel's tile machinery
- *                         from its scheduling, for measurements.
- *   MUON_SCHEDULE_AUTO    (default) FUSED when every shape group's smaller
- *                         dimension is at most 768 (there it measured within 1 %
- *                         of STAGED with one launch per step instead of 3 k),
- *                         else STAGED.
- * The small-matrix kernel (MUON_KERNEL_NS_SMALL) keeps precedence when its
- * conditions hold; FP32_REF handles always run staged.  Returns
- * MUON_ERR_UNSUPPORTED if FUSED is asked of a handle that cannot run it.
- * The setting applies to later calls; it must not change while a captured graph
- * of the handle is replayed.
- */
-/*
  * Host-only consistency check of the launch tables muon_step would build for
  * these shapes on a device with num_sms SMs (no device needed): the persistent
  * momentum/norm kernel's tile ranges and partial-sum slots, and the single-launch
@@ -353,6 +328,35 @@ MUON_API muon_status_t muon_get_plan(muon_handle_t handle, int ns_steps, int* n_
 MUON_API muon_status_t muon_check_plan(const muon_shape_t* shapes, int n, int ns_steps, int num_sms,
                                        int64_t* problems);
 
+/*
+ * How the k Newton-Schulz iterations of a MUON_MODE_FAST or MUON_MODE_HALF handle are launched (in HALF:
+ * of the shape groups that do not run on chip; the conditions below are about those).
+ *   MUON_SCHEDULE_STAGED  one tensor-core launch per stage and iteration (3 k
+ *                         launches: Gram, polynomial, update), each over every
+ *                         matrix of the handle.
+ *   MUON_SCHEDULE_FUSED   all 3 k stages in one persistent launch: the tiles of
+ *                         every stage form one list, and a tile waits (on the
+ *                         device, bounded) only until the stage it reads is
+ *                         complete for its own matrix, so the stages of different
+ *                         matrices overlap and no launch boundary drains the GPU.
+ *                         Same arithmetic and rounding as STAGED (results are
+ *                         bitwise equal).  Needs at most 6 distinct shape groups.
+ *                         Launches of several handles, and other work, may share
+ *                         the GPU: the tiles go to the CTAs that got an SM.
+ *   MUON_SCHEDULE_SPLIT   the tiles of FUSED, one launch per stage (3 k launches):
+ *                         separates the single-launch kernel's tile machinery
+ *                         from its scheduling, for measurements.
+ *   MUON_SCHEDULE_AUTO    (default) FAST: FUSED when every shape group's smaller
+ *                         dimension is at most 768 (there it measured within 1 %
+ *                         of STAGED with one launch per step instead of 3 k),
+ *                         else STAGED.  HALF: FUSED up to eight 256 x 256 Update
+ *                         tiles for each pair of SMs, else STAGED.
+ * The small-matrix kernel (MUON_KERNEL_NS_SMALL) keeps precedence when its
+ * conditions hold; FP32_REF handles always run staged.  Returns
+ * MUON_ERR_UNSUPPORTED if FUSED is asked of a handle that cannot run it.
+ * The setting applies to later calls; it must not change while a captured graph
+ * of the handle is replayed.
+ */
 #define MUON_SCHEDULE_AUTO 0
 #define MUON_SCHEDULE_STAGED 1
 #define MUON_SCHEDULE_FUSED 2

@@ -20,8 +20,14 @@
 // A stage that waits for every tile of its matrix's previous stage also orders all
 // write-after-read reuse of the buffers (A, B', the two X buffers).  Since a pair works through
 // its tiles in list order and a tile only waits for tiles earlier in the list, the earliest
-// unfinished tile can always proceed: with every pair resident (the grid never exceeds the
-// clusters that fit at once) the launch cannot deadlock, and every wait is bounded anyway.
+// unfinished tile can always proceed, provided that every pair with tiles is running.  So the list is
+// dealt to the pairs that have come: each takes a number as it starts, and the last one of the grid, or
+// one that has waited 100 us for it (other work on the GPU may hold SMs for as long as it likes),
+// closes the round at the numbers given out.  Pairs that come later find it closed and leave.  No launch
+// depends on an SM that it has not got (and every wait is bounded anyway).  The numbers are taken while the
+// CTAs set up, at no cost that shows (7 of 331 x 1003, fp32, five iterations: 157 us a call); pairs that claimed tile after
+// tile from a counter took longer (165; 48 of 768 x 768 628 for 616), since a stage of few tiles then gave some
+// of them two and others none.
 //
 // The per-tile machinery is that of the staged kernel (CTA pairs with tcgen05.mma.cta_group::2,
 // TMA operand ring without multicast, upper blocks only for the symmetric A and B', MN-major
@@ -78,7 +84,7 @@ struct FLayout {
   static_assert(EPI_F32_BYTES <= EPI_WARP_BYTES, "fp32 staging must fit the warp's own block");
   static_assert(SMEM_BYTES <= 232448, "shared memory per CTA");
   static_assert(EPI_AUX_BYTES == EPI_OUT_BYTES, "a chunk of A and its result share a tile");
-  static_assert(2 * NST + 5 + EPI_WARPS <= BAR_BYTES / 8, "barriers must fit their region");
+  static_assert(2 * NST + 6 + EPI_WARPS <= BAR_BYTES / 8, "barriers must fit their region");
 };
 constexpr unsigned int ARRIVALS_PER_TILE = 2 * EPI_WARPS;   // epilogue warps of both CTAs
 static_assert(sizeof(NsParams) <= 32764, "kernel parameters are limited to 32764 bytes");
@@ -192,6 +198,36 @@ __device__ __forceinline__ void mma_slice(uint32_t d_tmem, uint32_t sa, uint32_t
     tc_mma_bf16_pair(d_tmem, adesc0 + astep * j, bdesc0 + bstep * j, idesc, (!first || j != 0) ? 1u : 0u);
 }
 
+// The round of a launch: how many pairs have come (and, in the upper half, how often it was closed), and how many it
+// was closed at.  Writes this pair's number and that.
+__device__ __forceinline__ void join_round(const NsParams& p, uint32_t grid, uint32_t* out) {
+  constexpr unsigned int CLOSED = 0x10000u;  // (grids are far smaller)
+  constexpr unsigned long long PATIENCE_NS = 100000ull;
+  unsigned int* round = p.round;
+  const unsigned int mine = atomicAdd(round, 1u);
+  unsigned int n = 0;
+  if (mine < CLOSED) {
+    bool close = mine == grid - 1;
+    const uint64_t t0 = globaltimer_ns();
+    while ((n = ld_acquire_gpu(round + 1)) == 0) {
+      if (close) {  // the first to do so fixes the number
+        const unsigned int was = atomicAdd(round, CLOSED);
+        if (was < CLOSED) atomicExch(round + 1, was);
+        close = false;
+        continue;
+      }
+      const uint64_t waited = globaltimer_ns() - t0;
+      if (waited > PATIENCE_NS) close = ld_acquire_gpu(round) < CLOSED;
+      if (waited > p.timeout_ns) {
+        record_status(p.status, kDevTimeout);
+        break;
+      }
+    }
+  }
+  out[0] = mine;
+  out[1] = n;
+}
+
 template <bool WR, bool HALF>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     ns_fused_kernel(const __grid_constant__ NsParams p) {
@@ -209,14 +245,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   auto accf_bar = [&](int a) { return bar0 + 8u * (2 * NST + a); };
   auto acce_bar = [&](int a) { return bar0 + 8u * (2 * NST + 2 + a); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * NST + 4);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  auto aux_bar = [&](int w) { return bar0 + 8u * (2 * NST + 5 + w); };
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);  // (then two words: the pair's number, the pairs)
+  auto aux_bar = [&](int w) { return bar0 + 8u * (2 * NST + 6 + w); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();           // 0: issues the MMAs; 1: its peer
-  const int cl = static_cast<int>(cluster_id_x());
-  const int ncl = static_cast<int>(num_clusters_x());
-
   if (threadIdx.x == 0) {
     for (int s = 0; s < NST; ++s) {
       mbar_init(full_bar(s), 1);   // the even CTA's arrive.expect_tx (bytes of both CTAs)
@@ -244,6 +277,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       tma_prefetch_desc(&G.a_st);
     }
   }
+  if (warp == 2 && lane == 0 && rank == 0) join_round(p, num_clusters_x(), tmem_slot + 2);
   if (warp == 1) {
     tmem_alloc_pair(smem_u32(tmem_slot), TMEM_COLS);
     tmem_relinquish_pair();
@@ -253,6 +287,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint64_t tmo = p.timeout_ns;
+  // this pair's number, and the pairs of the launch: its tiles are every ncl-th one
+  const uint32_t joined = map_to_rank(smem_u32(tmem_slot + 2), 0);
+  const int cl = static_cast<int>(ld_cluster_u32(joined)), ncl = static_cast<int>(ld_cluster_u32(joined + 4));
+  const int t_first = cl < ncl ? p.t_begin + cl : p.t_end;
 
   if (warp == 0) {
     if (lane == 0) {
@@ -260,7 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      for (int t = p.t_begin + cl; t < p.t_end && ok; t += ncl) {
+      for (int t = t_first; t < p.t_end && ok; t += ncl) {
         const FTile f = decode(p, t);
         const NsGroup& G = p.g[f.g];
         const unsigned int* dep;
@@ -339,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
       uint32_t uses[2] = {0u, 0u};  // completed uses of each accumulator slot
       int next_slot = 0;
       bool ok = true;
-      for (int t = p.t_begin + cl; t < p.t_end && ok; t += ncl) {
+      for (int t = t_first; t < p.t_end && ok; t += ncl) {
         const FTile f = decode(p, t);
         const NsGroup& G = p.g[f.g];
         const int kblocks = k_slices(G, f.kind);
@@ -445,7 +483,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTcThreads, 1)
     uint32_t uses[2] = {0u, 0u};
     int next_slot = 0;
     bool ok = true;
-    for (int t = p.t_begin + cl; t < p.t_end && ok; t += ncl) {
+    for (int t = t_first; t < p.t_end && ok; t += ncl) {
       const FTile f = decode(p, t);
       const NsGroup& G = p.g[f.g];
       const int nsub = f.tw > TILE ? 2 : 1;
@@ -797,8 +835,7 @@ cudaError_t launch_fused_kind(const NsParams& p, int num_sms, cudaStream_t s) {
   if ((attr_set.load() & bit) == 0) {
     e = cudaFuncSetAttribute(ns_fused_kernel<WR, HALF>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
-    // Every pair must be resident at once (a tile may wait for a tile of any other pair): the
-    // grid never exceeds the clusters of two that fit on the device together.
+    // Clusters of two that fit on the device together: the tiles are dealt to those that come first.
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2 * (num_sms / 2), 1, 1);
     cfg.blockDim = dim3(kTcThreads, 1, 1);

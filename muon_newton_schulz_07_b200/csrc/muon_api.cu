@@ -110,9 +110,11 @@ void make_plan(const muon_shape_t* shapes, int n, muon_mode_t mode, Plan* P) {
   P->off_status = off;
   off = align_up(off + 64, 1024);
   // Counters, cleared on the stream of each call that uses them (clear_counters): CTAs of each matrix that have
-  // added to its norm, then the single-launch schedule's completion counters, [3 k][n] for k up to 64
+  // added to its norm; the CTA pairs of each of the single-launch schedule's launches; its completion counters,
+  // [3 k][n] for k up to 64
   P->off_arrivals = off;
-  P->off_deps = off + sizeof(unsigned int) * static_cast<size_t>(n);
+  P->off_rounds = off + sizeof(unsigned int) * static_cast<size_t>(n);
+  P->off_deps = P->off_rounds + sizeof(unsigned int) * kNsRounds;
   off = align_up(P->off_deps + sizeof(unsigned int) * 3 * 64 * static_cast<size_t>(n), 1024);
   P->off_scal = off;
   off = align_up(off + sizeof(float) * 2 * n, 1024);
@@ -237,7 +239,8 @@ void muon::trace_call_end(muon_ctx* h) {
 }
 
 cudaError_t muon::clear_counters(const muon_ctx* h, int k, cudaStream_t st) {
-  return cudaMemsetAsync(h->ws + h->plan.off_arrivals, 0, sizeof(unsigned int) * (1 + 3 * k) * static_cast<size_t>(h->n), st);
+  return cudaMemsetAsync(h->ws + h->plan.off_arrivals, 0,
+                         sizeof(unsigned int) * ((1 + 3 * k) * static_cast<size_t>(h->n) + kNsRounds), st);
 }
 
 // One group's part of a staged launch.
@@ -566,6 +569,8 @@ cudaError_t enqueue_ns(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st, i
     q.scal = h->d_scal;
     q.status = h->d_status;
     q.deps = reinterpret_cast<unsigned int*>(h->ws + P.off_deps);
+    unsigned int* rounds = reinterpret_cast<unsigned int*>(h->ws + P.off_rounds);
+    q.round = rounds;
     q.timeout_ns = kTimeoutNs;
     if (fuse) {
       q.w_decay = store_only ? 0.0f : 1.0f - hp->lr * hp->weight_decay;
@@ -595,6 +600,7 @@ cudaError_t enqueue_ns(muon_ctx* h, const muon_hparams_t* hp, cudaStream_t st, i
       const int base = it * q.tiles_iter;
       q.t_begin = base + q.begin[L][kind][0];
       q.t_end = base + q.begin[L][kind][q.ngroups];
+      q.round = rounds + 2 * s;
       cudaError_t e = launch_ns_fused(q, h->num_sms, st);
       if (e != cudaSuccess) return e;
       ++*launches;

@@ -41,7 +41,7 @@ struct Plan {
   std::vector<int> mat_group, mat_slot, scal_idx;
   std::vector<int> ew_ntiles;
   std::vector<size_t> off_u;  // MUON_MODE_HALF: a step's normalised direction of each matrix, in the caller's layout
-  size_t off_status, off_arrivals, off_deps, off_scal, off_norms, off_partials;
+  size_t off_status, off_arrivals, off_rounds, off_deps, off_scal, off_norms, off_partials;
   size_t total;
 };
 
@@ -100,8 +100,8 @@ namespace muon {
 bool hp_ok(const muon_hparams_t* hp, bool need_momentum);
 void trace(muon_ctx* h, int kind, cudaStream_t st);
 void trace_call_end(muon_ctx* h);
-// Zero the counters that a call uses, in stream order before its kernels: the arrivals, and the completion
-// counters of a single launch of k iterations (0: none).  What an earlier call left behind, one that overlapped another
+// Zero the counters that a call uses, in stream order before its kernels: the arrivals, the rounds, and the
+// completion counters of a single launch of k iterations (0: none).  What an earlier call left behind, one that overlapped another
 // on the handle for instance, does not reach this one.
 cudaError_t clear_counters(const muon_ctx* h, int k, cudaStream_t st);
 // One group's part of a staged Newton-Schulz launch (operands, output, tile counts; tile_begin is

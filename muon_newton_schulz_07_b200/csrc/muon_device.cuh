@@ -166,6 +166,13 @@ __device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint4 v) {
                : "memory");
 }
 
+// 4 bytes of the shared memory of a CTA of the cluster.
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
 // Make this thread's generic-proxy writes (to any state space, the peer CTA's shared
 // memory included) visible to later async-proxy reads (the tensor core, TMA).
 __device__ __forceinline__ void fence_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }

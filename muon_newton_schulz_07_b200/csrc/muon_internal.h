@@ -116,6 +116,8 @@ struct alignas(64) TcGroup {
 // Largest number of matrices whose parameter write can be fused into the last
 // Update launch (their pointers travel in the kernel parameters).
 constexpr int kTcMaxFused = 1024;
+// Words of NsParams::round for the launches of one call: one, or one per stage of up to 64 iterations.
+constexpr int kNsRounds = 2 * 3 * 64;
 
 struct TcParams {
   TcGroup g[kTcMaxGroups];
@@ -148,7 +150,7 @@ cudaError_t launch_tc_gemm(const TcParams& p, int num_sms, cudaStream_t s);
 // ------------------------------------------------------------------ every iteration in one launch
 // One persistent launch runs all k x {Gram, Poly, Update} stages of every matrix of up to
 // kTcMaxGroups shape groups.  Tiles are listed stage after stage (iteration-major, then
-// Gram / Poly / Update, then group, matrix and tile) and dealt round-robin to the CTA pairs;
+// Gram / Poly / Update, then group, matrix and tile) and dealt round-robin to the CTA pairs that run;
 // before loading a tile, a pair waits (bounded) until the stage the tile reads is complete for
 // its matrix: every epilogue warp that finishes a tile adds 1 to a per (stage, matrix)
 // completion counter in the workspace.
@@ -183,6 +185,7 @@ struct NsParams {
   const float* scal;
   unsigned int* status;
   unsigned int* deps;    // [3 k][nslots] completion counters, zero before the launch
+  unsigned int* round;   // two words: pairs that have come, and how many the tiles are dealt to; zero before the launch
   unsigned long long timeout_ns;
   float w_decay;
   void* wptr[kTcMaxFused];

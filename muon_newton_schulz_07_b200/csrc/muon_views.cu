@@ -348,7 +348,9 @@ cudaError_t enqueue_single(muon_ctx* h, const std::vector<Item>& items, const mu
   fill_iterations(h, hp, &q);
   q.scal = h->d_scal;
   q.status = h->d_status;
-  q.deps = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_deps);  // zero: clear_counters
+  q.deps = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_deps);  // zero, as the rounds: clear_counters
+  unsigned int* rounds = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_rounds);
+  q.round = rounds;
   q.timeout_ns = kTimeoutNs;
   if (fuse) fill_results(h, items, hp, store, &q);
   if (h->schedule != MUON_SCHEDULE_SPLIT) {
@@ -362,6 +364,7 @@ cudaError_t enqueue_single(muon_ctx* h, const std::vector<Item>& items, const mu
     const int it = s / 3, kind = s % 3, L = it == k - 1 ? 1 : 0;
     q.t_begin = it * q.tiles_iter + q.begin[L][kind][0];
     q.t_end = it * q.tiles_iter + q.begin[L][kind][q.ngroups];
+    q.round = rounds + 2 * s;
     e = launch_ns_fused(q, h->num_sms, st);
     if (e != cudaSuccess) return e;
     trace(h, MUON_KERNEL_GRAM + kind, st);
