@@ -499,21 +499,6 @@ __global__ void __launch_bounds__(THREADS, 4) state_dequantize_kernel(const __gr
   }
 }
 
-// The sum over the CTA, in thread 0.
-__device__ __forceinline__ float block_sum(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();  // `red` may be in use
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = 0.0f;
-  if (threadIdx.x == 0) {
-#pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i) t += red[i];
-  }
-  return t;
-}
-
 // Momentum and Nesterov blend of one CTA's units; F = kStateDense keeps m in T.  PASS says what a
 // launch does with u and m1 (see StatePass).
 template <typename T, int F, bool STOCHASTIC, bool LINEAR, int PASS>
@@ -526,7 +511,7 @@ __global__ void __launch_bounds__(THREADS, !LINEAR || sizeof(T) == 2 ? 3 : 1)
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
   const uint32_t key = STOCHASTIC ? matrix_key(p.seed, static_cast<uint32_t>(s.mat_begin + c.e)) : 0u;
-  const float mul = PASS == kPassStep ? normaliser(p.norms[s.caller_idx + c.e], p.eps) : 1.0f;
+  const float mul = PASS == kPassStep ? p.factors[s.caller_idx + c.e] : 1.0f;
   const float beta = p.beta, rest = __fsub_rn(1.0f, p.beta);
   const Sites<LINEAR> at(s, c);
   Eight<T> raw[PASSES];
@@ -572,21 +557,14 @@ __global__ void __launch_bounds__(THREADS, !LINEAR || sizeof(T) == 2 ? 3 : 1)
   }
   if (!DENSE && PASS != kPassNorm) write_units<DENSE ? kStateInt8 : F, STOCHASTIC, LINEAR>(at, vec, key, m);
   if (PASS == kPassStep) return;
-  ss = block_sum(ss, red);
-  if (threadIdx.x == 0) p.partials[blockIdx.x] = ss;
-  // The last CTA of a matrix adds its parts, in a fixed order.
-  if (threadIdx.x == 0) {
-    __threadfence();
-    last = atomicAdd(p.arrivals + s.caller_idx + c.e, 1u) == static_cast<unsigned>(s.unit_ctas) - 1u;
-  }
-  __syncthreads();
-  if (!last) return;
-  __threadfence();
+  ss = block_sum<THREADS>(ss, red);
+  if (!last_to_leave(p.partials + blockIdx.x, ss, p.arrivals + s.caller_idx + c.e, s.unit_ctas, &last)) return;
   const float* part = p.partials + s.cta_begin + c.e * s.unit_ctas;
-  float t = 0.0f;
-  for (int i = threadIdx.x; i < s.unit_ctas; i += THREADS) t += __ldcg(part + i);
-  t = block_sum(t, red);
-  if (threadIdx.x == 0) p.norms[s.caller_idx + c.e] = sqrtf(t);
+  const float norm = sqrtf(block_sum<THREADS>(sum_parts<THREADS>(part, s.unit_ctas), red));
+  if (threadIdx.x == 0) {
+    p.norms[s.caller_idx + c.e] = norm;
+    p.factors[s.caller_idx + c.e] = normaliser(norm, p.eps);
+  }
 }
 
 template <typename T, int F, bool LINEAR>

@@ -1,14 +1,15 @@
 // The ends of the fp16 Newton-Schulz iteration (MUON_MODE_HALF) for matrices that stay where and
 // how the caller holds them: slices of fused weights, stacks, transposed storage, bf16, fp16 or fp32.
 //
-//   view_sumsq_kernel   partial sums of squares, fp32, one per 64 x 128 tile
+//   view_sumsq_kernel   ||x||_F from partial sums of squares, fp32, one per 64 x 128 tile
 //   view_orient_kernel  X0 = 2^12 x / (||x||_F + eps), oriented to min x max, zero-padded, fp16
 //   view_write_kernel   dst = decay dst + coef X_k, oriented back
 //
 // The norm must be known before the first rounding to fp16: gradients reach far below fp16's
 // range, normalised matrices do not.  So the source is read twice; the second read finds it in L2
-// when the set fits (126 MB).  Every CTA of the second pass adds its matrix's partial sums itself,
-// in a fixed order, which saves the launch that would do only that.  All three are bound by
+// when the set fits (126 MB).  The last CTA of a matrix to leave its partial sum adds them all, in a
+// fixed order, which saves the launch that would do only that.  (Added by every CTA of the second pass, they
+// were work that grows with the square of the matrix's tiles: 4 GB from L2 for 16384 x 16384.)  All three are bound by
 // memory traffic: 2 x 2 + 2 bytes an element in, 2 + 2 out for bf16.  Measured with 113 M bf16 values (12 of
 // 1536 x 6144): sums 39 us (5.8 TB/s), X0 89 us (5.1 TB/s).
 #include "muon_view.cuh"
@@ -41,19 +42,6 @@ __device__ __forceinline__ Where find(const ViewParams& p) {
   w.r0 = w.tile / s.tiles_c * TR;
   w.c0 = w.tile % s.tiles_c * TC;
   return w;
-}
-
-// The sum over the CTA, in every thread.
-__device__ __forceinline__ float block_sum(float v) {
-  __shared__ float red[THREADS / 32];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = 0.0f;
-#pragma unroll
-  for (int i = 0; i < THREADS / 32; ++i) t += red[i];
-  return t;
 }
 
 // The 32 stored elements a thread handles.  Where every stored row is 16-byte aligned, four groups of
@@ -141,6 +129,8 @@ __device__ __forceinline__ bool load_tile(const ViewSeg& s, const Where& w, floa
 }
 
 __global__ void __launch_bounds__(THREADS, 6) view_sumsq_kernel(const __grid_constant__ ViewParams p) {
+  __shared__ float red[THREADS / 32];
+  __shared__ bool last;
   const Where w = find(p);
   const ViewSeg& s = p.seg[w.seg];
   float v[4][8];
@@ -150,8 +140,14 @@ __global__ void __launch_bounds__(THREADS, 6) view_sumsq_kernel(const __grid_con
   for (int q = 0; q < 4; ++q)
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss = fmaf(v[q][i], v[q][i], ss);
-  ss = block_sum(ss);
-  if (threadIdx.x == 0) p.partials[s.part_begin + w.e * s.parts + w.tile] = ss;
+  ss = block_sum<THREADS>(ss, red);
+  float* part = p.partials + s.part_begin + w.e * s.parts;
+  if (!last_to_leave(part + w.tile, ss, p.arrivals + s.caller_idx + w.e, s.parts, &last)) return;
+  const float norm = sqrtf(block_sum<THREADS>(sum_parts<THREADS>(part, s.parts), red));
+  if (threadIdx.x == 0) {
+    p.norms[s.caller_idx + w.e] = norm;
+    p.factors[s.caller_idx + w.e] = normaliser(norm, p.eps);
+  }
 }
 
 __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_constant__ ViewParams p) {
@@ -160,15 +156,7 @@ __global__ void __launch_bounds__(THREADS, 4) view_orient_kernel(const __grid_co
   const ViewSeg& s = p.seg[w.seg];
   float v[4][8];
   const bool grouped = load_tile<false>(s, w, v);
-  float mul = 1.0f;
-  if (!p.normalised) {
-    const float* part = p.partials + s.part_begin + w.e * s.parts;
-    float ss = 0.0f;
-    for (int i = threadIdx.x; i < s.parts; i += THREADS) ss += part[i];
-    const float norm = sqrtf(block_sum(ss));
-    if (w.tile == 0 && threadIdx.x == 0) p.norms[s.caller_idx + w.e] = norm;
-    mul = normaliser(norm, p.eps);
-  }
+  const float mul = p.normalised ? 1.0f : p.factors[s.caller_idx + w.e];
   __half* x = static_cast<__half*>(s.x) + static_cast<size_t>(w.e) * s.mp * s.np;
   const bool tr = s.src_tr != 0;
   const bool staged = tr || !grouped;

@@ -281,12 +281,14 @@ struct ViewParams {
   float eps;
   float decay;           // 0: dst is not read
   float* partials;
-  float* norms;
+  float* norms;          // each matrix's last CTA of the sums puts its norm there ...
+  float* factors;        // ... and here what its elements are multiplied by
+  unsigned int* arrivals;  // CTAs of each matrix that have left their part, zero before the call's first launch
 };
 
-// Sums of squares of the sources, one partial per CTA (a 64 x 128 tile).
+// The norms of the sources, from one partial sum of squares per CTA (a 64 x 128 tile).
 cudaError_t launch_view_sumsq(const ViewParams& p, cudaStream_t s);
-// X0 = 2^12 src / (||src|| + eps), oriented and zero-padded; adds the partial sums itself.
+// X0 = 2^12 src / (||src|| + eps), oriented and zero-padded.
 cudaError_t launch_view_orient(const ViewParams& p, cudaStream_t s);
 // dst = decay * dst + coef * X.
 cudaError_t launch_view_write(const ViewParams& p, cudaStream_t s);
@@ -363,8 +365,9 @@ struct StateParams {
   float beta;
   int nesterov;
   float* partials;       // momentum: one sum of squares per CTA
-  float eps;             // momentum, kPassStep
-  float* norms;          // momentum: each matrix's last CTA puts its norm there
+  float eps;             // momentum
+  float* norms;          // momentum: each matrix's last CTA puts its norm there ...
+  float* factors;        // ... and here what kPassStep multiplies u by
   unsigned int* arrivals;  // CTAs of each matrix that have left their part, zero before the call's first launch
 };
 cudaError_t launch_state_quantize(const StateParams& p, StateFormat f, cudaStream_t s);

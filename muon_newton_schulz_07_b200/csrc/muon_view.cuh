@@ -78,6 +78,41 @@ __device__ __forceinline__ void store_eight(void* base, int type, long long at, 
     if (i < have) store_one(base, type, at + i, v[i]);
 }
 
+// The sum over a CTA of THREADS threads, in thread 0; `red` holds a value for each of its warps.
+template <int THREADS>
+__device__ __forceinline__ float block_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  __syncthreads();  // `red` may be in use
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  float t = 0.0f;
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int i = 0; i < THREADS / 32; ++i) t += red[i];
+  }
+  return t;
+}
+// Thread 0 leaves `sum` at `part`; true in the CTA that is the last of `parts` to do so, which may then read them all.
+__device__ __forceinline__ bool last_to_leave(float* part, float sum, unsigned int* arrivals, int parts, bool* last) {
+  if (threadIdx.x == 0) {
+    *part = sum;
+    __threadfence();
+    *last = atomicAdd(arrivals, 1u) == static_cast<unsigned>(parts) - 1u;
+  }
+  __syncthreads();
+  if (!*last) return false;
+  __threadfence();
+  return true;
+}
+// This thread's share of the sum of the parts, in a fixed order.
+template <int THREADS>
+__device__ __forceinline__ float sum_parts(const float* part, int parts) {
+  float t = 0.0f;
+  for (int i = threadIdx.x; i < parts; i += THREADS) t += __ldcg(part + i);
+  return t;
+}
+
 // The factor that makes x into the stored 2^12 x / (norm + eps).  The denominator counts as 2^-100 at
 // least, so that its reciprocal is finite; a NaN stays one.
 __device__ __forceinline__ float normaliser(float norm, float eps) {

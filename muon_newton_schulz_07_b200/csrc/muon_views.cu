@@ -5,7 +5,7 @@
 // A HALF call enqueues, on the caller's stream and without any host sync:
 //   state_momentum_kernel   (steps only, twice) the norms; then m1 written back and the normalised u as
 //                           X0 itself, or in the caller's layout where it has to be transposed or padded
-//   view_sumsq_kernel       (orthogonaliser only) the norms' partial sums
+//   view_sumsq_kernel       (orthogonaliser only) the norms
 //   view_orient_kernel      X0, oriented and padded, fp16
 //   k x { Gram, Poly, Update }   tcgen05 kernels, the last Update writes the result when it can
 //   view_write_kernel       otherwise
@@ -215,6 +215,8 @@ cudaError_t view_pass(muon_ctx* h, const std::vector<Item>& items, ViewPass pass
     p.decay = store ? 0.0f : 1.0f - hp->lr * hp->weight_decay;
     p.partials = h->d_partials;
     p.norms = h->d_norms;
+    p.factors = h->d_scal;
+    p.arrivals = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_arrivals);
     for (; i < items.size() && p.nseg < kViewSegs; ++i) {
       const Item& it = items[i];
       const GroupPlan& gp = group_of(h, it.first);
@@ -518,9 +520,8 @@ cudaError_t half_run(muon_ctx* h, std::vector<Item>& items, const muon_hparams_t
   const int k = hp->ns_steps;
   cudaError_t e = cudaSuccess;
   if (!normalised) {
-    const int counted = counted_iterations(h, k);
-    if (counted > 0) e = clear_counters(h, counted, st);
-    // view_sumsq_kernel writes partial sums, one a tile, where view_orient_kernel looks for them
+    if (!tiled_groups(h).empty()) e = clear_counters(h, counted_iterations(h, k), st);
+    // view_sumsq_kernel's partial sums, one a tile
     int at = 0;
     for (Item& it : items) {
       const GroupPlan& gp = group_of(h, it.first);
@@ -693,6 +694,7 @@ cudaError_t momentum_pass(muon_ctx* h, const std::vector<MomentumIn>& in, StateF
     p.eps = hp->eps;
     p.partials = h->d_partials + part;
     p.norms = h->d_norms;
+    p.factors = h->d_scal;
     p.arrivals = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_arrivals);
     for (; j < in.size() && p.nseg < kStateSegs; ++j) {
       StateSeg g;
