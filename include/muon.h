@@ -90,7 +90,9 @@ typedef enum { MUON_BF16 = 0, MUON_FP32 = 1, MUON_FP16 = 2 } muon_dtype_t;
  *           after five quintic iterations).  X and A are stored times 2^12, so iterations
  *           whose singular values stay below 4 are in range (the usual ones stay below 1.3);
  *           beyond that a matrix comes out not finite.  X is normalised before it
- *           is rounded, so the inputs' size does not matter down to norms of about 1e-4 eps.
+ *           is rounded, so the inputs' size does not matter: from norms of about 1e-4 eps (2^-100
+ *           with eps = 0) up to the largest fp32 entries.  The norm itself is reported as fp32, so
+ *           as infinity beyond 3.4e38.  A matrix that is not finite comes out as NaN.
  *           Matrices of at most 128 rows (or columns) and 4096 columns (rows), or of fewer
  *           rows and as many times more columns, run every iteration on chip.  Takes views, coefficients per iteration and 8-bit
  *           momentum (below). */
@@ -240,7 +242,8 @@ MUON_API muon_status_t muon_state_dequantize(const muon_state_t* S, const muon_v
  *   m1 = beta m + (1-beta) g;  u = (1-beta) g + beta m1 if nesterov, else m1
  * in fp32; u is rounded once into U, m1 once into the state.  G and U are views of the handle's type
  * with col_stride 1 (U may be G).  Only hp->beta and nesterov are used.  The norms
- * of u are read with muon_get_norms.
+ * of u are read with muon_get_norms (where the squares of u leave fp32's range, below 1e-19 or above
+ * 1e19, they are those of U as it is stored).
  */
 MUON_API muon_status_t muon_momentum_state(muon_handle_t handle, const muon_view_t* G, const muon_state_t* S,
                                            const muon_view_t* U, int n, muon_state_format_t format,

@@ -98,9 +98,9 @@ __device__ __forceinline__ void copy_to_cta(uint32_t dst, uint32_t src, uint32_t
                "r"(src), "r"(bytes), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ double ld_cluster_f64(uint32_t addr) {
+  double v;
+  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
   return v;
 }
 // 16 bytes from global to shared memory without passing through registers.
@@ -140,7 +140,7 @@ __device__ __forceinline__ void transpose8(uint4 (&q)[8]) {
 }
 
 template <int TYPE>
-__device__ __forceinline__ void squares8(const uint4& q, float2& ss) {
+__device__ __forceinline__ void add_squares(const uint4& q, float2& ss) {
   float v[8];
   widen8(q, TYPE, v);
 #pragma unroll
@@ -181,6 +181,17 @@ __device__ __noinline__ void write_eight(void* dst, int type, long long at, uint
     for (int i = 0; i < 8; ++i) v[i] *= coef;
   }
   store_eight(dst, type, at, 8, true, v);
+}
+
+// The squares of up to eight neighbouring values whatever their size.
+__device__ __noinline__ double far_squares(const void* src, int type, long long at, int have) {
+  double sum = 0.0;
+#pragma unroll 1
+  for (int c = 0; c < min(have, 8); ++c) {
+    const double v = load_one(src, type, at + c);
+    sum = fma(v, v, sum);
+  }
+  return sum;
 }
 
 // CLUSTER: 1, 2, or 4 for any larger cluster.  FOLDED: matrices are cut into column ranges (their sums in code
@@ -275,9 +286,9 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
   const ViewSeg& sg = p.seg[seg];
   const int u0 = ((tid >> 7) << 3) + (tid & 7);  // first group of this thread, then every 32nd
   const bool wide_src = sg.src_type == kViewF32;
-  float* part = reinterpret_cast<float*>(abuf);  // [4][16] sums of squares; A is not there yet
-  float* total = part + 64;                      // [16]
-  float* factor = total + 16;                    // [16] by matrix of the tile
+  double* part = reinterpret_cast<double*>(abuf);          // [4][16] sums of squares; A is not there yet
+  double* total = part + 64;                               // [16]
+  float* factor = reinterpret_cast<float*>(total + 16);    // [16] by matrix of the tile
   // the storage rows of block (ig, u): address of the first, distance, how many, values in each
   struct Block { long long at; long long ld; int rows, have; };
   auto block_of = [&](int u, bool tr, long long ld, long long bs) {
@@ -353,40 +364,57 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
         if (sg.src_type == kViewBF16) {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            squares8<kViewBF16>(*reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u)), ss2);
+            add_squares<kViewBF16>(*reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u)), ss2);
         } else {
 #pragma unroll
           for (int k = 0; k < 8; ++k)
-            squares8<kViewF16>(*reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u)), ss2);
+            add_squares<kViewF16>(*reinterpret_cast<const uint4*>(xbuf + group_at(ig * 8 + k, u)), ss2);
         }
       }
     }
     ss += ss2.x + ss2.y;
+    double sum = ss;
+    if (e >= 0 && !usual_sum(sum)) {  // squares that fp32 has no values for (see Squares): once more, in fp64
+      sum = 0.0;
+#pragma unroll 1
+      for (int u = u0; u < groups; u += EPI / 16) {
+        const Block b = block_of(u, src_tr, sg.src_ld, sg.src_bs);
+#pragma unroll 1
+        for (int k = 0; k < min(b.rows, 8); ++k)
+          sum += wide_src ? far_squares(sg.src, kViewF32, b.at + k * b.ld, b.have)
+                          : far_squares(xbuf + group_at(ig * 8 + k, u), sg.src_type, 0, b.have);
+      }
+    }
+    if (__any_sync(0xffffffffu, sum != ss)) {
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if ((tid & 7) == 0) part[(tid >> 7) * 16 + ig] = ss;
+      for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    } else {
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      sum = ss;
+    }
+    if ((tid & 7) == 0) part[(tid >> 7) * 16 + ig] = sum;
   }
   sync_all();  // (also: barriers initialised, TMEM allocated)
   const uint32_t tmem = *tmem_slot;
   if (tid < 16) {
-    float t = 0.0f;
+    double t = 0.0;
     for (int c = 0; c < C; ++c)
       for (int h = 0; h < EPI / 128; ++h)
-        t += C > 1 ? ld_cluster_f32(map_to_rank(smem_u32(part + h * 16 + tid), c)) : part[h * 16 + tid];
+        t += C > 1 ? ld_cluster_f64(map_to_rank(smem_u32(part + h * 16 + tid), c)) : part[h * 16 + tid];
     total[tid] = t;
   }
   __syncthreads();
   if (tid < 128 && (tid & ((1 << ls) - 1)) == 0 && tid < used) {  // one thread a matrix
     const int slot = tid >> ls;
-    float t = 0.0f;
+    double t = 0.0;
     for (int i = 0; i < (1 << ls) / 8; ++i) t += total[(tid >> 3) + i];
-    const float norm = sqrtf(t);
-    if (!isfinite(norm)) poison[slot] = 1;
-    factor[slot] = p.normalised ? 1.0f : normaliser(norm, p.eps);
+    if (!isfinite(t)) poison[slot] = 1;
+    factor[slot] = p.normalised ? 1.0f : normaliser(t, p.eps);
     if (first_mat + slot < p.total && rank == 0 && !p.normalised) {
       int s = 0;
       while (s + 1 < p.nseg && p.seg[s + 1].mat_begin <= first_mat + slot) ++s;
-      p.norms[p.seg[s].caller_idx + first_mat + slot - p.seg[s].mat_begin] = norm;
+      p.norms[p.seg[s].caller_idx + first_mat + slot - p.seg[s].mat_begin] = norm_of(t);
     }
   }
   __syncthreads();

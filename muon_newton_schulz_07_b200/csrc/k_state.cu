@@ -504,9 +504,9 @@ __global__ void __launch_bounds__(THREADS, 4) state_dequantize_kernel(const __gr
 template <typename T, int F, bool STOCHASTIC, bool LINEAR, int PASS>
 __global__ void __launch_bounds__(THREADS, !LINEAR || sizeof(T) == 2 ? 3 : 1)
     state_momentum_kernel(const __grid_constant__ StateParams p) {
-  __shared__ float red[THREADS / 32];
-  __shared__ bool last;
   constexpr bool DENSE = F == kStateDense;
+  __shared__ double red[THREADS / 32];
+  __shared__ bool last;
   const Cta c = find(p);
   const StateSeg& s = p.seg[c.seg];
   const bool vec = s.vec != 0;
@@ -517,53 +517,74 @@ __global__ void __launch_bounds__(THREADS, !LINEAR || sizeof(T) == 2 ? 3 : 1)
   Eight<T> raw[PASSES];
   Codes codes[DENSE ? 1 : PASSES];
   Eight<T> dense[DENSE ? PASSES : 1];
-#pragma unroll
-  for (int q = 0; q < PASSES; ++q) {
-    load_values<LINEAR, T>(at.template in<T>(q), vec, at.have(q), raw[q]);
+  auto load = [&](int q, Eight<T>& g, Codes& m8, Eight<T>& m) {
+    load_values<LINEAR, T>(at.template in<T>(q), vec, at.have(q), g);
     if (DENSE)
-      load_values<LINEAR, T>(static_cast<const T*>(s.codes) + at.code_at(q), vec, at.have(q), dense[DENSE ? q : 0]);
+      load_values<LINEAR, T>(static_cast<const T*>(s.codes) + at.code_at(q), vec, at.have(q), m);
     else
-      load_codes<LINEAR>(at, q, vec, codes[DENSE ? 0 : q]);
-  }
-  float ss = 0.0f;
+      load_codes<LINEAR>(at, q, vec, m8);
+  };
+  // m1 and u of eight values
+  auto moments = [&](const Eight<T>& g8, const Codes& m8, const Eight<T>& m, float (&m1)[8], float (&u)[8]) {
+    g8.widen(u);
+    if (DENSE)
+      m.widen(m1);
+    else
+      read_codes<DENSE ? kStateInt8 : F>(m8, m1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      u[i] = __fmul_rn(u[i], rest);
+      m1[i] = __fadd_rn(__fmul_rn(m1[i], beta), u[i]);
+      if (p.nesterov)
+        u[i] = __fadd_rn(u[i], __fmul_rn(m1[i], beta));
+      else
+        u[i] = m1[i];
+    }
+  };
+#pragma unroll
+  for (int q = 0; q < PASSES; ++q) load(q, raw[q], codes[DENSE ? 0 : q], dense[DENSE ? q : 0]);
+  float sum = 0.0f;
   float m[PASSES][8];
 #pragma unroll
   for (int q = 0; q < PASSES; ++q) {
-    float g[8];
-    raw[q].widen(g);
-    if (DENSE)
-      dense[DENSE ? q : 0].widen(m[q]);
-    else
-      read_codes<DENSE ? kStateInt8 : F>(codes[DENSE ? 0 : q], m[q]);
-    float part = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      g[i] = __fmul_rn(g[i], rest);
-      m[q][i] = __fadd_rn(__fmul_rn(m[q][i], beta), g[i]);
-      if (p.nesterov)
-        g[i] = __fadd_rn(g[i], __fmul_rn(m[q][i], beta));
-      else
-        g[i] = m[q][i];
-      part = fmaf(g[i], g[i], part);
-    }
-    ss += at.have(q) > 0 ? part : 0.0f;
+    float u[8];
+    moments(raw[q], codes[DENSE ? 0 : q], dense[DENSE ? q : 0], m[q], u);
+    if (PASS != kPassStep) sum += at.have(q) > 0 ? squares8(u) : 0.0f;
     if (PASS == kPassStep) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] *= mul;
-      store_values<LINEAR, __half>(at.template out<__half>(q), vec, at.have(q), g);
+      for (int i = 0; i < 8; ++i) u[i] *= mul;
+      store_values<LINEAR, __half>(at.template out<__half>(q), vec, at.have(q), u);
     }
-    if (PASS == kPassMomentum) store_values<LINEAR, T>(at.template out<T>(q), vec, at.have(q), g);
+    if (PASS == kPassMomentum) store_values<LINEAR, T>(at.template out<T>(q), vec, at.have(q), u);
     if (DENSE && PASS != kPassNorm) store_values<LINEAR, T>(static_cast<T*>(s.codes) + at.code_at(q), vec, at.have(q), m[q]);
   }
   if (!DENSE && PASS != kPassNorm) write_units<DENSE ? kStateInt8 : F, STOCHASTIC, LINEAR>(at, vec, key, m);
   if (PASS == kPassStep) return;
-  ss = block_sum<THREADS>(ss, red);
+  // The values of an unusual sum come from memory again: u as this thread stored it (held until now, in registers or in
+  // shared memory, u costs every call 2 to 10 %), or what it is made of where nothing has been written.
+  const Squares squares(sum, at.have(0) > 0, [&](auto add) {
+#pragma unroll
+    for (int q = 0; q < PASSES; ++q) {
+      Eight<T> g8, m8;
+      Codes c8;
+      float m1[8], u[8];
+      if (PASS == kPassMomentum) {
+        load_values<LINEAR, T>(at.template out<T>(q), vec, at.have(q), g8);
+        g8.widen(u);
+      } else {
+        load(q, g8, c8, m8);
+        moments(g8, c8, m8, m1, u);
+      }
+      add(u);  // (values beyond the matrix: zeros)
+    }
+  });
+  const double ss = block_sum<THREADS>(squares, red);
   if (!last_to_leave(p.partials + blockIdx.x, ss, p.arrivals + s.caller_idx + c.e, s.unit_ctas, &last)) return;
-  const float* part = p.partials + s.cta_begin + c.e * s.unit_ctas;
-  const float norm = sqrtf(block_sum<THREADS>(sum_parts<THREADS>(part, s.unit_ctas), red));
+  const double* part = p.partials + s.cta_begin + c.e * s.unit_ctas;
+  const double total = block_sum<THREADS>(sum_parts<THREADS>(part, s.unit_ctas), red);
   if (threadIdx.x == 0) {
-    p.norms[s.caller_idx + c.e] = norm;
-    p.factors[s.caller_idx + c.e] = normaliser(norm, p.eps);
+    p.norms[s.caller_idx + c.e] = norm_of(total);
+    p.factors[s.caller_idx + c.e] = normaliser(total, p.eps);
   }
 }
 
@@ -597,15 +618,17 @@ cudaError_t dequantize(const StateParams& p, StateFormat f, cudaStream_t s) {
 }
 template <typename T, int F, bool LINEAR>
 cudaError_t momentum(const StateParams& p, StatePass pass, cudaStream_t s) {
-  constexpr bool ROUNDS = F != kStateDense;
+  constexpr bool CODES = F != kStateDense;  // (a dense momentum has steps only)
   if (pass == kPassNorm)
     state_momentum_kernel<T, F, false, LINEAR, kPassNorm><<<p.total, THREADS, 0, s>>>(p);
-  else if (ROUNDS && p.stochastic && pass == kPassStep)
-    state_momentum_kernel<T, F, ROUNDS, LINEAR, kPassStep><<<p.total, THREADS, 0, s>>>(p);
-  else if (ROUNDS && p.stochastic)
-    state_momentum_kernel<T, F, ROUNDS, LINEAR, kPassMomentum><<<p.total, THREADS, 0, s>>>(p);
-  else if (pass == kPassStep)
+  else if (pass == kPassStep && !(CODES && p.stochastic))
     state_momentum_kernel<T, F, false, LINEAR, kPassStep><<<p.total, THREADS, 0, s>>>(p);
+  else if constexpr (!CODES)
+    return cudaErrorInvalidValue;
+  else if (pass == kPassStep)
+    state_momentum_kernel<T, F, true, LINEAR, kPassStep><<<p.total, THREADS, 0, s>>>(p);
+  else if (p.stochastic)
+    state_momentum_kernel<T, F, true, LINEAR, kPassMomentum><<<p.total, THREADS, 0, s>>>(p);
   else
     state_momentum_kernel<T, F, false, LINEAR, kPassMomentum><<<p.total, THREADS, 0, s>>>(p);
   return cudaGetLastError();

@@ -1,7 +1,7 @@
 // The ends of the fp16 Newton-Schulz iteration (MUON_MODE_HALF) for matrices that stay where and
 // how the caller holds them: slices of fused weights, stacks, transposed storage, bf16, fp16 or fp32.
 //
-//   view_sumsq_kernel   ||x||_F from partial sums of squares, fp32, one per 64 x 128 tile
+//   view_sumsq_kernel   ||x||_F from partial sums of squares, one per 64 x 128 tile
 //   view_orient_kernel  X0 = 2^12 x / (||x||_F + eps), oriented to min x max, zero-padded, fp16
 //   view_write_kernel   dst = decay dst + coef X_k, oriented back
 //
@@ -129,24 +129,26 @@ __device__ __forceinline__ bool load_tile(const ViewSeg& s, const Where& w, floa
 }
 
 __global__ void __launch_bounds__(THREADS, 6) view_sumsq_kernel(const __grid_constant__ ViewParams p) {
-  __shared__ float red[THREADS / 32];
+  __shared__ double red[THREADS / 32];
   __shared__ bool last;
   const Where w = find(p);
   const ViewSeg& s = p.seg[w.seg];
   float v[4][8];
   load_tile<false>(s, w, v);
-  float ss = 0.0f;
+  float sum32 = 0.0f;
 #pragma unroll
-  for (int q = 0; q < 4; ++q)
+  for (int q = 0; q < 4; ++q) sum32 += squares8(v[q]);
+  const Squares squares(sum32, true, [&](auto add) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = fmaf(v[q][i], v[q][i], ss);
-  ss = block_sum<THREADS>(ss, red);
-  float* part = p.partials + s.part_begin + w.e * s.parts;
+    for (int q = 0; q < 4; ++q) add(v[q]);
+  });
+  const double ss = block_sum<THREADS>(squares, red);
+  double* part = p.partials + s.part_begin + w.e * s.parts;
   if (!last_to_leave(part + w.tile, ss, p.arrivals + s.caller_idx + w.e, s.parts, &last)) return;
-  const float norm = sqrtf(block_sum<THREADS>(sum_parts<THREADS>(part, s.parts), red));
+  const double sum = block_sum<THREADS>(sum_parts<THREADS>(part, s.parts), red);
   if (threadIdx.x == 0) {
-    p.norms[s.caller_idx + w.e] = norm;
-    p.factors[s.caller_idx + w.e] = normaliser(norm, p.eps);
+    p.norms[s.caller_idx + w.e] = norm_of(sum);
+    p.factors[s.caller_idx + w.e] = normaliser(sum, p.eps);
   }
 }
 

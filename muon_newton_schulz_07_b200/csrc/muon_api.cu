@@ -103,7 +103,8 @@ void make_plan(const muon_shape_t* shapes, int n, muon_mode_t mode, Plan* P) {
     P->ew_ntiles[i] = (gp.mp / kEwTileR) * (gp.np / kEwTileC);
   }
   // One partial sum per (CTA, warp) of the momentum/norm kernel, one CTA per tile; launches in
-  // sequence reuse the buffer, so the whole set bounds it.
+  // sequence reuse the buffer, so the whole set bounds it.  (The view and state kernels' sums, in 64 bits, one per
+  // 64 x 128 tile of the unpadded matrix or per 64 blocks of up to 128 columns of a row, take a quarter of it at most.)
   size_t parts = 0;
   for (int i = 0; i < n; ++i) parts += static_cast<size_t>(P->ew_ntiles[i]) * (kEwThreads / 32);
   size_t off = 0;

@@ -280,7 +280,7 @@ struct ViewParams {
   int normalised;        // the source is 2^12 X already: no norm is taken
   float eps;
   float decay;           // 0: dst is not read
-  float* partials;
+  double* partials;
   float* norms;          // each matrix's last CTA of the sums puts its norm there ...
   float* factors;        // ... and here what its elements are multiplied by
   unsigned int* arrivals;  // CTAs of each matrix that have left their part, zero before the call's first launch
@@ -364,7 +364,7 @@ struct StateParams {
   unsigned int seed;
   float beta;
   int nesterov;
-  float* partials;       // momentum: one sum of squares per CTA
+  double* partials;      // momentum: one sum of squares per CTA
   float eps;             // momentum
   float* norms;          // momentum: each matrix's last CTA puts its norm there ...
   float* factors;        // ... and here what kPassStep multiplies u by

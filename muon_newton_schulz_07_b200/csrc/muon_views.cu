@@ -213,7 +213,7 @@ cudaError_t view_pass(muon_ctx* h, const std::vector<Item>& items, ViewPass pass
     p.normalised = normalised ? 1 : 0;
     p.eps = hp->eps;
     p.decay = store ? 0.0f : 1.0f - hp->lr * hp->weight_decay;
-    p.partials = h->d_partials;
+    p.partials = reinterpret_cast<double*>(h->d_partials);
     p.norms = h->d_norms;
     p.factors = h->d_scal;
     p.arrivals = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_arrivals);
@@ -692,7 +692,7 @@ cudaError_t momentum_pass(muon_ctx* h, const std::vector<MomentumIn>& in, StateF
     p.beta = hp->beta;
     p.nesterov = hp->nesterov ? 1 : 0;
     p.eps = hp->eps;
-    p.partials = h->d_partials + part;
+    p.partials = reinterpret_cast<double*>(h->d_partials) + part;
     p.norms = h->d_norms;
     p.factors = h->d_scal;
     p.arrivals = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_arrivals);
