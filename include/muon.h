@@ -213,7 +213,8 @@ MUON_API muon_status_t muon_set_coefficients(muon_handle_t handle, const float* 
  * Rounding is to nearest even where `seed` is NULL.  Otherwise it is stochastic: up with the
  * probability of the remainder (to 16 bits), by a generator that depends on *seed (read
  * before returning), the matrix's place in the call and the value's place in the matrix only.
- * Give every step another seed.  A captured call repeats the seed it was captured with.
+ * Give every step another seed, and each of a step's calls (on several handles or ranks) one of its own: equal
+ * places of two calls with one seed share their bits.  A captured call repeats the seed it was captured with.
  */
 #define MUON_STATE_BLOCK 128
 typedef enum { MUON_STATE_INT8 = 0, MUON_STATE_E4M3 = 1 } muon_state_format_t;

@@ -60,7 +60,9 @@ class ShardedMuon:
 
     local_step(W_owned, G_owned, M_owned) performs the Muon step on the owned matrices in place
     (by default a MuonStep over their shapes); W, G are the full lists on every rank and M holds
-    only the owned momentum buffers, in owned order.
+    only the owned momentum buffers, in owned order: tensors, or a QuantizedState of the owned shapes for a
+    local_step with mode="half".  Every rank is given the same `seed` then, and rounds with one of its own
+    (random bits depend on the seed and the places in a rank's call, which start at 0 on each).
 
     Data layout of the exchanges: one flat buffer of world segments, segment q holding the
     matrices rank q owns, back to back in owned order, padded to the longest segment.  Matrix i
@@ -113,10 +115,16 @@ class ShardedMuon:
         return self._views(flat, range(len(self.shapes)))
 
     # ------------------------------------------------------------ steps
+    def _own_seed(self, hp):
+        if hp.get("seed") is None or self.rank == 0:
+            return hp
+        # an odd multiple near 2^32 over the golden ratio: the ranks' sequences of consecutive seeds lie far apart
+        return {**hp, "seed": (int(hp["seed"]) + self.rank * 0x9E3779B1) & 0xFFFFFFFF}
+
     def step(self, W, G, M_owned, **hp):
         """A step from gradients already averaged over the ranks (G: the full list on every rank)."""
         if self.owned:
-            self.local_step([W[i] for i in self.owned], [G[i] for i in self.owned], M_owned, **hp)
+            self.local_step([W[i] for i in self.owned], [G[i] for i in self.owned], M_owned, **self._own_seed(hp))
         self.exchange(W)
 
     def step_local_grads(self, W, G_local, M_owned, **hp):
@@ -124,7 +132,7 @@ class ShardedMuon:
         reduce-scatter that hands each rank only the matrices it owns, step those, all-gather W."""
         G_owned = self.reduce_gradients(G_local)
         if self.owned:
-            self.local_step([W[i] for i in self.owned], G_owned, M_owned, **hp)
+            self.local_step([W[i] for i in self.owned], G_owned, M_owned, **self._own_seed(hp))
         self.exchange(W)
 
     def reduce_gradients(self, G_local):
