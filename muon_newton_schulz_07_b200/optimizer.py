@@ -188,13 +188,15 @@ class MuonStep:
 
     def _coefficients(self, abc, ns_steps):
         """(abc for the hyper-parameters, iterations); a list of triples, one per iteration, goes to the handle."""
-        if len(abc) == 3 and not hasattr(abc[0], "__len__"):
+        # (a tensor of no dimensions has a len)
+        scalars = (True,) * 3 if abc is QUINTIC else [not hasattr(t, "__len__") or getattr(t, "ndim", 1) == 0 for t in abc]
+        if len(abc) == 3 and all(scalars):
             if self.mode == "half":
                 B.muon_set_coefficients(self.handle, ())
             return abc, 5 if ns_steps is None else ns_steps
         if self.mode != "half":
-            raise ValueError("coefficients per iteration need mode='half'")
-        if any(len(t) != 3 for t in abc) or (ns_steps is not None and ns_steps != len(abc)):
+            raise ValueError("abc must be one (a, b, c): coefficients per iteration need mode='half'")
+        if any(one or len(t) != 3 for one, t in zip(scalars, abc)) or (ns_steps is not None and ns_steps != len(abc)):
             raise ValueError("abc must be one (a, b, c), or one for each of the ns_steps iterations")
         B.muon_set_coefficients(self.handle, abc)
         return QUINTIC, len(abc)
