@@ -279,6 +279,8 @@ class MuonStep:
         hp = B.make_hparams(0.0, beta, 0.0, 0.0, QUINTIC, nesterov, 0)
         g = _views(G, self._entries, self.device, "G", self.dtype, by_rows=True)
         u = _views(U, self._entries, self.device, "U", self.dtype, by_rows=True)
+        if norms is not None:
+            self._check_norms(norms)
         B.muon_momentum_state(self.handle, g, self._momentum_state(state), u, len(self.shapes), state._fmt, hp, seed, s)
         return self.norms(norms, stream=stream)
 
@@ -300,14 +302,21 @@ class MuonStep:
         hp = B.make_hparams(0.0, 0.0, 0.0, eps, abc, False, ns_steps)
         B.muon_orthogonalize(self.handle, self._check(X, "X"), self._check(O, "O"), hp, s.cuda_stream)
 
+    def _check_norms(self, out):
+        if out.dtype is not torch.float32 or out.numel() < self._n or not out.is_contiguous() or \
+                out.device not in (self.device, torch.device("cpu")):
+            raise ValueError(f"norms: tensor {tuple(out.shape)} {out.dtype} {out.device} is not {self._n} contiguous "
+                             f"torch.float32 on {self.device} or the host")
+
     def norms(self, out=None, stream=None) -> torch.Tensor:
         """||U_i||_F of the last step, fp32, enqueued as one copy into `out` (device or pinned host)."""
-        if out is None:
-            if stream is None:
+        if out is not None:
+            self._check_norms(out)
+        elif stream is None:
+            out = torch.empty(self._n, dtype=torch.float32, device=self.device)
+        else:  # memory of the stream that writes it
+            with torch.cuda.stream(stream):
                 out = torch.empty(self._n, dtype=torch.float32, device=self.device)
-            else:  # memory of the stream that writes it
-                with torch.cuda.stream(stream):
-                    out = torch.empty(self._n, dtype=torch.float32, device=self.device)
         B.muon_get_norms(self.handle, out.data_ptr(), _stream(self.device, stream))
         return out
 

@@ -58,3 +58,31 @@ def test_coefficients_that_are_neither(coefficients):
         with pytest.raises(ValueError):
             step("half")._coefficients(abc, None)
     assert coefficients == []
+
+
+def test_a_buffer_that_does_not_hold_the_norms_is_refused(monkeypatch):
+    """The copy goes to its address: one that is too short, of another type or strided would be written past its end."""
+    sent = []
+    monkeypatch.setattr(B, "muon_get_norms", lambda handle, dst, stream: sent.append(dst))
+    monkeypatch.setattr("muon_newton_schulz_07_b200.optimizer._stream", lambda device, stream: 0)
+    op = step("half", n=3)
+    for bad in (torch.zeros(2), torch.zeros(3, dtype=torch.float64), torch.zeros(3, dtype=torch.bfloat16),
+                torch.zeros(6)[::2], torch.zeros(3, device="meta")):
+        with pytest.raises(ValueError):
+            op.norms(bad)
+    assert sent == []
+    for good in (torch.zeros(3), torch.zeros(1, 3), torch.zeros(7)[1:]):
+        assert op.norms(good) is good
+    assert len(sent) == 3
+
+
+def test_momentum_refuses_before_it_updates_anything(monkeypatch):
+    """A call that is refused leaves the state as it was: the buffer for the norms is looked at first."""
+    monkeypatch.setattr(B, "muon_momentum_state", lambda *a: pytest.fail("called"))
+    monkeypatch.setattr("muon_newton_schulz_07_b200.optimizer._stream", lambda device, stream: 0)
+    op = step("half", n=1)
+    op._entries, op.shapes, op.dtype = [(1, 4, 4, (4, 4))], [(4, 4)], torch.float32
+    state = type("S", (), {"shapes": [(4, 4)], "device": op.device, "_fmt": 0, "_states": lambda self: b""})()
+    g = [torch.zeros(4, 4)]
+    with pytest.raises(ValueError):
+        op.momentum(g, state, [torch.zeros(4, 4)], norms=torch.zeros(0))
