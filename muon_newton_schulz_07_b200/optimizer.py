@@ -161,9 +161,18 @@ class MuonStep:
             # the block may be one that this stream's earlier work still uses; muon_create fills it on another stream
             torch.cuda.current_stream(self.device).synchronize()
             self.handle = B.muon_create(matrices, self._dt, self._mode, self._ws_ptr, nbytes)
+        self._streams = {_stream(self.device, None)}
         self.n_groups, _ = B.muon_get_plan(self.handle, 5)
         if schedule != "auto":
             self.set_schedule(schedule)
+
+    def _on(self, stream):
+        """The stream of a call.  The workspace's block stays allocated until that stream's work on it is done."""
+        raw = _stream(self.device, stream)
+        if raw not in self._streams:
+            self._streams.add(raw)
+            self._ws.record_stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        return raw
 
     def set_schedule(self, schedule: str) -> None:
         """'auto', 'staged' (one launch per Newton-Schulz stage), 'fused' (every iteration in one launch)
@@ -225,12 +234,11 @@ class MuonStep:
             g = _views(G, self._entries, self.device, "G", self.dtype, by_rows=True)
             abc, ns_steps = self._coefficients(abc, ns_steps)
             hp = B.make_hparams(lr, beta, weight_decay, eps, abc, nesterov, ns_steps)
-            B.muon_step_state(self.handle, w, g, states, len(self.shapes), M._fmt, hp, seed, _stream(self.device, stream))
+            B.muon_step_state(self.handle, w, g, states, len(self.shapes), M._fmt, hp, seed, self._on(stream))
             return
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
         abc, ns_steps = self._coefficients(abc, ns_steps)
         hp = B.make_hparams(lr, beta, weight_decay, eps, abc, nesterov, ns_steps)
-        B.muon_step(self.handle, self._check(W, "W"), self._check(G, "G"), self._check(M, "M"), hp, s.cuda_stream)
+        B.muon_step(self.handle, self._check(W, "W"), self._check(G, "G"), self._check(M, "M"), hp, self._on(stream))
 
     def step_from_host(self, W, G_host, M, stream=None, **hp):
         """A step whose gradients are in pinned host memory.
@@ -275,7 +283,7 @@ class MuonStep:
     def momentum(self, G, state, U, beta=0.95, nesterov=True, seed=None, norms=None, stream=None) -> torch.Tensor:
         """The momentum of a step on a QuantizedState, by itself: the state updated in place, the blended direction
         in U, its Frobenius norms (one a matrix, fp32) returned.  G and U: the handle's dtype, stored by rows; U may be G."""
-        s = _stream(self.device, stream)
+        s = self._on(stream)
         hp = B.make_hparams(0.0, beta, 0.0, 0.0, QUINTIC, nesterov, 0)
         g = _views(G, self._entries, self.device, "G", self.dtype, by_rows=True)
         u = _views(U, self._entries, self.device, "U", self.dtype, by_rows=True)
@@ -295,12 +303,11 @@ class MuonStep:
             o = _views(O, self._entries, self.device, "O")
             abc, ns_steps = self._coefficients(abc, ns_steps)
             hp = B.make_hparams(0.0, 0.0, 0.0, eps, abc, False, ns_steps)
-            B.muon_orthogonalize_views(self.handle, x, o, len(self.shapes), hp, _stream(self.device, stream))
+            B.muon_orthogonalize_views(self.handle, x, o, len(self.shapes), hp, self._on(stream))
             return
-        s = stream if stream is not None else torch.cuda.current_stream(self.device)
         abc, ns_steps = self._coefficients(abc, ns_steps)
         hp = B.make_hparams(0.0, 0.0, 0.0, eps, abc, False, ns_steps)
-        B.muon_orthogonalize(self.handle, self._check(X, "X"), self._check(O, "O"), hp, s.cuda_stream)
+        B.muon_orthogonalize(self.handle, self._check(X, "X"), self._check(O, "O"), hp, self._on(stream))
 
     def _check_norms(self, out):
         if out.dtype is not torch.float32 or out.numel() < self._n or not out.is_contiguous() or \
@@ -317,7 +324,7 @@ class MuonStep:
         else:  # memory of the stream that writes it
             with torch.cuda.stream(stream):
                 out = torch.empty(self._n, dtype=torch.float32, device=self.device)
-        B.muon_get_norms(self.handle, out.data_ptr(), _stream(self.device, stream))
+        B.muon_get_norms(self.handle, out.data_ptr(), self._on(stream))
         return out
 
     def status(self, stream=None) -> int:

@@ -154,3 +154,42 @@ def test_a_captured_call_clears_its_counters():
     assert op.status() == B.MUON_OK
     del graph
     op.close()
+
+
+@pytest.mark.parametrize("how", ["stream=", "current", "graph"])
+@pytest.mark.parametrize("call", ["orthogonalize", "step", "momentum"])
+def test_a_workspace_outlives_the_work_on_another_stream(call, how):
+    """A handle that goes while another stream's work is queued: its block is not handed out before that is done."""
+    op = MuonStep(SHAPES, mode="half")
+    W, G, U, state = tensors()
+
+    def run(**kw):
+        if call == "orthogonalize":
+            op.orthogonalize(G, U, **kw)
+        elif call == "step":
+            op(W, G, state, **kw)
+        else:
+            op.momentum(G, state, U, **kw)
+
+    run()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    if how == "graph":
+        with torch.cuda.graph(graph, stream=side):
+            run()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(200_000_000)
+        if how == "graph":
+            graph.replay()
+        elif how == "current":
+            run()
+    if how == "stream=":
+        run(stream=side)
+    at, nbytes = op._ws.data_ptr(), op._ws.numel()
+    op.close()
+    op._ws = None
+    taken = [torch.empty(nbytes, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    assert not side.query() and at not in [t.data_ptr() for t in taken]
+    torch.cuda.synchronize()
+    del graph

@@ -16,7 +16,7 @@ TRIPLE = (3.0, -3.25, 1.125)
 
 def step(mode, n=3):
     op = object.__new__(MuonStep)
-    op.mode, op.handle, op.device, op._n = mode, None, torch.device("cpu"), n
+    op.mode, op.handle, op.device, op._n, op._streams = mode, None, torch.device("cpu"), n, {0}
     return op
 
 
