@@ -49,9 +49,10 @@ __host__ __device__ __forceinline__ uint32_t mixed(uint32_t h) {
   return h;
 }
 __device__ __forceinline__ uint32_t matrix_key(uint32_t seed, uint32_t matrix) { return mixed(mixed(seed) ^ matrix); }
-// The 32 bits that places 2 pair and 2 pair + 1 of a matrix share, the lower half first: mixed(...) of
+// Places 2 pair and 2 pair + 1 of a matrix share the 32 bits mixed(pair_counter(key, pair)), the lower half first.  (Of
+// a matrix of more than 2^33 values, those 2^33 apart have the same bits.)
 __device__ __forceinline__ uint32_t pair_counter(uint32_t key, unsigned long long pair) {
-  return static_cast<uint32_t>(pair) + key + static_cast<uint32_t>(pair >> 32) * 0x9E3779B1u;
+  return static_cast<uint32_t>(pair) + key;
 }
 
 // ---------------------------------------------------------------- codes
@@ -389,7 +390,6 @@ __device__ __forceinline__ void write_units(const Sites<LINEAR>& at, bool vec, u
     if (STOCHASTIC) {
       const unsigned long long first = at.place_of(q);
       if (LINEAR) {  // eight neighbours from an even place: four pairs
-        // (A CTA's pairs are 4096 neighbours from a multiple of that: their upper 32 bits are the same.)
         const uint32_t counter = pair_counter(key, (at.place_of(0) + lane * 8) / 2) + q * (Sites<LINEAR>::kPass / 2);
 #pragma unroll
         for (int i = 0; i < 4; ++i) r[i] = mixed(counter + i);
