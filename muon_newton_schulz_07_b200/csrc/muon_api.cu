@@ -19,6 +19,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <map>
+#include <memory>
 #include <new>
 #include <vector>
 
@@ -809,10 +810,12 @@ muon_status_t muon_workspace_size(const muon_shape_t* shapes, int n, muon_dtype_
                                   size_t* bytes) {
   if (bytes == nullptr || !shapes_ok(shapes, n)) return MUON_ERR_INVALID_ARG;
   if (!type_ok(dtype, mode)) return MUON_ERR_INVALID_ARG;
-  Plan P;
-  make_plan(shapes, n, mode, &P);
-  *bytes = P.total;
-  return MUON_OK;
+  return no_throw([&]() -> muon_status_t {
+    Plan P;
+    make_plan(shapes, n, mode, &P);
+    *bytes = P.total;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_create(muon_handle_t* handle, const muon_shape_t* shapes, int n, muon_dtype_t dtype,
@@ -821,72 +824,68 @@ muon_status_t muon_create(muon_handle_t* handle, const muon_shape_t* shapes, int
   *handle = nullptr;
   if (!shapes_ok(shapes, n)) return MUON_ERR_INVALID_ARG;
   if (!type_ok(dtype, mode)) return MUON_ERR_INVALID_ARG;
-  int dev = -1, ndev = 0;
-  if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev < 1 || cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return MUON_ERR_NO_DEVICE;
-  }
-  int major = 0, sms = 0;
-  cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (major != 10) return MUON_ERR_UNSUPPORTED;
-  muon_ctx* h = new (std::nothrow) muon_ctx();
-  if (h == nullptr) return MUON_ERR_INVALID_ARG;
-  h->device = dev;
-  h->num_sms = sms;
-  h->dtype = dtype;
-  h->mode = mode;
-  h->n = n;
-  h->shapes.assign(shapes, shapes + n);
-  make_plan(shapes, n, mode, &h->plan);
-  h->fuse_shapes_ok = n <= kTcMaxFused;
-  for (const GroupPlan& gp : h->plan.groups)
-    if (gp.m % 32 != 0 || gp.n % 32 != 0) h->fuse_shapes_ok = false;
-  if (workspace == nullptr || ws_bytes < h->plan.total || (reinterpret_cast<uintptr_t>(workspace) & 1023u) != 0) {
-    delete h;
-    return MUON_ERR_WORKSPACE;
-  }
-  h->ws = static_cast<char*>(workspace);
-  h->ws_bytes = ws_bytes;
-  h->d_status = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_status);
-  h->d_scal = reinterpret_cast<float*>(h->ws + h->plan.off_scal);
-  h->d_partials = reinterpret_cast<float*>(h->ws + h->plan.off_partials);
-  h->d_norms = reinterpret_cast<float*>(h->ws + h->plan.off_norms);
-  // cudaMemset of device memory does not wait for the fill, and a stream created non-blocking does not wait for
-  // the default stream: without the second call the handle's first work there could meet the fill.
-  if (cudaMemset(workspace, 0, h->plan.total) != cudaSuccess || cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
-    cudaGetLastError();
-    delete h;
-    return MUON_ERR_CUDA;
-  }
-  if (mode != MUON_MODE_FP32_REF) {
-    for (GroupPlan& gp : h->plan.groups) {
-      if (gp.skinny) continue;
-      bool ok = true;
-      for (int b = 0; b < 2; ++b)
-        ok = ok && encode_rows(&gp.tm_x[b], h->ws + gp.off_x[b], gp.np, gp.mp, gp.cnt) &&
-             encode_chunks(&gp.tt_x[b], h->ws + gp.off_x[b], gp.np, gp.mp, gp.cnt) &&
-             encode_store(&gp.ts_x[b], h->ws + gp.off_x[b], gp.np, gp.mp, gp.cnt);
-      ok = ok && encode_rows(&gp.tm_a, h->ws + gp.off_a, gp.mp, gp.mp, gp.cnt) &&
-           encode_chunks(&gp.tt_a, h->ws + gp.off_a, gp.mp, gp.mp, gp.cnt) &&
-           encode_store(&gp.ts_a, h->ws + gp.off_a, gp.mp, gp.mp, gp.cnt) &&
-           encode_rows(&gp.tm_b, h->ws + gp.off_b, gp.mp, gp.mp, gp.cnt) &&
-           encode_chunks(&gp.tt_b, h->ws + gp.off_b, gp.mp, gp.mp, gp.cnt) &&
-           encode_store(&gp.ts_b, h->ws + gp.off_b, gp.mp, gp.mp, gp.cnt);
-      if (!ok) {
-        delete h;
-        return MUON_ERR_CUDA;
+  return no_throw([&]() -> muon_status_t {
+    int dev = -1, ndev = 0;
+    if (cudaGetDeviceCount(&ndev) != cudaSuccess || ndev < 1 || cudaGetDevice(&dev) != cudaSuccess) {
+      cudaGetLastError();
+      return MUON_ERR_NO_DEVICE;
+    }
+    int major = 0, sms = 0;
+    cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev);
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (major != 10) return MUON_ERR_UNSUPPORTED;
+    std::unique_ptr<muon_ctx> own(new muon_ctx());
+    muon_ctx* h = own.get();
+    h->device = dev;
+    h->num_sms = sms;
+    h->dtype = dtype;
+    h->mode = mode;
+    h->n = n;
+    h->shapes.assign(shapes, shapes + n);
+    make_plan(shapes, n, mode, &h->plan);
+    h->fuse_shapes_ok = n <= kTcMaxFused;
+    for (const GroupPlan& gp : h->plan.groups)
+      if (gp.m % 32 != 0 || gp.n % 32 != 0) h->fuse_shapes_ok = false;
+    if (workspace == nullptr || ws_bytes < h->plan.total || (reinterpret_cast<uintptr_t>(workspace) & 1023u) != 0)
+      return MUON_ERR_WORKSPACE;
+    h->ws = static_cast<char*>(workspace);
+    h->ws_bytes = ws_bytes;
+    h->d_status = reinterpret_cast<unsigned int*>(h->ws + h->plan.off_status);
+    h->d_scal = reinterpret_cast<float*>(h->ws + h->plan.off_scal);
+    h->d_partials = reinterpret_cast<float*>(h->ws + h->plan.off_partials);
+    h->d_norms = reinterpret_cast<float*>(h->ws + h->plan.off_norms);
+    // cudaMemset of device memory does not wait for the fill, and a stream created non-blocking does not wait for
+    // the default stream: without the second call the handle's first work there could meet the fill.
+    if (cudaMemset(workspace, 0, h->plan.total) != cudaSuccess || cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) {
+      cudaGetLastError();
+      return MUON_ERR_CUDA;
+    }
+    if (mode != MUON_MODE_FP32_REF) {
+      for (GroupPlan& gp : h->plan.groups) {
+        if (gp.skinny) continue;
+        bool ok = true;
+        for (int b = 0; b < 2; ++b)
+          ok = ok && encode_rows(&gp.tm_x[b], h->ws + gp.off_x[b], gp.np, gp.mp, gp.cnt) &&
+               encode_chunks(&gp.tt_x[b], h->ws + gp.off_x[b], gp.np, gp.mp, gp.cnt) &&
+               encode_store(&gp.ts_x[b], h->ws + gp.off_x[b], gp.np, gp.mp, gp.cnt);
+        ok = ok && encode_rows(&gp.tm_a, h->ws + gp.off_a, gp.mp, gp.mp, gp.cnt) &&
+             encode_chunks(&gp.tt_a, h->ws + gp.off_a, gp.mp, gp.mp, gp.cnt) &&
+             encode_store(&gp.ts_a, h->ws + gp.off_a, gp.mp, gp.mp, gp.cnt) &&
+             encode_rows(&gp.tm_b, h->ws + gp.off_b, gp.mp, gp.mp, gp.cnt) &&
+             encode_chunks(&gp.tt_b, h->ws + gp.off_b, gp.mp, gp.mp, gp.cnt) &&
+             encode_store(&gp.ts_b, h->ws + gp.off_b, gp.mp, gp.mp, gp.cnt);
+        if (!ok) return MUON_ERR_CUDA;
       }
     }
-  }
-  if (std::getenv("MUON_DEBUG") != nullptr) {
-    std::fprintf(stderr, "[muon] %d matrices, %zu groups, workspace %zu bytes\n", n, h->plan.groups.size(),
-                 h->plan.total);
-    for (const GroupPlan& gp : h->plan.groups)
-      std::fprintf(stderr, "[muon]   group %dx%d (padded %dx%d) x %d\n", gp.m, gp.n, gp.mp, gp.np, gp.cnt);
-  }
-  *handle = h;
-  return MUON_OK;
+    if (std::getenv("MUON_DEBUG") != nullptr) {
+      std::fprintf(stderr, "[muon] %d matrices, %zu groups, workspace %zu bytes\n", n, h->plan.groups.size(),
+                   h->plan.total);
+      for (const GroupPlan& gp : h->plan.groups)
+        std::fprintf(stderr, "[muon]   group %dx%d (padded %dx%d) x %d\n", gp.m, gp.n, gp.mp, gp.np, gp.cnt);
+    }
+    *handle = own.release();
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_step(muon_handle_t h, void* const* W, const void* const* G, void* const* M,
@@ -895,15 +894,17 @@ muon_status_t muon_step(muon_handle_t h, void* const* W, const void* const* G, v
   for (int i = 0; i < h->n; ++i)
     if (W[i] == nullptr || G[i] == nullptr || M[i] == nullptr) return MUON_ERR_INVALID_ARG;
   if (h->mode == MUON_MODE_HALF) return half_step(h, W, G, M, hp, stream);
-  DeviceGuard guard(h->device);
-  NvtxRange range("muon_step");
-  int launches = 0;
-  bool fused = false;
-  cudaError_t e = enqueue_front(h, G, M, hp, stream, &launches);
-  if (e == cudaSuccess) e = enqueue_ns(h, hp, stream, &launches, W, false, &fused);
-  if (e == cudaSuccess && !fused) e = enqueue_back(h, W, hp, false, stream, &launches);
-  trace_call_end(h);
-  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return no_throw([&]() -> muon_status_t {
+    DeviceGuard guard(h->device);
+    NvtxRange range("muon_step");
+    int launches = 0;
+    bool fused = false;
+    cudaError_t e = enqueue_front(h, G, M, hp, stream, &launches);
+    if (e == cudaSuccess) e = enqueue_ns(h, hp, stream, &launches, W, false, &fused);
+    if (e == cudaSuccess && !fused) e = enqueue_back(h, W, hp, false, stream, &launches);
+    trace_call_end(h);
+    return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  });
 }
 
 muon_status_t muon_orthogonalize(muon_handle_t h, const void* const* X, void* const* O, const muon_hparams_t* hp,
@@ -912,20 +913,22 @@ muon_status_t muon_orthogonalize(muon_handle_t h, const void* const* X, void* co
   for (int i = 0; i < h->n; ++i)
     if (X[i] == nullptr || O[i] == nullptr) return MUON_ERR_INVALID_ARG;
   if (h->mode == MUON_MODE_HALF) return half_orthogonalize(h, X, O, hp, stream);
-  DeviceGuard guard(h->device);
-  NvtxRange range("muon_orthogonalize");
-  muon_hparams_t q = *hp;
-  q.beta = 0.0f;
-  q.nesterov = 0;
-  q.lr = 0.0f;
-  q.weight_decay = 0.0f;
-  int launches = 0;
-  cudaError_t e = enqueue_front(h, X, nullptr, &q, stream, &launches);
-  bool fused = false;
-  if (e == cudaSuccess) e = enqueue_ns(h, &q, stream, &launches, O, true, &fused);
-  if (e == cudaSuccess && !fused) e = enqueue_back(h, O, &q, true, stream, &launches);
-  trace_call_end(h);
-  return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  return no_throw([&]() -> muon_status_t {
+    DeviceGuard guard(h->device);
+    NvtxRange range("muon_orthogonalize");
+    muon_hparams_t q = *hp;
+    q.beta = 0.0f;
+    q.nesterov = 0;
+    q.lr = 0.0f;
+    q.weight_decay = 0.0f;
+    int launches = 0;
+    cudaError_t e = enqueue_front(h, X, nullptr, &q, stream, &launches);
+    bool fused = false;
+    if (e == cudaSuccess) e = enqueue_ns(h, &q, stream, &launches, O, true, &fused);
+    if (e == cudaSuccess && !fused) e = enqueue_back(h, O, &q, true, stream, &launches);
+    trace_call_end(h);
+    return e == cudaSuccess ? MUON_OK : MUON_ERR_CUDA;
+  });
 }
 
 muon_status_t muon_get_norms(muon_handle_t h, float* dst, cudaStream_t stream) {
@@ -968,33 +971,28 @@ muon_status_t muon_check_plan(const muon_shape_t* shapes, int n, int ns_steps, i
   if (problems == nullptr || !shapes_ok(shapes, n) || ns_steps < 0 || ns_steps > 64 || num_sms < 2 ||
       num_sms > 4096)
     return MUON_ERR_INVALID_ARG;
-  Plan P;
-  make_plan(shapes, n, MUON_MODE_FAST, &P);
-  std::vector<muon_shape_t> sh(shapes, shapes + n);
-  long long bad = 0;
-  EwParams* ew = new (std::nothrow) EwParams;
-  NsParams* ns = new (std::nothrow) NsParams;
-  if (ew == nullptr || ns == nullptr) {
-    delete ew;
-    delete ns;
-    return MUON_ERR_INVALID_ARG;
-  }
-  for (int b = 0; b < n; b += kEwMatsPerLaunch) {
-    front_tables(P, sh, b, std::min(kEwMatsPerLaunch, n - b), ew);
-    bad += check_front_tables(*ew);
-  }
-  if (ns_steps >= 1 && P.groups.size() <= static_cast<size_t>(kTcMaxGroups)) {
-    for (int fw = 0; fw < 2; ++fw) {
-      for (int pairs : {0, num_sms / 2, 0x7fffffff}) {  // never narrow, as the rule has it, always
-        fused_tables(all_groups(P), n, ns_steps, fw != 0, true, pairs, ns);
-        bad += check_fused_tiles(*ns);
+  return no_throw([&]() -> muon_status_t {
+    Plan P;
+    make_plan(shapes, n, MUON_MODE_FAST, &P);
+    std::vector<muon_shape_t> sh(shapes, shapes + n);
+    long long bad = 0;
+    std::unique_ptr<EwParams> ew(new EwParams);
+    std::unique_ptr<NsParams> ns(new NsParams);
+    for (int b = 0; b < n; b += kEwMatsPerLaunch) {
+      front_tables(P, sh, b, std::min(kEwMatsPerLaunch, n - b), ew.get());
+      bad += check_front_tables(*ew);
+    }
+    if (ns_steps >= 1 && P.groups.size() <= static_cast<size_t>(kTcMaxGroups)) {
+      for (int fw = 0; fw < 2; ++fw) {
+        for (int pairs : {0, num_sms / 2, 0x7fffffff}) {  // never narrow, as the rule has it, always
+          fused_tables(all_groups(P), n, ns_steps, fw != 0, true, pairs, ns.get());
+          bad += check_fused_tiles(*ns);
+        }
       }
     }
-  }
-  delete ew;
-  delete ns;
-  *problems = bad;
-  return MUON_OK;
+    *problems = bad;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_set_schedule(muon_handle_t h, int schedule) {
@@ -1032,12 +1030,14 @@ muon_status_t muon_get_group_buffers(muon_handle_t h, int group, int* mp, int* n
 
 muon_status_t muon_profile_begin(muon_handle_t h, int max_steps) {
   if (h == nullptr || max_steps < 1 || max_steps > 100000) return MUON_ERR_INVALID_ARG;
-  DeviceGuard guard(h->device);
-  for (auto& pe : h->prof_events) cudaEventDestroy(pe.second);
-  h->prof_events.clear();
-  h->prof_events.reserve(static_cast<size_t>(max_steps) * 64);
-  h->prof_steps_left = max_steps;
-  return MUON_OK;
+  return no_throw([&]() -> muon_status_t {
+    DeviceGuard guard(h->device);
+    for (auto& pe : h->prof_events) cudaEventDestroy(pe.second);
+    h->prof_events.clear();
+    h->prof_events.reserve(static_cast<size_t>(max_steps) * 64);
+    h->prof_steps_left = max_steps;
+    return MUON_OK;
+  });
 }
 
 muon_status_t muon_profile_end(muon_handle_t h, double* ms, int* launches, int n_kinds) {

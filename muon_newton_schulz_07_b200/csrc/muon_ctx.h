@@ -2,6 +2,7 @@
 // (muon_api.cu: the dense step and the orthogonaliser; muon_views.cu: views and 8-bit state).
 #pragma once
 
+#include <exception>
 #include <utility>
 #include <vector>
 
@@ -44,6 +45,16 @@ struct Plan {
   size_t off_status, off_arrivals, off_rounds, off_deps, off_scal, off_norms, off_partials;
   size_t total;
 };
+
+// No exception leaves a C entry point: host tables that cannot be allocated are an error code.
+template <typename F>
+muon_status_t no_throw(F f) noexcept {
+  try {
+    return f();
+  } catch (const std::exception&) {
+    return MUON_ERR_INVALID_ARG;
+  }
+}
 
 class DeviceGuard {
  public:

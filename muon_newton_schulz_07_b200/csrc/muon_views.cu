@@ -13,7 +13,6 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
-#include <exception>
 #include <utility>
 #include <vector>
 
@@ -128,16 +127,6 @@ bool states_distinct(const muon_state_t* S, int n) {
     at.push_back(S[j].scales);
   }
   return distinct(at);
-}
-
-// No exception leaves a C entry point: host tables that cannot be allocated are an error code.
-template <typename F>
-muon_status_t no_throw(F f) noexcept {
-  try {
-    return f();
-  } catch (const std::exception&) {
-    return MUON_ERR_INVALID_ARG;
-  }
 }
 
 // (a, b, c) of iteration t.
