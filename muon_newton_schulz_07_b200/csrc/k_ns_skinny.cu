@@ -2,8 +2,8 @@
 //
 //   X0 = X / (||X||_F + eps);   k times: A = X X^T, B' = a I + b A + c A A, X <- B' X
 //
-// for min(rows, cols) = m <= 128 and n = max(rows, cols) up to 8 x 512, in fp16 operands
-// (MUON_MODE_HALF).  The general path pads m to 256, which costs a 64-row head 4 (update) to 16
+// for min(rows, cols) = m <= 128 and n = max(rows, cols) up to 8 x 512 (of at most 64 rows, cut into column ranges, up to
+// that for each: 16 x 4096 for 8 rows), in fp16 operands (MUON_MODE_HALF).  The general path pads m to 256, which costs a 64-row head 4 (update) to 16
 // (Gram) times its work, and takes 3 k launches that each read X or A from L2.  Here a cluster of
 // C CTAs owns a tile of 128 rows x n: CTA c keeps columns [c w, c w + w) of X in shared memory
 // for the whole iteration, and the matrix is read from and written to global memory in the
@@ -37,7 +37,7 @@
 // the row by the exact diagonal entry over the rounded one, which takes a third off the error
 // of the result (64 x 768, five quintic iterations: 1.9e-3 -> 1.2e-3).
 //
-// Measured, five iterations: 12 of 64 x 768 43 us, 288 of 1536 x 128 (clusters of two) 320 us.  An iteration of 128 x 768
+// Measured, five iterations: 12 of 64 x 768 44 us, 288 of 1536 x 128 (clusters of two) 322 us.  An iteration of 128 x 768
 // a CTA takes 13 k cycles, 7 k of them the six blocks (their MMAs at the rate of the tensor core), 5 k the chain from A to the first
 // block, 1 k the last block's Gram product; a cluster of two adds 6 k for the exchange of A.  Loading, converting
 // and storing a tile is 30 to 45 k once, which one CTA an SM has nothing to hide behind.
@@ -173,14 +173,14 @@ __device__ __noinline__ void write_eight(void* dst, int type, long long at, uint
   widen8(q, kViewF16, v);
   if (decay != 0.0f) {
     float w[8];
-    load_eight(dst, type, at, 8, true, w);
+    load_eight(dst, type, at, 8, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = fmaf(decay, w[i], coef * v[i]);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] *= coef;
   }
-  store_eight(dst, type, at, 8, true, v);
+  store_eight(dst, type, at, 8, v);
 }
 
 // The squares of up to eight neighbouring values whatever their size.
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(THREADS, 1) ns_skinny_kernel(const __grid_cons
         for (int k = 0; k < 8; ++k) {  // (fp32: the second read, an L2 hit)
           float v[8];
           if (full) {
-            load_eight(sg.src, kViewF32, b.at + k * b.ld, 8, true, v);
+            load_eight(sg.src, kViewF32, b.at + k * b.ld, 8, v);
           } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i)

@@ -22,7 +22,8 @@
 // consecutive in memory, so a CTA of 64 units streams up to 8192 contiguous values whatever the
 // row length, and a thread has the loads of all four of its units in flight before it computes.
 // Three or four CTAs an SM (the launch bounds): the loads of one hide behind the arithmetic of the others (30 of
-// 1001 x 1001 bf16, value by value: momentum on int8 113 us unbounded, 89 with three).
+// 1001 x 1001 bf16, value by value: momentum on int8 113 us unbounded, 89 with three).  Momentum on fp32 rows of whole
+// blocks is not held to a number (one CTA fewer fits; 24 of 1536 x 1536 as int8, to nearest, 116 us a call with the norms).
 // Rows that are not whole blocks back to back interleave the 16 lanes instead, four values each where
 // rows are multiples of 4 and aligned so, else one, which keeps the accesses of a half-warp contiguous.
 #include <cuda_fp8.h>
@@ -325,7 +326,7 @@ template <bool LINEAR, typename T>
 __device__ __forceinline__ void store_values(T* base, bool vec, int have, const float (&x)[8]) {
   const int lane = unit_lane();
   if (LINEAR) {
-    if (lane * 8 < have) store_eight(base, TypeOf<T>::id, lane * 8, 8, true, x);
+    if (lane * 8 < have) store_eight(base, TypeOf<T>::id, lane * 8, 8, x);
   } else if (vec) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

@@ -106,7 +106,7 @@ __device__ __forceinline__ bool load_tile(const ViewSeg& s, const Where& w, floa
       int r, c;
       place(tr, q, r, c);
       const int have = r0 + r < rows ? cols - (c0 + c) : 0;
-      load_eight(base, type, w.e * bs + (r0 + r) * ld + c0 + c, have, true, v[q]);
+      load_eight(base, type, w.e * bs + (r0 + r) * ld + c0 + c, have, v[q]);
     }
     return true;
   }
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(THREADS, 3) view_write_kernel(const __grid_con
       const float y = s.coef * (tr ? stage[c + i][r] : o[q][i]);
       o[q][i] = p.decay != 0.0f ? fmaf(p.decay, d[q][i], y) : y;
     }
-    store_eight(s.dst, s.dst_type, at + r * s.dst_ld + c, have, true, o[q]);
+    store_eight(s.dst, s.dst_type, at + r * s.dst_ld + c, have, o[q]);
   }
 }
 

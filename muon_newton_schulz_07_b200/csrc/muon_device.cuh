@@ -196,19 +196,8 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, bf16 inputs, fp32 accumulator, one CTA.
-__device__ __forceinline__ void tc_mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// The same issued by the lanes whose `lead` is nonzero (one of them), from code that the whole warp
-// runs: the operands then stay in uniform registers, where a divergent branch moves each there first.
+// D[tmem] (+)= A[smem] * B[smem]^T, 16-bit inputs, fp32 accumulator, one CTA; issued by the lane whose `lead` is
+// nonzero, from code that the whole warp runs: the operands then stay in uniform registers, where a divergent branch moves each there first.
 __device__ __forceinline__ void tc_mma_lead(uint32_t lead, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                             uint32_t idesc, uint32_t accumulate) {
   asm volatile(
@@ -231,12 +220,7 @@ __device__ __forceinline__ void tc_mma_tmem_a_lead(uint32_t lead, uint32_t d_tme
       : "memory");
 }
 
-// Arrive on `bar` once every tcgen05.mma issued so far by this thread has completed.
-__device__ __forceinline__ void tc_commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
-               : "memory");
-}
-
+// Arrive on `bar` once every tcgen05.mma issued so far by the lane whose `lead` is nonzero has completed.
 __device__ __forceinline__ void tc_commit_lead(uint32_t lead, uint32_t bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"

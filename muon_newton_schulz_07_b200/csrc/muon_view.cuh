@@ -32,10 +32,9 @@ __device__ __forceinline__ void store_one(void* base, int type, long long at, fl
 }
 
 // Elements at .. at + 7 of a stored row; the first `have` exist, the others come back as 0.
-// `vec`: the row starts 16-byte aligned and `at` is a multiple of 8 elements into it.
-__device__ __forceinline__ void load_eight(const void* base, int type, long long at, int have, bool vec,
-                                           float (&v)[8]) {
-  if (vec && have >= 8) {
+// The row starts 16-byte aligned and `at` is a multiple of 8 elements into it.
+__device__ __forceinline__ void load_eight(const void* base, int type, long long at, int have, float (&v)[8]) {
+  if (have >= 8) {
     if (type == kViewF32) {
       const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + at);
       const float4 a = p[0], b = p[1];
@@ -50,9 +49,8 @@ __device__ __forceinline__ void load_eight(const void* base, int type, long long
   for (int i = 0; i < 8; ++i) v[i] = i < have ? load_one(base, type, at + i) : 0.0f;
 }
 
-__device__ __forceinline__ void store_eight(void* base, int type, long long at, int have, bool vec,
-                                            const float (&v)[8]) {
-  if (vec && have >= 8) {
+__device__ __forceinline__ void store_eight(void* base, int type, long long at, int have, const float (&v)[8]) {
+  if (have >= 8) {
     if (type == kViewF32) {
       float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + at);
       p[0] = make_float4(v[0], v[1], v[2], v[3]);
