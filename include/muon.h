@@ -85,17 +85,19 @@ typedef enum { MUON_BF16 = 0, MUON_FP32 = 1, MUON_FP16 = 2 } muon_dtype_t;
  *           rounded A).
  * FP32_REF: fp32 operands and intermediates, products accumulated in fp64 on
  *           the CUDA cores (no TF32): a slow, accurate mode for checking.
- * HALF:     the products of FAST with fp16 operands: three more significant bits at the
- *           same tensor-core rate, an error about eight times smaller (2e-3 instead of 1-2e-2
- *           after five quintic iterations).  X and A are stored times 2^12, so iterations
- *           whose singular values stay below 4 are in range (the usual ones stay below 1.3);
- *           beyond that a matrix comes out not finite.  X is normalised before it
- *           is rounded, so the inputs' size does not matter: from norms of about 1e-4 eps (2^-100
- *           with eps = 0) up to the largest fp32 entries.  The norm itself is reported as fp32, so
- *           as infinity beyond 3.4e38.  A matrix that is not finite comes out as NaN.
- *           Matrices of at most 128 rows (or columns) and 4096 columns (rows), or of fewer
- *           rows and as many times more columns, run every iteration on chip.  Takes views, coefficients per iteration and 8-bit
- *           momentum (below). */
+ * HALF:     the products of FAST with fp16 operands: three more significant bits in the
+ *           same tensor-core instructions, an error about eight times smaller (2e-3 instead of
+ *           1-2e-2 after five quintic iterations).  A call takes about as long as in FAST
+ *           (measured from 6 % less to 9 % more; 23 % more in a step on 64 of 256 x 256).
+ *           X and A are stored times 2^12, so iterations whose singular values stay below 4
+ *           are in range (the usual ones stay below 1.3); beyond that a matrix comes out not
+ *           finite.  X is normalised before it is rounded, so the inputs' size does not
+ *           matter: from norms of about 1e-4 eps (2^-100 with eps = 0) up to the largest fp32
+ *           entries.  The norm itself is reported as fp32, so as infinity beyond 3.4e38.  A
+ *           matrix that is not finite comes out as NaN.  Matrices of at most 128 rows (or
+ *           columns) and 4096 columns (rows), or of fewer rows and as many times more
+ *           columns, run every iteration on chip.  Takes views, coefficients per iteration
+ *           and 8-bit momentum (below). */
 typedef enum { MUON_MODE_FAST = 0, MUON_MODE_FP32_REF = 1, MUON_MODE_HALF = 2 } muon_mode_t;
 
 typedef struct { int64_t rows, cols; } muon_shape_t;
@@ -124,7 +126,7 @@ typedef struct muon_ctx* muon_handle_t;
  *   shapes: host array of n shapes, rows >= 1, cols >= 1.
  *   bytes:  host out-pointer.
  * Returns MUON_ERR_INVALID_ARG on a null pointer, n < 1 or n > MUON_MAX_MATRICES,
- * or a non-positive dimension.
+ * or a dimension below 1 or above 2^20.
  */
 MUON_API muon_status_t muon_workspace_size(const muon_shape_t* shapes, int n, muon_dtype_t dtype,
                                   muon_mode_t mode, size_t* bytes);

@@ -38,7 +38,7 @@
 // drains the first half, hands that slot back, then drains the second, while the MMA issuer
 // already accumulates the next tile's first k slices into the freed half.
 //
-// Measured with fp16 operands, five iterations: 48 of 768 x 768 485 us, bound by what the tiles read from L2 (6.3 GB,
+// Measured with fp16 operands, five iterations, the launch alone: 48 of 768 x 768 485 us, bound by what the tiles read from L2 (6.3 GB,
 // 13 TB/s; tensor pipe 56 %); 7 of 331 x 1003 132 us, bound by the 15 stages' latency: of about 15 k cycles, the
 // first loads take 1.7, the products 3 to 10, the epilogue 5, its stores and the counter 2.5.
 #include <cuda_bf16.h>

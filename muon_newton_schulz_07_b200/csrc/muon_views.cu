@@ -292,8 +292,11 @@ long long update_tiles(const std::vector<const GroupPlan*>& groups) {
 // Whether the k iterations of the groups that go through the workspace run as one launch.  AUTO
 // does so up to eight Update tiles a pair: there the launch boundaries (a ramp, a tail and a gap each)
 // cost more than the single launch's waits on completion counters.  Measured, five iterations,
-// one launch against one per stage: 4 x 768 x 768 207 and 242 us, 16 x 1024 x 1024 400 and 560, 48 x 768 x 768
-// 566 and 622; but 24 x 1536 x 1536 (12 tiles a pair) 1880 and 1750, 12 x 1536 x 6144 (23) 3090 and 2740.
+// one launch against one per stage, the orthogonaliser on bf16 by itself: 4 x 768 x 768 (half a tile a pair) 158 and 218 us,
+// 16 x 1024 x 1024 (3.5) 381 and 497, 48 x 768 x 768 (5.8) 540 and 653, 16 x 1536 x 1536 (7.8) 1231 and 1326.  Beyond,
+// where the power cap sets the pace, it depends on the set and on what else the call does: 40 x 1024 x 1024 (8.6) 1069
+// and 1192, 24 x 1536 x 1536 (12) 1903 and 1895, 12 x 1536 x 6144 (23) 2820 and 2928; steps on an 8-bit state, 24 x 1536 x 1536
+// 1998 and 1956, 12 x 1536 x 6144 3194 and 3092.
 bool single_launch(const muon_ctx* h, int k) {
   if (k < 1 || !half_fused_possible(h)) return false;
   if (h->schedule != MUON_SCHEDULE_AUTO) return h->schedule != MUON_SCHEDULE_STAGED;
@@ -386,8 +389,8 @@ cudaError_t enqueue_tiles(muon_ctx* h, const std::vector<Item>& items, const muo
         prm.status = h->d_status;
         prm.timeout_ns = kTimeoutNs;
         const bool last = kind == kUpdate && t + 1 == k && fuse;
-        // 256 x 512 Update tiles under the same rule as the bf16 path: every padded width allows
-        // them and, where the launch writes the result, the k loops are long (mean m >= 2048)
+        // 256 x 512 Update tiles where there are enough of them (wide_pays) and, as on the bf16 path, every
+        // padded width allows them and, where the launch writes the result, the k loops are long (mean m >= 2048)
         bool wide = kind == kUpdate && wide_pays(h, groups);
         double wsum = 0.0, wm = 0.0;
         for (int gi = 0; gi < ng; ++gi) {

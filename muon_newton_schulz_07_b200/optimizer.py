@@ -131,8 +131,8 @@ class MuonStep:
     """A Muon step for one fixed list of matrix shapes, bound to one CUDA device.
 
     A shape is (rows, cols), or (count, rows, cols) for a stack of equal matrices, each stepped by itself (experts,
-    attention heads).  mode: "fast" (bf16 operands), "half" (fp16 operands: an eighth of the rounding error at the
-    same rate; takes strided views, coefficients per iteration and 8-bit momentum) or "fp32_ref" (slow, exact).
+    attention heads).  mode: "fast" (bf16 operands), "half" (fp16 operands: an eighth of the rounding error in about
+    the same time; takes strided views, coefficients per iteration and 8-bit momentum) or "fp32_ref" (slow, exact).
     """
 
     SCHEDULES = {"auto": B.MUON_SCHEDULE_AUTO, "staged": B.MUON_SCHEDULE_STAGED, "fused": B.MUON_SCHEDULE_FUSED,
