@@ -8,10 +8,11 @@
 // The norm must be known before the first rounding to fp16: gradients reach far below fp16's
 // range, normalised matrices do not.  So the source is read twice; the second read finds it in L2
 // when the set fits (126 MB).  The last CTA of a matrix to leave its partial sum adds them all, in a
-// fixed order, which saves the launch that would do only that.  (Added by every CTA of the second pass, they
-// were work that grows with the square of the matrix's tiles: 4 GB from L2 for 16384 x 16384.)  All three are bound by
+// fixed order.  That costs each CTA a fence and an atomic, but no launch: one that only added them took 3 us more of
+// small calls (7 of 331 x 1003: 162 us for 158) and 18 less of the largest.  Added by every CTA of the second pass,
+// they were work that grows with the square of the matrix's tiles (4 GB from L2 for 16384 x 16384).  All three are bound by
 // memory traffic: 2 x 2 + 2 bytes an element in, 2 + 2 out for bf16.  Measured with 113 M bf16 values (12 of
-// 1536 x 6144): sums 39 us (5.8 TB/s), X0 89 us (5.1 TB/s).
+// 1536 x 6144): norms 58 us (3.9 TB/s), X0 71 us (6.4 TB/s).
 #include "muon_view.cuh"
 
 namespace muon {
