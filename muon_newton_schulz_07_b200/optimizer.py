@@ -253,12 +253,19 @@ class MuonStep:
             self._gbuf = [[torch.empty(sh, dtype=self.dtype, device=self.device) for sh in self.shapes]
                           for _ in range(2)]
             self._copy_stream = torch.cuda.Stream(self.device)
+            self._copy_stream.wait_stream(torch.cuda.current_stream(self.device))  # earlier work on these blocks
             self._buf_free = [None, None]
+            self._buf_streams = {torch.cuda.current_stream(self.device).cuda_stream}
             self._nfed = 0
         if len(G_host) != len(self.shapes):
             raise ValueError(f"G_host: expected {len(self.shapes)} tensors, got {len(G_host)}")
         b = self._nfed & 1
         cs = self._copy_stream
+        for used in (cs, s):  # the blocks stay allocated until these streams' work on them is done
+            if used.cuda_stream not in self._buf_streams:
+                self._buf_streams.add(used.cuda_stream)
+                for d in self._gbuf[0] + self._gbuf[1]:
+                    d.record_stream(used)
         with torch.cuda.stream(cs):
             if self._buf_free[b] is not None:
                 cs.wait_event(self._buf_free[b])
